@@ -469,6 +469,146 @@ int awq_search(const void* W, int w_dtype, const void* X, int x_dtype, int64_t N
                const double* alphas, int64_t n_alpha, uint8_t* codes, float* scales, uint8_t* zeros, float* smooth,
                double* err, int64_t* best, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit paged key/value cache.
+ *
+ * With the weights at 4 bits the cache is what a decode step on a batch of
+ * long sequences reads most of ("Quantization from Scratch", "What it buys at
+ * decode": the cache-adjusted speedup); here it is stored by the same
+ * asymmetric rule as the weights, in groups of channels of one token and head.
+ *
+ * For every token, kv head and group of g channels of its key (and value) x:
+ *   lo = min(0, min x), hi = max(0, max x)
+ *   s  = binary16(fl32((hi - lo) / 15)), saturating at 65504, 1 if that is 0
+ *   z  = clamp(round(fl32(-lo / s)), 0, 15)
+ *   c  = clamp(round(fl32(x / s)) + z, 0, 15),  value (c - z) s
+ * in IEEE fp32 with correctly rounded division and round-half-to-even (the
+ * rule of quantize_groupwise_ex with binary16 scales; z is clamped as well, as
+ * rounding the scale can carry it past 15).
+ *
+ * cache : uint8 [pages, kv_heads, page, D + 8 D/g], 16-byte aligned, D the
+ *         head dimension.  `page` tokens of one head are one record of
+ *         page (D + 8 D/g) bytes (4 D/g bytes of scales and zero-points per
+ *         token for keys, as many for values):
+ *           K codes   [page][D/2]: code word w (channels 8w .. 8w+7, in the
+ *                     order of the INT4 format's words) of a token at word
+ *                     (w % 4) (D/32) + w / 4 of its row;
+ *           V codes   [page/4][D/8][4] code words: word w of four consecutive
+ *                     tokens side by side;
+ *           K params  [D/g][page], then V params [D/g][page]: 32-bit words,
+ *                     the binary16 scale in bits 0-15, the zero-point in
+ *                     bits 16-19, the others 0.
+ *         A 16-byte load then gives a lane of the attention kernel whole
+ *         matrix-core operands: four 32-channel steps of one key, or eight
+ *         channels of four values; a token's words belong to it alone, so
+ *         appending one never reads or rewrites another's.
+ * slot  : page id * page + place in the page (int64).
+ * D 64, 128 or 256; page 16, 32, 64, 128 or 256; g 32, 64 or 128, dividing D
+ * (QMM_EUNSUPPORTED otherwise).  16-bit types: QMM_BF16, QMM_F16.  A call on
+ * no tokens (pages, sequences) is QMM_OK and launches nothing.
+ * Memory of the cache that no token was appended to may hold anything.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of one page of all heads: kv_heads * page * (D + 8 D/g); 0 for a
+ * shape that is not supported.  Host-only. */
+size_t kv4_page_bytes(int64_t kv_heads, int64_t head_dim, int64_t page, int group);
+
+/* Quantize the keys and values of T tokens into their slots.
+ * k, v  : [T, kv_heads, D] of dtype, channels consecutive; token and head
+ *         strides in elements, multiples of 8; 16-byte aligned.
+ * slots : int64 [T], device, distinct; a slot outside [0, pages * page) (such
+ *         as -1 for padding) writes nothing. */
+int kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+               int64_t v_head_stride, int dtype, int64_t T, const int64_t* slots, uint8_t* cache, int64_t pages,
+               int64_t kv_heads, int64_t head_dim, int64_t page, int group, void* stream);
+
+/* The values that the codes of T slots stand for: k_out, v_out [T, kv_heads,
+ * D] of out_dtype (QMM_BF16, QMM_F16 or QMM_F32; (c - z) s is exact in fp32,
+ * then one rounding), 16-byte aligned; zeros for a slot outside the cache. */
+int kv4_read(const uint8_t* cache, int64_t pages, int64_t kv_heads, int64_t head_dim, int64_t page, int group,
+             const int64_t* slots, int64_t T, void* k_out, void* v_out, int out_dtype, void* stream);
+
+/* Copy n pages within every layer: page src[i] to page dst[i] (int64, device)
+ * of cache [layers, pages, page_bytes], whatever the bytes are (page_bytes a
+ * multiple of 16).  For forking a sequence (its last page) and for compacting
+ * a cache.  The destinations are distinct and none of them is a source; a
+ * pair with an id outside [0, pages) copies nothing. */
+int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_bytes, const int64_t* src,
+                   const int64_t* dst, int64_t n, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kv4_attention -- causal attention of new queries over the 4-bit cache.
+ *
+ * Sequence b has context[b] tokens in the cache (its new ones appended), its
+ * n_b queries stand at positions context[b] - n_b + i.  Key j is visible to a
+ * query at position p when
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < sinks)
+ * and its page has an id in [0, pages) (pages no query sees may be gone from
+ * the table: -1).  With x_j = scale q.k_j over the visible keys:
+ *   out = sum_j softmax(x)_j v_j,   lse = log sum_j exp(x_j)
+ * and out = 0, lse = -inf where no key is visible (an unused slot of the
+ * batch, context 0).  Query head h reads kv head h / (q_heads / kv_heads).
+ * What the memory of invisible keys holds never reaches the result.
+ *
+ * q       : [T, q_heads, D] of dtype (QMM_BF16 or QMM_F16), channels
+ *           consecutive, strides in elements, multiples of 8; 16-byte aligned.
+ * cu_q    : int32 [seqs + 1], device: sequence b's queries are rows cu_q[b] ..
+ *           cu_q[b + 1] - 1 of q; NULL when every sequence has one (T == seqs).
+ * max_q   : the most queries of a sequence (at least 1).  A hint: it only
+ *           shapes the launch.
+ * context : int32 [seqs], device; at most table_width * page is used.
+ * page_table : int32 [seqs, table_width], rows table_stride elements apart.
+ *           The launch is shaped for contexts up to table_width * page, so a
+ *           table no wider than the longest sequence needs is the faster one.
+ * window  : 0 for none, else the keys a query sees (itself included);
+ *           sinks: the first keys that stay visible.
+ * out     : [T, q_heads, D] of dtype; lse: float32 [T, q_heads] or NULL.
+ * workspace : device memory of at least kv4_attention_workspace_bytes bytes
+ *           with the same arguments (max_context = table_width * page), which
+ *           may be 0; 16-byte aligned, no clearing needed.
+ * Arithmetic: fp32 scores, maxima and sums; see the kernels for the roundings
+ * of matrix-core operands.  Results do not depend on timing (no atomics).
+ * ------------------------------------------------------------------------- */
+size_t kv4_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t q_heads, int64_t kv_heads,
+                                     int64_t head_dim, int64_t max_context, int64_t window, int64_t sinks);
+int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, int64_t T, int64_t q_heads,
+                  const int32_t* cu_q, int64_t seqs, int64_t max_q, const int32_t* context, const int32_t* page_table,
+                  int64_t table_width, int64_t table_stride, const uint8_t* cache, int64_t pages, int64_t kv_heads,
+                  int64_t head_dim, int64_t page, int group, float scale, int64_t window, int64_t sinks, void* out,
+                  float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * qk_norm_rope -- norms of queries and keys for each head, with the rotation
+ * by position in the same pass.  For every head x of D channels, in fp32:
+ *   y = x / sqrt(mean(x^2) + eps) * w      (where a weight w [D] is given)
+ * then the first `rot` channels in pairs (a, b) at the token's position p:
+ *   (a cos - b sin, b cos + a sin),  cos, sin = table[p][i],
+ * pair i being channels (i, i + rot/2), or (2i, 2i + 1) when interleaved; the
+ * others pass.  One rounding, to dtype, at the end.
+ * q [T, q_heads, D], k [T, k_heads, D] of dtype (QMM_BF16 / QMM_F16), channels
+ * consecutive, strides in elements, multiples of 8; k NULL with k_heads 0 for
+ * queries alone.  D a multiple of 8 up to 512, rot a multiple of 16 up to D
+ * (0: norms alone; positions and table may then be NULL).
+ * positions int64 [T]; table float32 [table_rows, rot/2, 2] (rope_table).  A
+ * position outside the table gives NaN in the rotated channels.
+ * q_weight, k_weight [D] of w_dtype (dtype or QMM_F32), either may be NULL.
+ * q_out [T, q_heads, D], k_out [T, k_heads, D] dense; q_out may be q (and
+ * k_out k) where that is dense.  All 16-byte aligned (positions 8).
+ * ------------------------------------------------------------------------- */
+int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
+                 int64_t k_token_stride, int64_t k_head_stride, int64_t k_heads, int dtype, int64_t T,
+                 int64_t head_dim, const int64_t* positions, const float* table, int64_t table_rows, int64_t rot,
+                 int interleaved, const void* q_weight, const void* k_weight, int w_dtype, float eps, void* q_out,
+                 void* k_out, void* stream);
+
+/* table[p][i] = (m cos(p f_i), m sin(p f_i)) for p < rows, i < half: angles and
+ * functions in fp64 (a float angle of a position past 10^5 is off by 10^-2),
+ * rounded once to fp32.  inv_freq: HOST array of half (1 .. 256) frequencies
+ * f_i in radians per position, as scaled for the context; m: the magnitude
+ * some scalings ask for (1 otherwise).  table float32 [rows, half, 2], 16-byte
+ * aligned; rows < 2^31. */
+int rope_table(const double* inv_freq, int64_t half, int64_t rows, double m, float* table, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

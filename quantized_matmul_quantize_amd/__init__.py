@@ -12,6 +12,7 @@ has not been built.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -26,6 +27,8 @@ __all__ = [
     "sq_int8_gemm", "sq_workspace_bytes", "smooth_quant_w8a8_gemm", "smooth_quant_w8a8_gemm_noalloc",
     "fp8_quantize", "fp8_gemm", "fp8_w8a8_gemm",
     "llm_int8_outliers", "llm_int8_workspace_bytes", "llm_int8_gemm", "awq_workspace_bytes", "awq_search", "stream_read",
+    "kv4_cache", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention_workspace_bytes",
+    "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope",
 ]
 
 F32, F16, BF16, I32 = 0, 1, 2, 3
@@ -86,6 +89,16 @@ _SIGS = {
     "qmm_stream_read": ([_P, _SZ, _P, _P], _I),
     "awq_search": ([_P, _I, _P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
     "llm_int8_gemm": ([_P, _I, _P, _P, _I64, _I64, _I64, _F, _I64, _P, _I, _P, _P, _SZ, _P], _I),
+    "kv4_page_bytes": ([_I64, _I64, _I64, _I], _SZ),
+    "kv4_append": ([_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _I64, _I64, _I, _P], _I),
+    "kv4_read": ([_P, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _I, _P], _I),
+    "kv4_copy_pages": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P], _I),
+    "kv4_attention_workspace_bytes": ([_I64] * 9, _SZ),
+    "kv4_attention": ([_P, _I64, _I64, _I, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64,
+                       _I, _F, _I64, _I64, _P, _P, _P, _SZ, _P], _I),
+    "qk_norm_rope": ([_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I64, _I64, _P, _P, _I64, _I64, _I, _P, _P, _I,
+                      _F, _P, _P, _P], _I),
+    "rope_table": ([_P, _I64, _I64, ctypes.c_double, _P, _P], _I),
 }
 
 
@@ -706,3 +719,255 @@ def stream_read(data: torch.Tensor) -> torch.Tensor:
     out = torch.empty(1, dtype=torch.int32, device=dev)
     _call("qmm_stream_read", _ptr(data), nbytes, _ptr(out), _stream(data))
     return out
+
+
+# ---------------------------------------------------------------------------
+# 4-bit paged key/value cache.  cache: uint8 [pages, kv_heads, page, D + 8 D/g]
+# (its shape carries the page and group sizes; include/qmm.h states the layout
+# of a record).
+# ---------------------------------------------------------------------------
+def kv4_page_bytes(kv_heads: int, head_dim: int, page: int = 64, group: int = 64) -> int:
+    """Bytes of one page of all heads; 0 for a shape that is not supported."""
+    return int(lib().kv4_page_bytes(kv_heads, head_dim, page, group))
+
+
+def kv4_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, group: int = 64, layers: Optional[int] = None,
+              device="cuda") -> torch.Tensor:
+    """An uninitialized cache, uint8 [pages, kv_heads, page, D + 8 D/g] (with `layers`: one such for each layer)."""
+    if not kv4_page_bytes(kv_heads, head_dim, page, group):
+        raise ValueError(f"unsupported cache shape: kv_heads={kv_heads} head_dim={head_dim} page={page} group={group}")
+    shape = (pages, kv_heads, page, head_dim + 8 * (head_dim // group))
+    return torch.empty(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _cache_shape(cache, head_dim: int):
+    """(pages, kv_heads, page, group) of a cache for heads of head_dim channels."""
+    _req(cache, "cache", (torch.uint8,), ndim=4)
+    pages, heads, page, token = cache.shape
+    groups, rest = divmod(token - head_dim, 8)
+    if groups <= 0 or rest or head_dim % groups:
+        raise ValueError(f"cache has shape {tuple(cache.shape)}; a token of head_dim {head_dim} takes head_dim + 8 bytes "
+                         "per group of channels")
+    return pages, heads, page, head_dim // groups
+
+
+def _heads(t, name: str, dtypes, shape: Tuple):
+    """Check rows of heads [T, heads, D] (strided views, as slices of a projection's output, are fine); returns the
+    token and head strides."""
+    _req(t, name, dtypes, shape=shape)
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have its channels consecutive, has strides {t.stride()}")
+    ts, hs = t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    if (ts | hs) & 7:
+        raise ValueError(f"{name} must have token and head strides that are multiples of 8, has strides {t.stride()}")
+    return ts, hs
+
+
+def _same_device(dev, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other operands on {dev}")
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor) -> None:
+    """Quantize keys and values [T, kv_heads, D] into the slots (int64 [T], page id * page + place; distinct; -1
+    writes nothing) of the cache."""
+    _req(k, "k", _HALVES, ndim=3)
+    T, heads, D = k.shape
+    pages, _, page, group = _cache_shape(cache, D)
+    _req(cache, "cache", (torch.uint8,), shape=(None, heads, None, None))
+    kt, kh = _heads(k, "k", (k.dtype,), (T, heads, D))
+    vt, vh = _heads(v, "v", (k.dtype,), (T, heads, D))
+    _req(slots, "slots", (torch.int64,), shape=(T,))
+    dev = _place(cache=cache, slots=slots)
+    _same_device(dev, k=k, v=v)
+    _call("kv4_append", _ptr(k), kt, kh, _ptr(v), vt, vh, _dt(k.dtype), T, _ptr(slots), _ptr(cache), pages, heads, D,
+          page, group, _stream(cache))
+
+
+def kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16):
+    """-> (k, v) [T, kv_heads, head_dim] in dtype: the values that the codes of the slots (int64 [T]) stand for, zeros
+    for a slot outside the cache."""
+    if dtype not in _FLOATS:
+        raise ValueError(f"unsupported output dtype {dtype}")
+    pages, heads, page, group = _cache_shape(cache, head_dim)
+    _req(slots, "slots", (torch.int64,), ndim=1)
+    dev = _place(cache=cache, slots=slots)
+    k = torch.empty((slots.shape[0], heads, head_dim), dtype=dtype, device=dev)
+    v = torch.empty_like(k)
+    _call("kv4_read", _ptr(cache), pages, heads, head_dim, page, group, _ptr(slots), slots.shape[0], _ptr(k), _ptr(v),
+          _dt(dtype), _stream(cache))
+    return k, v
+
+
+def kv4_copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Copy page src[i] to page dst[i] (int64 [n]) in every layer of cache [layers, pages, kv_heads, page, token]
+    (or of one layer's [pages, kv_heads, page, token]).  Destinations are distinct and no sources."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() not in (4, 5):
+        raise ValueError("cache must be a torch.Tensor of 4 dimensions, or 5 with layers")
+    _req(cache, "cache", (torch.uint8,))
+    _req(src, "src", (torch.int64,), ndim=1)
+    _req(dst, "dst", (torch.int64,), shape=(src.shape[0],))
+    _place(cache=cache, src=src, dst=dst)
+    layers, pages = (1, cache.shape[0]) if cache.dim() == 4 else cache.shape[:2]
+    _call("kv4_copy_pages", _ptr(cache), layers, pages, math.prod(cache.shape[-3:]), _ptr(src), _ptr(dst),
+          src.shape[0], _stream(cache))
+
+
+def kv4_attention_workspace_bytes(T: int, seqs: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
+                                  max_context: int, window: int = 0, sinks: int = 0) -> int:
+    return int(lib().kv4_attention_workspace_bytes(T, seqs, max_q, q_heads, kv_heads, head_dim, max_context, window,
+                                                   sinks))
+
+
+def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, context: torch.Tensor,
+                  cu_q: Optional[torch.Tensor] = None, max_q: Optional[int] = None, scale: Optional[float] = None,
+                  window: int = 0, sinks: int = 0, return_lse: bool = False, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None):
+    """Causal attention of q [T, q_heads, D] over the cache: sequence b's context[b] (int32 [seqs]) tokens lie in the
+    pages page_table[b] (int32 [seqs, width], -1 for pages that are gone), its queries are its last tokens, one each or
+    rows cu_q[b] .. cu_q[b + 1] - 1 of q (int32 [seqs + 1]; max_q, a hint, the most of a sequence).  window: the keys a
+    query sees (0: all before it), sinks: the first keys that stay visible.  Returns out [T, q_heads, D], with
+    return_lse also the fp32 log-sum-exp [T, q_heads]; a row that sees no key is 0 and -inf."""
+    _req(q, "q", _HALVES, ndim=3)
+    T, q_heads, D = q.shape
+    pages, kv_heads, page, group = _cache_shape(cache, D)
+    if q_heads % kv_heads:
+        raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {kv_heads}")
+    qt, qh = _heads(q, "q", (q.dtype,), (T, q_heads, D))
+    _req(context, "context", (torch.int32,), ndim=1)
+    seqs = context.shape[0]
+    _req(page_table, "page_table", (torch.int32,), shape=(seqs, None))
+    width = page_table.shape[1]
+    if width > 1 and page_table.stride(1) != 1:
+        raise ValueError(f"page_table must have consecutive rows, has strides {page_table.stride()}")
+    stride = page_table.stride(0) if seqs > 1 else width
+    if cu_q is not None:
+        _req(cu_q, "cu_q", (torch.int32,), shape=(seqs + 1,))
+    elif T != seqs:
+        raise ValueError(f"q has {T} rows for {seqs} sequences: without cu_q each has one")
+    if window < 0 or sinks < 0:
+        raise ValueError(f"window and sinks must be >= 0, not {window} and {sinks}")
+    most = 1 if cu_q is None else max(1, T if max_q is None else int(max_q))
+    _out(out, (T, q_heads, D), q.dtype)
+    dev = _place(cache=cache, context=context, cu_q=cu_q, out=out, workspace=workspace)
+    _same_device(dev, q=q, page_table=page_table)
+    need = kv4_attention_workspace_bytes(T, seqs, most, q_heads, kv_heads, D, width * page, window, sinks)
+    if workspace is not None:
+        _req(workspace, "workspace", (torch.uint8,), ndim=1)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes; {need} needed")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    out = _alloc(out, (T, q_heads, D), q.dtype, dev)
+    lse = torch.empty((T, q_heads), dtype=torch.float32, device=dev) if return_lse else None
+    _call("kv4_attention", _ptr(q), qt, qh, _dt(q.dtype), T, q_heads, _ptr(cu_q), seqs, most, _ptr(context),
+          _ptr(page_table), width, stride, _ptr(cache), pages, kv_heads, D, page, group,
+          D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse), _ptr(workspace),
+          workspace.numel() if workspace is not None else 0, _stream(q))
+    return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# Norms of queries and keys with the rotation by position.
+# ---------------------------------------------------------------------------
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                     original: int = 4096, low: float = 1.0, high: Optional[float] = None):
+    """-> (frequencies [rot/2] in radians per position, magnitude) for `rot` rotated channels, base^(-2i/rot), scaled
+    for contexts `factor` times the `original` one:
+      "linear"      every frequency over factor (positions interpolated);
+      "ntk"         the base raised by factor^(rot / (rot - 2)), so the slowest pair is interpolated, the fastest kept;
+      "wavelength"  a pair that turns more than `high` (default 4) times in the original context keeps its frequency,
+                    one that turns less than `low` times is divided by factor, linear in the turns between;
+      "yarn"        the same two ends (high default 32), linear in the pair's index between, and the rotated channels
+                    grow by 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and positive, not {rot}")
+    if base <= 0 or factor <= 0:
+        raise ValueError(f"base and factor must be positive, not {base} and {factor}")
+    half = rot // 2
+    f = [base ** (-i / half) for i in range(half)]
+    if scaling is None:
+        return f, 1.0
+    if scaling == "linear":
+        return [v / factor for v in f], 1.0
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot >= 4")
+        raised = base * factor ** (rot / (rot - 2))
+        return [raised ** (-i / half) for i in range(half)], 1.0
+    if scaling not in ("wavelength", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    high = (4.0 if scaling == "wavelength" else 32.0) if high is None else high
+    if not 0 < low < high:
+        raise ValueError(f"needs 0 < low < high, not {low} and {high}")
+    if scaling == "wavelength":
+        keep = [min(1.0, max(0.0, (original * v / (2 * math.pi) - low) / (high - low))) for v in f]
+        return [k * v + (1.0 - k) * v / factor for k, v in zip(keep, f)], 1.0
+    index = lambda turns: half * math.log(original / (2 * math.pi * turns)) / math.log(base)
+    first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), half - 1)
+    keep = [1.0 - min(1.0, max(0.0, (i - first) / max(last - first, 0.001))) for i in range(half)]
+    return [k * v + (1.0 - k) * v / factor for k, v in zip(keep, f)], \
+        0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def rope_table(rows: int, frequencies: Sequence[float], magnitude: float = 1.0, device="cuda") -> torch.Tensor:
+    """float32 [rows, len(frequencies), 2] of cosines and sines of position * frequency (times magnitude), for
+    positions 0 .. rows - 1; computed in fp64."""
+    half = len(frequencies)
+    if not 1 <= half <= 256 or rows < 1:
+        raise ValueError(f"takes 1 to 256 frequencies and at least one row, not {half} and {rows}")
+    table = torch.empty((rows, half, 2), dtype=torch.float32, device=device)
+    _place(table=table)
+    host = (ctypes.c_double * half)(*[float(v) for v in frequencies])
+    _call("rope_table", ctypes.cast(host, ctypes.c_void_p), half, rows, float(magnitude), _ptr(table), _stream(table))
+    return table
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor] = None,
+                 table: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """Norms of each head of q [T, q_heads, D] and k [T, k_heads, D] (RMS, where its weight [D] is given, in their type
+    or fp32) and the rotation of its first 2 * table.shape[1] channels at positions (int64 [T]) by the table, in halves
+    or interleaved pairs; returns (q_out, k_out).  k may be None, q_out / k_out the inputs themselves (dense ones)."""
+    _req(q, "q", _HALVES, ndim=3)
+    T, q_heads, D = q.shape
+    qt, qh = _heads(q, "q", (q.dtype,), (T, q_heads, D))
+    _out(q_out, (T, q_heads, D), q.dtype, "q_out")
+    k_heads = kt = kh = 0
+    if k is not None:
+        kt, kh = _heads(k, "k", (q.dtype,), (T, None, D))
+        k_heads = k.shape[1]
+        _out(k_out, (T, k_heads, D), q.dtype, "k_out")
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    w_dtype = q.dtype
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _req(w, name, (q.dtype, torch.float32), shape=(D,))
+            w_dtype = w.dtype
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError(f"q_weight has dtype {q_weight.dtype}, k_weight {k_weight.dtype}")
+    if not eps >= 0.0:
+        raise ValueError(f"eps must be >= 0, not {eps}")
+    rows = rot = 0
+    if table is not None:
+        _req(table, "table", (torch.float32,), shape=(None, None, 2))
+        rows, rot = table.shape[0], 2 * table.shape[1]
+        if rot > D:
+            raise ValueError(f"table rotates {rot} channels of heads of {D}")
+        _req(positions, "positions", (torch.int64,), shape=(T,))
+    elif positions is not None:
+        raise ValueError("positions need a table")
+    dev = _place(q_weight=q_weight, k_weight=k_weight, positions=positions, table=table, q_out=q_out, k_out=k_out)
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    _same_device(dev or q.device, q=q, k=k)
+    q_out = _alloc(q_out, (T, q_heads, D), q.dtype, q.device)
+    if k is not None:
+        k_out = _alloc(k_out, (T, k_heads, D), q.dtype, q.device)
+    _call("qk_norm_rope", _ptr(q), qt, qh, q_heads, _ptr(k), kt, kh, k_heads, _dt(q.dtype), T, D, _ptr(positions),
+          _ptr(table), rows, rot, int(interleaved), _ptr(q_weight), _ptr(k_weight), _dt(w_dtype), eps, _ptr(q_out),
+          _ptr(k_out), _stream(q))
+    return q_out, k_out
