@@ -1,0 +1,449 @@
+// kv4_attention_chunk.h -- the attention kernel for chunks of queries (see
+// kv4_attention.h for the products and their operand layouts).
+//
+// With many rows the operations that make operands of codes would outweigh the
+// products, so the wavefronts of a block, each with rows of its own, share
+// them: per round of keys two wavefronts expand keys, two values, subtract the
+// zero-points (c - z is exact in binary16) and leave whole matrix-core operands
+// in LDS for the next round, while all compute on those of the round before:
+// one barrier a round.  What is left per score is one multiplication by the
+// key's scale (with the running base in the same operation where a head is one
+// group), the exponential, a conversion and half a packed product with the
+// value's scale; the sums of the probabilities come from the matrix cores too.
+// q is binary16 here: bf16 queries are first scaled by a power of two per
+// block (their largest to 2^14 .. 2^15), exactly but for what lies 2^38 below
+// the largest.
+#pragma once
+
+#include "kv4_attention.h"
+
+namespace qmm {
+namespace {
+
+template <int D, int GROUP, int NT>
+struct Chunk {
+  static constexpr int kG = D / GROUP;
+  static constexpr int kRows = 16 * NT * kWaves;
+  static constexpr int kKeys = 8192 / D;                    // of a round: two 16-byte pieces of codes a producing lane
+  static constexpr int kSteps = D / 32;
+  // operands of 1 KiB: [16-key tile][k-extent] of keys, [step][16 channels] of values
+  static constexpr int kKOps = kKeys / 16 * kSteps, kVOps = kKeys / kStep * (D / 16);
+  static constexpr int kVStride = 1024 + 80;                // spreads the writes to eight operands over the banks
+  static constexpr int kVAt = kKOps * 1024;
+  static constexpr int kKScales = kVAt + kVOps * kVStride;  // fp32 [group][key]
+  static constexpr int kVScales = kKScales + kG * kKeys * 4;  // binary16 [group][key]
+  static constexpr int kBuffer = kVScales + kG * kKeys * 2;
+  static_assert(kBuffer % 16 == 0, "alignment");
+};
+
+// Where lane (r, kb) finds its 16 bytes of an operand: rotated so that neither
+// 16 reading lanes of one kb nor the writes of a key's pieces collide.
+__device__ __forceinline__ int op_at(int r, int kb) { return 16 * (4 * r + ((kb + (r >> 2)) & 3)); }
+
+template <int DT, int D, int GROUP, int NT>
+__device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
+  using L = Chunk<D, GROUP, NT>;
+  constexpr int G = L::kG, MT = GROUP / 16, KEYS = L::kKeys, kSteps = L::kSteps;
+  constexpr int kPer = KEYS / kStep;               // steps of a round
+  constexpr int kPieces = D / 32;                  // 16-byte pieces of a key
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][L::kBuffer];
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+  const int r = lane & 15, kb = lane >> 4;
+  uint32_t id = blockIdx.x;
+  const int kvh = static_cast<int>(id % a.sh.heads);
+  id /= a.sh.heads;
+  const int split = static_cast<int>(id % a.splits);
+  id /= a.splits;
+  const int b = static_cast<int>(id % a.seqs);
+  const int order = static_cast<int>(id / a.seqs);
+  const Sequence sq = sequence_of(a, b);
+  const int rows = sq.n * a.ratio;
+  const int tiles = (rows + L::kRows - 1) / L::kRows;
+  const int record = static_cast<int>(a.sh.record_bytes());
+  const int64_t page_bytes = static_cast<int64_t>(a.sh.heads) * record;
+  const uint8_t* head = a.cache + static_cast<int64_t>(kvh) * record;
+  const int32_t* table = a.table + b * a.table_stride;
+
+  // Producers: wavefronts 0 and 1 keys, 2 and 3 values.  Of a round a lane
+  // takes two pieces of 16 bytes: two keys' (units of 64 (2 i + half) + lane,
+  // kPieces a key), or of the two 16-key tiles of one step the same word of
+  // the same quad of keys.
+  const bool values = wave >= 2;
+  const int half = wave & 1;
+  const int unit = 64 * half + lane;
+  const int v_word = unit % (D / 8), v_quad = unit / (D / 8) % 4, v_step = unit / (D / 2);
+  const int v_group = v_word / (GROUP / 8);
+
+  // the last tiles see the most keys and go first
+  for (int tile = tiles - 1 - order; tile >= 0; tile -= a.row_tiles) {
+    const int blk_last = min((tile + 1) * L::kRows, rows) - 1;
+    const Steps st = steps_of(a, sq.first + tile * L::kRows / a.ratio, sq.first + blk_last / a.ratio);
+    const int chunks = max(1, (st.count + a.chunk - 1) / a.chunk);
+    if (split >= chunks) continue;
+    const int s_lo = split * a.chunk, s_hi = min(s_lo + a.chunk, st.count);
+    const int rounds = (s_hi - s_lo + kPer - 1) / kPer;
+    const int row_lo = tile * L::kRows + wave * 16 * NT;
+    const int row_hi = min(row_lo + 16 * NT, rows) - 1;
+    const int pos_lo = sq.first + row_lo / a.ratio;
+    const int pos_hi = row_hi < row_lo ? -1 : sq.first + row_hi / a.ratio;
+    auto key_of = [&](int s) { return s < s_hi ? st.key(s) : kBeyond; };
+
+    // ---- queries: second operands, the block's power of two, positions
+    u32x4 qv[NT][kSteps];
+    int pos[NT];
+    float most = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row_lo + 16 * n + r;
+      const bool live = row < rows;
+      const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;
+      pos[n] = live ? sq.first + tok : -1;
+      const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * kb;
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
+        if constexpr (DT == QMM_BF16) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            most = fmaxf(most, fmaxf(fabsf(bf16lo_to_f32(qv[n][j][w])), fabsf(bf16hi_to_f32(qv[n][j][w]))));
+        }
+      }
+    }
+    float unscale = 1.0f;
+    __syncthreads();                               // LDS is free: the rows before are done
+    if constexpr (DT == QMM_BF16) {
+      float* stat = reinterpret_cast<float*>(&lds[0][0]);
+      most = wave_max(most);
+      if (lane == 0) stat[wave] = most;
+      __syncthreads();
+      most = fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3]));
+      __syncthreads();
+      // 2^(14 - exponent) of the largest, held to normal numbers
+      const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 27), 254);
+      const float down = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+      unscale = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            qv[n][j][w] = pack2<QMM_F16>(bf16lo_to_f32(qv[n][j][w]) * down, bf16hi_to_f32(qv[n][j][w]) * down);
+    }
+    const float key_scale = a.scale_log2 * unscale;
+
+    // ---- producers
+    u32x4 raw[2];
+    uint32_t kpar[2][G];                           // keys: params of the two keys
+    u32x4 vpar[2];                                 // values: params of the two quads' keys
+    auto fetch = [&](int round) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int piece = 128 * i + unit;          // of the round's keys
+        const int s = s_lo + round * kPer + (values ? v_step : piece / kPieces / kStep);
+        const int t0 = key_of(s);
+        const int key = t0 + (values ? 16 * i + 4 * v_quad : piece / kPieces % kStep);
+        int page = -1;
+        if (key < sq.ctx) page = table[key >> a.sh.shift];
+        const bool here = page >= 0 && page < a.sh.pages;
+        const uint8_t* rec = head + (here ? page * page_bytes : 0);
+        const int place = key & (a.sh.page - 1);
+        raw[i] = u32x4{0u, 0u, 0u, 0u};
+        vpar[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int g = 0; g < G; ++g) kpar[i][g] = 0u;
+        if (here) {
+          if (!values) {
+            raw[i] = ld16(rec + place * (D / 2) + 16 * (piece % kPieces));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              kpar[i][g] = *reinterpret_cast<const uint32_t*>(rec + a.sh.page * D + (g * a.sh.page + place) * 4);
+          } else {
+            raw[i] = ld16(rec + a.sh.page * (D / 2) + place / 4 * (2 * D) + 16 * v_word);
+            vpar[i] = ld16(rec + a.sh.page * (D + 4 * G) + (v_group * a.sh.page + place) * 4);
+            // memory past the context may hold anything
+#pragma unroll
+            for (int x = 0; x < 4; ++x) vpar[i][x] = key + x < sq.ctx ? vpar[i][x] : 0u;
+          }
+        }
+      }
+    };
+    const uint32_t magic = vgpr_const(Codes<QMM_F16>::magic);
+    auto less = [](uint32_t p, uint32_t z) {       // pairs: (64 + c) + -(64 + z)
+      return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, p) + __builtin_bit_cast(f16x2_t, z));
+    };
+    auto expand = [&](uint8_t* buf) {
+      if (!values) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int piece = 128 * i + unit, kk = piece / kPieces, first = 4 * (piece % kPieces);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int j = (first + x) % kSteps;    // the word's k-extent and eight channels of it
+            uint32_t par = kpar[i][0];
+            if constexpr (G > 1) {
+              // D 128: word x of a piece is k-extent x; D 256, 64: first selects the half
+#pragma unroll
+              for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? kpar[i][g] : par;
+            }
+            const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
+            uint32_t p[4];
+            Codes<QMM_F16>::unpack(raw[i][x], magic, p);
+            *reinterpret_cast<u32x4*>(buf + ((kk / 16) * kSteps + j) * 1024 + op_at(kk % 16, (first + x) / kSteps)) =
+                u32x4{less(p[0], z), less(p[1], z), less(p[2], z), less(p[3], z)};
+          }
+          if (piece % kPieces == 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+              *reinterpret_cast<float*>(buf + L::kKScales + (g * KEYS + kk) * 4) = kv4_scale(kpar[i][g]) * key_scale;
+          }
+        }
+      } else {
+        uint32_t z[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          z[e] = (__builtin_amdgcn_perm(vpar[e >> 1][2 * (e & 1) + 1], vpar[e >> 1][2 * (e & 1)], 0x0c060c02u) << 4 &
+                  0x00F000F0u) | 0xD400D400u;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = __builtin_amdgcn_perm(raw[e >> 1][2 * (e & 1) + 1], raw[e >> 1][2 * (e & 1)],
+                                         part ? 0x07060302u : 0x05040100u);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = less(((y == 0 ? w[e] << 4 : w[e] >> (4 * y - 4)) & Codes<QMM_F16>::mask) | magic, z[e]);
+            const int row = 8 * (v_word & 1) + 2 * y + part;
+            *reinterpret_cast<u32x4*>(buf + L::kVAt + (v_step * (D / 16) + v_word / 2) * L::kVStride +
+                                      op_at(row, v_quad)) = v;
+          }
+        }
+        if (v_word % (GROUP / 8) == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<u32x2*>(buf + L::kVScales + (v_group * KEYS + v_step * kStep + 16 * i + 4 * v_quad) * 2) =
+                u32x2{__builtin_amdgcn_perm(vpar[i][1], vpar[i][0], 0x05040100u),
+                      __builtin_amdgcn_perm(vpar[i][3], vpar[i][2], 0x05040100u)};
+        }
+      }
+    };
+
+    f32x4 o[NT][G][MT], l[NT];
+    float base[NT];
+    float shrink[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) shrink[g] = 32768.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      base[n] = -INFINITY;
+      l[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int y = 0; y < MT; ++y) o[n][g][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const uint32_t one2 = 0x3C003C00u;
+    const u32x4 ones{one2, one2, one2, one2};
+
+    auto compute = [&](int s, int c, const uint8_t* buf) {   // step s, the c-th of the round
+      const int t0 = st.key(s);
+      // ---- scores: products of c - z, then the keys' scales
+      f32x4 x[NT][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          f32x4 acc[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j) {
+            const u32x4 k = *reinterpret_cast<const u32x4*>(buf + ((2 * c + u) * kSteps + j) * 1024 + op_at(r, kb));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n] = mfma<QMM_F16>(k, qv[n][j], acc[n]);
+          }
+          const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + c * kStep + 16 * u + 4 * kb) * 4);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[n][u][i] = g == 0 ? acc[n][i] * sc[i] : fmaf(acc[n][i], sc[i], x[n][u][i]);
+        }
+      // ---- masks
+      bool holes = false;
+      int page[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = t0 + 16 * u;
+        typedef const __attribute__((address_space(4))) int32_t* table_t;
+        page[u] = t < sq.ctx ? ((table_t)table)[t >> a.sh.shift] : -1;
+        holes |= page[u] < 0 || page[u] >= a.sh.pages;
+      }
+      const bool whole = !holes && t0 + kStep - 1 <= pos_lo &&
+                         (a.window == 0 || t0 > pos_hi - a.window || t0 + kStep <= a.sinks);
+      if (!whole) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const bool here = page[u] >= 0 && page[u] < a.sh.pages;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = t0 + 16 * u + 4 * kb + i;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const bool seen = here && t <= pos[n] && (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
+              x[n][u][i] = seen ? x[n][u][i] : -INFINITY;
+            }
+          }
+        }
+      }
+      // ---- scales of the values, pairs of keys
+      f16x2_t sv[G][4];
+      f16x2_t top2{0, 0};
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        f16x2_t t{0, 0};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const u32x2 v = *reinterpret_cast<const u32x2*>(buf + L::kVScales + (g * KEYS + c * kStep + 16 * u + 4 * kb) * 2);
+          const uint32_t first = v.x, second = v.y;
+          sv[g][2 * u] = __builtin_bit_cast(f16x2_t, first);
+          sv[g][2 * u + 1] = __builtin_bit_cast(f16x2_t, second);
+          t = pk_max(t, pk_max(sv[g][2 * u], sv[g][2 * u + 1]));
+        }
+        top2 = pk_max(top2, t * pair16(shrink[g]));
+      }
+      bool grow = top2[0] > static_cast<_Float16>(1.0f) || top2[1] > static_cast<_Float16>(1.0f);
+      if (__any(grow)) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          f16x2_t t{0, 0};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t = pk_max(t, sv[g][e]);
+          const float top = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
+          const float next = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(top) >> 23)) << 23));
+          const float f = next / shrink[g];
+          shrink[g] = next;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
+        }
+      }
+      // ---- running maximum
+      grow = false;
+      float top[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float t = fmaxf(fmaxf(x[n][0][0], x[n][0][1]), fmaxf(x[n][0][2], x[n][0][3]));
+        t = fmaxf(t, fmaxf(fmaxf(x[n][1][0], x[n][1][1]), fmaxf(x[n][1][2], x[n][1][3])));
+        top[n] = t;
+        grow |= t > base[n] + 15.0f;
+      }
+      if (__any(grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float to = fmaxf(base[n], max_over_quads(top[n]) - 7.0f);
+          const float fade = to == -INFINITY ? 1.0f : exp2_fast(base[n] - to);
+          base[n] = to;
+          l[n] *= fade;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int y = 0; y < MT; ++y) o[n][g][y] *= fade;
+        }
+      }
+      f16x2_t p[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float from = base[n] == -INFINITY ? 0.0f : base[n];
+        u32x4 pw;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[n][e] = f16x2_t{static_cast<_Float16>(exp2_fast(x[n][e >> 1][2 * (e & 1)] - from)),
+                            static_cast<_Float16>(exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - from))};
+          pw[e] = __builtin_bit_cast(uint32_t, p[n][e]);
+        }
+        l[n] = mfma<QMM_F16>(ones, pw, l[n]);
+      }
+      // ---- values
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        u32x4 pv[NT];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f16x2_t s2 = sv[g][e] * pair16(shrink[g]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) pv[n][e] = __builtin_bit_cast(uint32_t, p[n][e] * s2);
+        }
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(buf + L::kVAt + (c * (D / 16) + g * MT + y) * L::kVStride +
+                                                          op_at(r, kb));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[n][g][y] = mfma<QMM_F16>(v, pv[n], o[n][g][y]);
+        }
+      }
+    };
+
+    // ---- rounds: operands of the next one, codes of the one after
+    if (rounds > 0) {
+      fetch(0);
+      expand(&lds[0][0]);
+      if (rounds > 1) fetch(1);
+    }
+    __syncthreads();
+    for (int round = 0; round < rounds; ++round) {
+      if (round + 1 < rounds) expand(&lds[(round + 1) & 1][0]);
+      if (round + 2 < rounds) fetch(round + 2);
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        const int s = s_lo + round * kPer + c;
+        if (s < s_hi) compute(s, c, &lds[round & 1][0]);
+      }
+      __syncthreads();
+    }
+
+    // ---- results: column r of row 4 kb + i of every tile
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = row_lo + 16 * n + r;
+      if (row >= rows) continue;
+      const int tok = row / a.ratio;
+      const int64_t rh = static_cast<int64_t>(sq.row0 + tok) * a.q_heads + kvh * a.ratio + row - tok * a.ratio;
+      const float sum = l[n][0];
+      const float inv = chunks > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float f = inv / shrink[g];
+#pragma unroll
+        for (int y = 0; y < MT; ++y) {
+          const f32x4 v = o[n][g][y] * f;
+          const int c0 = (g * MT + y) * 16 + 4 * kb;
+          if (chunks > 1)
+            *reinterpret_cast<f32x4*>(a.part_o + (rh * a.splits + split) * D + c0) = v;
+          else
+            *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w)};
+        }
+      }
+      if (kb == 0) {
+        if (chunks > 1) a.part_ml[rh * a.splits + split] = make_float2(base[n], sum);
+        else if (a.lse) a.lse[rh] = lse_of(base[n], sum);
+      }
+    }
+  }
+}
+
+// Two blocks a compute unit where the registers allow it: one wavefront's
+// products then run under the other's exponentials.
+template <int DT, int D, int GROUP, int NT>
+__global__ __launch_bounds__(256, NT * D <= 256 ? 2 : 1) void attention_chunk_kernel(AttnArgs a) {
+  attention_chunk_block<DT, D, GROUP, NT>(a);
+}
+
+}  // namespace
+}  // namespace qmm
