@@ -28,7 +28,7 @@ struct Chunk {
   static constexpr int kSteps = D / 32;
   // operands of 1 KiB: [16-key tile][k-extent] of keys, [step][16 channels] of values
   static constexpr int kKOps = kKeys / 16 * kSteps, kVOps = kKeys / kStep * (D / 16);
-  static constexpr int kVStride = 1024 + 80;                // spreads the writes to eight operands over the banks
+  static constexpr int kVStride = 1024 + 80;                // a value's eight channels go to 16 operand rows: no bank twice
   static constexpr int kVAt = kKOps * 1024;
   static constexpr int kKScales = kVAt + kVOps * kVStride;  // fp32 [group][key]
   static constexpr int kVScales = kKScales + kG * kKeys * 4;  // binary16 [group][key]
@@ -36,9 +36,16 @@ struct Chunk {
   static_assert(kBuffer % 16 == 0, "alignment");
 };
 
-// Where lane (r, kb) finds its 16 bytes of an operand: rotated so that neither
-// 16 reading lanes of one kb nor the writes of a key's pieces collide.
-__device__ __forceinline__ int op_at(int r, int kb) { return 16 * (4 * r + ((kb + (r >> 2)) & 3)); }
+// Lane (r, kb) finds its 16 bytes of an operand in lane order, and producers
+// are mapped so that any 16 lanes write 16 different rows: no bank conflicts.
+__device__ __forceinline__ int op_at(int r, int kb) { return 16 * (16 * kb + r); }
+
+// The compiler's maximum quiets each operand first; these are products already.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
 
 template <int DT, int D, int GROUP, int NT>
 __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
@@ -46,6 +53,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   constexpr int G = L::kG, MT = GROUP / 16, KEYS = L::kKeys, kSteps = L::kSteps;
   constexpr int kPer = KEYS / kStep;               // steps of a round
   constexpr int kPieces = D / 32;                  // 16-byte pieces of a key
+  constexpr int kTiles = KEYS / 16;                // 16-key tiles of a round
+  constexpr int U = kPer < 2 ? 1 : 2;              // steps whose scores are taken together
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][L::kBuffer];
 
   const int lane = threadIdx.x & (kWave - 1);
@@ -64,17 +73,29 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   const int record = static_cast<int>(a.sh.record_bytes());
   const int64_t page_bytes = static_cast<int64_t>(a.sh.heads) * record;
   const uint8_t* head = a.cache + static_cast<int64_t>(kvh) * record;
-  const int32_t* table = a.table + b * a.table_stride;
+  typedef const __attribute__((address_space(4))) int32_t* table_t;
+  const table_t table = (table_t)(a.table + b * a.table_stride);
 
   // Producers: wavefronts 0 and 1 keys, 2 and 3 values.  Of a round a lane
-  // takes two pieces of 16 bytes: two keys' (units of 64 (2 i + half) + lane,
-  // kPieces a key), or of the two 16-key tiles of one step the same word of
-  // the same quad of keys.
+  // takes two pieces of 16 bytes: of keys the lane's (lane & 15) in one or two
+  // 16-key tiles, or of both tiles of a step the same word of the same quad of
+  // keys.
   const bool values = wave >= 2;
   const int half = wave & 1;
   const int unit = 64 * half + lane;
   const int v_word = unit % (D / 8), v_quad = unit / (D / 8) % 4, v_step = unit / (D / 2);
   const int v_group = v_word / (GROUP / 8);
+  int k_piece[2], my_tile[2];                      // my_tile: the 16-key tile of a piece
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = 4 * (2 * i + half) + (lane >> 4);
+    k_piece[i] = m % kPieces;
+    my_tile[i] = values ? 2 * v_step + i : m / kPieces;
+  }
+  const int first_key = values ? 4 * v_quad : r;   // of the lane's in a tile
+  // byte offsets in a record: at + place * per (codes), params likewise
+  const int raw_at = values ? a.sh.page * (D / 2) + 16 * v_word + v_quad * (2 * D) : r * (D / 2);
+  const int par_at = values ? a.sh.page * (D + 4 * G) + v_group * a.sh.page * 4 + 16 * v_quad : a.sh.page * D + 4 * r;
 
   // the last tiles see the most keys and go first
   for (int tile = tiles - 1 - order; tile >= 0; tile -= a.row_tiles) {
@@ -136,38 +157,76 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 
     // ---- producers
     u32x4 raw[2];
-    uint32_t kpar[2][G];                           // keys: params of the two keys
+    uint32_t kpar[2][G];                           // keys: params of the two pieces' keys
     u32x4 vpar[2];                                 // values: params of the two quads' keys
-    auto fetch = [&](int round) {
+    struct Round {                                 // first keys of its steps, pages of its tiles
+      int key[kPer], page[kTiles];
+    };
+    auto round_of = [&](int round) {
+      Round x;
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        const int at = s_lo + round * kPer + c;
+        x.key[c] = at < s_hi ? st.key(at) : kBeyond;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int t = x.key[c] + 16 * u;
+          x.page[2 * c + u] = t < sq.ctx ? table[t >> a.sh.shift] : -1;
+        }
+      }
+      return x;
+    };
+    auto holes_of = [&](const Round& x) {
+      int h = 0;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) h |= x.page[t] < 0 || x.page[t] >= a.sh.pages ? 1 << t : 0;
+      return h;
+    };
+    auto fetch = [&](const Round& x) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int piece = 128 * i + unit;          // of the round's keys
-        const int s = s_lo + round * kPer + (values ? v_step : piece / kPieces / kStep);
-        const int t0 = key_of(s);
-        const int key = t0 + (values ? 16 * i + 4 * v_quad : piece / kPieces % kStep);
-        int page = -1;
-        if (key < sq.ctx) page = table[key >> a.sh.shift];
-        const bool here = page >= 0 && page < a.sh.pages;
-        const uint8_t* rec = head + (here ? page * page_bytes : 0);
-        const int place = key & (a.sh.page - 1);
-        raw[i] = u32x4{0u, 0u, 0u, 0u};
-        vpar[i] = u32x4{0u, 0u, 0u, 0u};
+        // D 128 and 256: the tile is the wavefront's; D 64: two tiles of 32 lanes each, with a part of the lanes each
+        constexpr int kPasses = D == 64 ? 2 : 1;
 #pragma unroll
-        for (int g = 0; g < G; ++g) kpar[i][g] = 0u;
-        if (here) {
-          if (!values) {
-            raw[i] = ld16(rec + place * (D / 2) + 16 * (piece % kPieces));
+        for (int pass = 0; pass < kPasses; ++pass) {
+          const int tile_n = D == 64 ? (values ? 4 * half + 2 * pass + i : 2 * (2 * i + half) + pass)
+                             : D == 128 ? (values ? 2 * half + i : 2 * i + half) : i;
+          int page = x.page[0], t0 = x.key[0];
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-              kpar[i][g] = *reinterpret_cast<const uint32_t*>(rec + a.sh.page * D + (g * a.sh.page + place) * 4);
-          } else {
-            raw[i] = ld16(rec + a.sh.page * (D / 2) + place / 4 * (2 * D) + 16 * v_word);
-            vpar[i] = ld16(rec + a.sh.page * (D + 4 * G) + (v_group * a.sh.page + place) * 4);
-            // memory past the context may hold anything
+          for (int t = 1; t < kTiles; ++t) {
+            page = tile_n == t ? x.page[t] : page;
+            t0 = tile_n == t ? x.key[t / 2] + 16 * (t % 2) : t0;
+          }
+          if (D != 64 || (lane >> 5) == pass) {
+            const bool here = page >= 0 && page < a.sh.pages;
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t*>(head + (here ? page * page_bytes : 0)), 0, here ? record : 0, kBufferWord3);
+            const int place = t0 & (a.sh.page - 1);
+            raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   rs, raw_at + (values ? 0 : 16 * k_piece[i]), place * (D / 2), 0));
+            if (values) {
+              vpar[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, par_at, place * 4, 0));
+            } else {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) vpar[i][x] = key + x < sq.ctx ? vpar[i][x] : 0u;
+              for (int g = 0; g < G; ++g)
+                kpar[i][g] = __builtin_amdgcn_raw_buffer_load_b32(rs, par_at + g * a.sh.page * 4, place * 4, 0);
+            }
           }
         }
+      }
+    };
+    // Memory past the context may hold anything: its scales and zero-points are taken as 0.
+    auto clean = [&](const Round& x) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int t0 = x.key[0];
+#pragma unroll
+        for (int t = 1; t < kTiles; ++t) t0 = my_tile[i] == t ? x.key[t / 2] + 16 * (t % 2) : t0;
+        const int key = t0 + first_key;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vpar[i][e] = key + e < sq.ctx ? vpar[i][e] : 0u;
+#pragma unroll
+        for (int g = 0; g < G; ++g) kpar[i][g] = key < sq.ctx ? kpar[i][g] : 0u;
       }
     };
     const uint32_t magic = vgpr_const(Codes<QMM_F16>::magic);
@@ -178,26 +237,24 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       if (!values) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int piece = 128 * i + unit, kk = piece / kPieces, first = 4 * (piece % kPieces);
+          const int first = 4 * k_piece[i];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int j = (first + x) % kSteps;    // the word's k-extent and eight channels of it
             uint32_t par = kpar[i][0];
-            if constexpr (G > 1) {
-              // D 128: word x of a piece is k-extent x; D 256, 64: first selects the half
 #pragma unroll
-              for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? kpar[i][g] : par;
-            }
+            for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? kpar[i][g] : par;
             const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
             uint32_t p[4];
             Codes<QMM_F16>::unpack(raw[i][x], magic, p);
-            *reinterpret_cast<u32x4*>(buf + ((kk / 16) * kSteps + j) * 1024 + op_at(kk % 16, (first + x) / kSteps)) =
+            *reinterpret_cast<u32x4*>(buf + (my_tile[i] * kSteps + j) * 1024 + op_at(r, (first + x) / kSteps)) =
                 u32x4{less(p[0], z), less(p[1], z), less(p[2], z), less(p[3], z)};
           }
-          if (piece % kPieces == 0) {
+          if (k_piece[i] == 0) {
 #pragma unroll
             for (int g = 0; g < G; ++g)
-              *reinterpret_cast<float*>(buf + L::kKScales + (g * KEYS + kk) * 4) = kv4_scale(kpar[i][g]) * key_scale;
+              *reinterpret_cast<float*>(buf + L::kKScales + (g * KEYS + 16 * my_tile[i] + r) * 4) =
+                  kv4_scale(kpar[i][g]) * key_scale;
           }
         }
       } else {
@@ -251,12 +308,12 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     const uint32_t one2 = 0x3C003C00u;
     const u32x4 ones{one2, one2, one2, one2};
 
-    auto compute = [&](int s, int c, const uint8_t* buf) {   // step s, the c-th of the round
-      const int t0 = st.key(s);
+    // U steps from the c0-th of a round on
+    auto compute = [&](const int (&key)[kPer], int holes, int c0, const uint8_t* buf) {
       // ---- scores: products of c - z, then the keys' scales
-      f32x4 x[NT][2];
+      f32x4 x[NT][2 * U];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2 * U; ++u)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           f32x4 acc[NT];
@@ -264,35 +321,28 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(buf + ((2 * c + u) * kSteps + j) * 1024 + op_at(r, kb));
+            const u32x4 k = *reinterpret_cast<const u32x4*>(buf + ((2 * c0 + u) * kSteps + j) * 1024 + op_at(r, kb));
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[n] = mfma<QMM_F16>(k, qv[n][j], acc[n]);
           }
-          const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + c * kStep + 16 * u + 4 * kb) * 4);
+          const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + 32 * c0 + 16 * u + 4 * kb) * 4);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[n][u][i] = g == 0 ? acc[n][i] * sc[i] : fmaf(acc[n][i], sc[i], x[n][u][i]);
         }
       // ---- masks
-      bool holes = false;
-      int page[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int t = t0 + 16 * u;
-        typedef const __attribute__((address_space(4))) int32_t* table_t;
-        page[u] = t < sq.ctx ? ((table_t)table)[t >> a.sh.shift] : -1;
-        holes |= page[u] < 0 || page[u] >= a.sh.pages;
-      }
-      const bool whole = !holes && t0 + kStep - 1 <= pos_lo &&
-                         (a.window == 0 || t0 > pos_hi - a.window || t0 + kStep <= a.sinks);
+      const int first = key[c0], end = key[c0 + U - 1] + kStep;
+      const int miss = (holes >> (2 * c0)) & ((1 << (2 * U)) - 1);
+      const bool whole = miss == 0 && end - first == U * kStep && end - 1 <= pos_lo &&
+                         (a.window == 0 || first > pos_hi - a.window || end <= a.sinks);
       if (!whole) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const bool here = page[u] >= 0 && page[u] < a.sh.pages;
+        for (int u = 0; u < 2 * U; ++u) {
+          const bool here = !((miss >> u) & 1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = t0 + 16 * u + 4 * kb + i;
+            const int t = key[c0 + u / 2] + 16 * (u % 2) + 4 * kb + i;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const bool seen = here && t <= pos[n] && (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
@@ -302,17 +352,17 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         }
       }
       // ---- scales of the values, pairs of keys
-      f16x2_t sv[G][4];
+      f16x2_t sv[G][4 * U];
       f16x2_t top2{0, 0};
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         f16x2_t t{0, 0};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const u32x2 v = *reinterpret_cast<const u32x2*>(buf + L::kVScales + (g * KEYS + c * kStep + 16 * u + 4 * kb) * 2);
-          const uint32_t first = v.x, second = v.y;
-          sv[g][2 * u] = __builtin_bit_cast(f16x2_t, first);
-          sv[g][2 * u + 1] = __builtin_bit_cast(f16x2_t, second);
+        for (int u = 0; u < 2 * U; ++u) {
+          const u32x2 v = *reinterpret_cast<const u32x2*>(buf + L::kVScales + (g * KEYS + 32 * c0 + 16 * u + 4 * kb) * 2);
+          const uint32_t v0 = v.x, v1 = v.y;
+          sv[g][2 * u] = __builtin_bit_cast(f16x2_t, v0);
+          sv[g][2 * u + 1] = __builtin_bit_cast(f16x2_t, v1);
           t = pk_max(t, pk_max(sv[g][2 * u], sv[g][2 * u + 1]));
         }
         top2 = pk_max(top2, t * pair16(shrink[g]));
@@ -323,7 +373,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         for (int g = 0; g < G; ++g) {
           f16x2_t t{0, 0};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t = pk_max(t, sv[g][e]);
+          for (int e = 0; e < 4 * U; ++e) t = pk_max(t, sv[g][e]);
           const float top = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
           const float next = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(top) >> 23)) << 23));
           const float f = next / shrink[g];
@@ -339,8 +389,18 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       float top[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float t = fmaxf(fmaxf(x[n][0][0], x[n][0][1]), fmaxf(x[n][0][2], x[n][0][3]));
-        t = fmaxf(t, fmaxf(fmaxf(x[n][1][0], x[n][1][1]), fmaxf(x[n][1][2], x[n][1][3])));
+        float t = max3(x[n][0][0], x[n][0][1], x[n][0][2]);
+        t = max3(t, x[n][0][3], x[n][1][0]);
+        t = max3(t, x[n][1][1], x[n][1][2]);
+        if constexpr (U == 1) {
+          t = max3(t, x[n][1][3], x[n][1][3]);
+        } else {
+          t = max3(t, x[n][1][3], x[n][2][0]);
+          t = max3(t, x[n][2][1], x[n][2][2]);
+          t = max3(t, x[n][2][3], x[n][3][0]);
+          t = max3(t, x[n][3][1], x[n][3][2]);
+          t = max3(t, x[n][3][3], x[n][3][3]);
+        }
         top[n] = t;
         grow |= t > base[n] + 15.0f;
       }
@@ -357,54 +417,67 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
             for (int y = 0; y < MT; ++y) o[n][g][y] *= fade;
         }
       }
-      f16x2_t p[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float from = base[n] == -INFINITY ? 0.0f : base[n];
-        u32x4 pw;
+      for (int c = 0; c < U; ++c) {
+        f16x2_t p[NT][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[n][e] = f16x2_t{static_cast<_Float16>(exp2_fast(x[n][e >> 1][2 * (e & 1)] - from)),
-                            static_cast<_Float16>(exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - from))};
-          pw[e] = __builtin_bit_cast(uint32_t, p[n][e]);
+        for (int n = 0; n < NT; ++n) {
+          const float from = base[n] == -INFINITY ? 0.0f : base[n];
+          u32x4 pw;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f32x4& xs = x[n][2 * c + (e >> 1)];
+            p[n][e] = f16x2_t{static_cast<_Float16>(exp2_fast(xs[2 * (e & 1)] - from)),
+                              static_cast<_Float16>(exp2_fast(xs[2 * (e & 1) + 1] - from))};
+            pw[e] = __builtin_bit_cast(uint32_t, p[n][e]);
+          }
+          l[n] = mfma<QMM_F16>(ones, pw, l[n]);
         }
-        l[n] = mfma<QMM_F16>(ones, pw, l[n]);
-      }
-      // ---- values
+        // ---- values
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        u32x4 pv[NT];
+        for (int g = 0; g < G; ++g) {
+          u32x4 pv[NT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f16x2_t s2 = sv[g][e] * pair16(shrink[g]);
+          for (int e = 0; e < 4; ++e) {
+            const f16x2_t s2 = sv[g][4 * c + e] * pair16(shrink[g]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) pv[n][e] = __builtin_bit_cast(uint32_t, p[n][e] * s2);
-        }
+            for (int n = 0; n < NT; ++n) pv[n][e] = __builtin_bit_cast(uint32_t, p[n][e] * s2);
+          }
 #pragma unroll
-        for (int y = 0; y < MT; ++y) {
-          const u32x4 v = *reinterpret_cast<const u32x4*>(buf + L::kVAt + (c * (D / 16) + g * MT + y) * L::kVStride +
-                                                          op_at(r, kb));
+          for (int y = 0; y < MT; ++y) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(
+                buf + L::kVAt + ((c0 + c) * (D / 16) + g * MT + y) * L::kVStride + op_at(r, kb));
 #pragma unroll
-          for (int n = 0; n < NT; ++n) o[n][g][y] = mfma<QMM_F16>(v, pv[n], o[n][g][y]);
+            for (int n = 0; n < NT; ++n) o[n][g][y] = mfma<QMM_F16>(v, pv[n], o[n][g][y]);
+          }
         }
       }
     };
 
-    // ---- rounds: operands of the next one, codes of the one after
+    // ---- rounds: this one's products, the next one's operands, the codes of
+    // the one after, and the pages of the one after that
+    Round now = round_of(0), next = round_of(1), then = round_of(2);
     if (rounds > 0) {
-      fetch(0);
+      fetch(now);
+      if (now.key[kPer - 1] + kStep > sq.ctx) clean(now);
       expand(&lds[0][0]);
-      if (rounds > 1) fetch(1);
+      if (rounds > 1) fetch(next);
     }
     __syncthreads();
     for (int round = 0; round < rounds; ++round) {
-      if (round + 1 < rounds) expand(&lds[(round + 1) & 1][0]);
-      if (round + 2 < rounds) fetch(round + 2);
-#pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        const int s = s_lo + round * kPer + c;
-        if (s < s_hi) compute(s, c, &lds[round & 1][0]);
+      if (round + 1 < rounds) {
+        if (next.key[kPer - 1] + kStep > sq.ctx) clean(next);
+        expand(&lds[(round + 1) & 1][0]);
       }
+      if (round + 2 < rounds) fetch(then);
+      const Round last = round_of(round + 3);
+      const int holes = holes_of(now);
+#pragma unroll
+      for (int c = 0; c < kPer; c += U)
+        if (now.key[c] < kBeyond) compute(now.key, holes, c, &lds[round & 1][0]);
+      now = next;
+      next = then;
+      then = last;
       __syncthreads();
     }
 
