@@ -12,6 +12,7 @@ has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Sequence, Tuple
@@ -125,11 +126,11 @@ def _call(name: str, *args) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())     # without a Stream object around it
 
 
 def _dt(dtype: torch.dtype) -> int:
@@ -740,9 +741,13 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, group: i
     return torch.empty(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
 
 
+# Small calls are bound by what happens before the launch, so each operand is
+# first compared with what is wanted in one expression, and only where that
+# fails goes through the checks that name the fault.
 def _cache_shape(cache, head_dim: int):
     """(pages, kv_heads, page, group) of a cache for heads of head_dim channels."""
-    _req(cache, "cache", (torch.uint8,), ndim=4)
+    if type(cache) is not torch.Tensor or cache.dtype is not torch.uint8 or cache.dim() != 4:
+        _req(cache, "cache", (torch.uint8,), ndim=4)
     pages, heads, page, token = cache.shape
     groups, rest = divmod(token - head_dim, 8)
     if groups <= 0 or rest or head_dim % groups:
@@ -751,38 +756,61 @@ def _cache_shape(cache, head_dim: int):
     return pages, heads, page, head_dim // groups
 
 
-def _heads(t, name: str, dtypes, shape: Tuple):
-    """Check rows of heads [T, heads, D] (strided views, as slices of a projection's output, are fine); returns the
-    token and head strides."""
-    _req(t, name, dtypes, shape=shape)
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name} must have its channels consecutive, has strides {t.stride()}")
-    ts, hs = t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
-    if (ts | hs) & 7:
-        raise ValueError(f"{name} must have token and head strides that are multiples of 8, has strides {t.stride()}")
+def _rows(t, name: str, dtypes) -> Tuple:
+    """Shape of rows of heads [T, heads, D]."""
+    if type(t) is not torch.Tensor or t.dtype not in dtypes or t.dim() != 3:
+        _req(t, name, dtypes, ndim=3)
+    return t.shape
+
+
+def _strides(t, name: str):
+    """Token and head strides of rows of heads (strided views, as slices of a projection's output, are fine)."""
+    ts, hs, cs = t.stride()
+    if cs != 1 or (ts | hs) & 7:
+        T, heads, D = t.shape                              # a single row's stride means nothing
+        ts, hs = ts if T > 1 else 0, hs if heads > 1 else 0
+        if cs != 1 and D > 1:
+            raise ValueError(f"{name} must have its channels consecutive, has strides {t.stride()}")
+        if (ts | hs) & 7:
+            raise ValueError(f"{name} must have token and head strides that are multiples of 8, has strides {t.stride()}")
     return ts, hs
 
 
-def _same_device(dev, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other operands on {dev}")
+def _vector(t, name: str, dtype, n: int) -> None:
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != (n,):
+        _req(t, name, (dtype,), shape=(n,))
+
+
+def _on(dev: int, strided: Sequence, **dense) -> None:
+    """All operands on GPU `dev` (None entries are skipped), the dense ones contiguous."""
+    if dev < 0:
+        raise ValueError("the operands must be device tensors")
+    for t in strided:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"an operand is on {t.device}, another on GPU {dev}")
+    for name, t in dense.items():
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, another operand on GPU {dev}")
+            raise ValueError(f"{name} must be contiguous")
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor) -> None:
     """Quantize keys and values [T, kv_heads, D] into the slots (int64 [T], page id * page + place; distinct; -1
     writes nothing) of the cache."""
-    _req(k, "k", _HALVES, ndim=3)
-    T, heads, D = k.shape
-    pages, _, page, group = _cache_shape(cache, D)
-    _req(cache, "cache", (torch.uint8,), shape=(None, heads, None, None))
-    kt, kh = _heads(k, "k", (k.dtype,), (T, heads, D))
-    vt, vh = _heads(v, "v", (k.dtype,), (T, heads, D))
-    _req(slots, "slots", (torch.int64,), shape=(T,))
-    dev = _place(cache=cache, slots=slots)
-    _same_device(dev, k=k, v=v)
-    _call("kv4_append", _ptr(k), kt, kh, _ptr(v), vt, vh, _dt(k.dtype), T, _ptr(slots), _ptr(cache), pages, heads, D,
-          page, group, _stream(cache))
+    T, heads, D = shape = _rows(k, "k", _HALVES)
+    pages, kv_heads, page, group = _cache_shape(cache, D)
+    if heads != kv_heads:
+        raise ValueError(f"k has {heads} heads, the cache {kv_heads}")
+    dtype = k.dtype
+    if _rows(v, "v", (dtype,)) != shape:
+        _req(v, "v", (dtype,), shape=shape)
+    kt, kh = _strides(k, "k")
+    vt, vh = _strides(v, "v")
+    _vector(slots, "slots", torch.int64, T)
+    _on(cache.get_device(), (k, v), cache=cache, slots=slots)
+    _call("kv4_append", k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DT[dtype], T, slots.data_ptr(), cache.data_ptr(),
+          pages, heads, D, page, group, _stream(cache))
 
 
 def kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16):
@@ -792,11 +820,11 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: tor
         raise ValueError(f"unsupported output dtype {dtype}")
     pages, heads, page, group = _cache_shape(cache, head_dim)
     _req(slots, "slots", (torch.int64,), ndim=1)
-    dev = _place(cache=cache, slots=slots)
-    k = torch.empty((slots.shape[0], heads, head_dim), dtype=dtype, device=dev)
-    v = torch.empty_like(k)
-    _call("kv4_read", _ptr(cache), pages, heads, head_dim, page, group, _ptr(slots), slots.shape[0], _ptr(k), _ptr(v),
-          _dt(dtype), _stream(cache))
+    T = slots.shape[0]
+    _on(cache.get_device(), (), cache=cache, slots=slots)
+    k, v = cache.new_empty((2, T, heads, head_dim), dtype=dtype).unbind()
+    _call("kv4_read", cache.data_ptr(), pages, heads, head_dim, page, group, slots.data_ptr(), T, k.data_ptr(),
+          v.data_ptr(), _DT[dtype], _stream(cache))
     return k, v
 
 
@@ -807,13 +835,15 @@ def kv4_copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) ->
         raise ValueError("cache must be a torch.Tensor of 4 dimensions, or 5 with layers")
     _req(cache, "cache", (torch.uint8,))
     _req(src, "src", (torch.int64,), ndim=1)
-    _req(dst, "dst", (torch.int64,), shape=(src.shape[0],))
-    _place(cache=cache, src=src, dst=dst)
-    layers, pages = (1, cache.shape[0]) if cache.dim() == 4 else cache.shape[:2]
-    _call("kv4_copy_pages", _ptr(cache), layers, pages, math.prod(cache.shape[-3:]), _ptr(src), _ptr(dst),
-          src.shape[0], _stream(cache))
+    n = src.shape[0]
+    _vector(dst, "dst", torch.int64, n)
+    _on(cache.get_device(), (), cache=cache, src=src, dst=dst)
+    *layers, pages, heads, page, token = cache.shape
+    _call("kv4_copy_pages", cache.data_ptr(), layers[0] if layers else 1, pages, heads * page * token, src.data_ptr(),
+          dst.data_ptr(), n, _stream(cache))
 
 
+@functools.lru_cache(maxsize=4096)      # of sizes alone
 def kv4_attention_workspace_bytes(T: int, seqs: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
                                   max_context: int, window: int = 0, sinks: int = 0) -> int:
     return int(lib().kv4_attention_workspace_bytes(T, seqs, max_q, q_heads, kv_heads, head_dim, max_context, window,
@@ -829,42 +859,47 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     rows cu_q[b] .. cu_q[b + 1] - 1 of q (int32 [seqs + 1]; max_q, a hint, the most of a sequence).  window: the keys a
     query sees (0: all before it), sinks: the first keys that stay visible.  Returns out [T, q_heads, D], with
     return_lse also the fp32 log-sum-exp [T, q_heads]; a row that sees no key is 0 and -inf."""
-    _req(q, "q", _HALVES, ndim=3)
-    T, q_heads, D = q.shape
+    T, q_heads, D = shape = _rows(q, "q", _HALVES)
+    dtype = q.dtype
     pages, kv_heads, page, group = _cache_shape(cache, D)
     if q_heads % kv_heads:
         raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {kv_heads}")
-    qt, qh = _heads(q, "q", (q.dtype,), (T, q_heads, D))
-    _req(context, "context", (torch.int32,), ndim=1)
-    seqs = context.shape[0]
-    _req(page_table, "page_table", (torch.int32,), shape=(seqs, None))
-    width = page_table.shape[1]
-    if width > 1 and page_table.stride(1) != 1:
+    qt, qh = _strides(q, "q")
+    if type(page_table) is not torch.Tensor or page_table.dtype is not torch.int32 or page_table.dim() != 2:
+        _req(page_table, "page_table", (torch.int32,), ndim=2)
+    seqs, width = page_table.shape
+    _vector(context, "context", torch.int32, seqs)
+    stride, one = page_table.stride()
+    if width > 1 and one != 1:
         raise ValueError(f"page_table must have consecutive rows, has strides {page_table.stride()}")
-    stride = page_table.stride(0) if seqs > 1 else width
+    if seqs < 2:
+        stride = width
     if cu_q is not None:
-        _req(cu_q, "cu_q", (torch.int32,), shape=(seqs + 1,))
+        _vector(cu_q, "cu_q", torch.int32, seqs + 1)
+        most = max(1, T if max_q is None else int(max_q))
     elif T != seqs:
         raise ValueError(f"q has {T} rows for {seqs} sequences: without cu_q each has one")
+    else:
+        most = 1
     if window < 0 or sinks < 0:
         raise ValueError(f"window and sinks must be >= 0, not {window} and {sinks}")
-    most = 1 if cu_q is None else max(1, T if max_q is None else int(max_q))
-    _out(out, (T, q_heads, D), q.dtype)
-    dev = _place(cache=cache, context=context, cu_q=cu_q, out=out, workspace=workspace)
-    _same_device(dev, q=q, page_table=page_table)
+    if out is not None:
+        _out(out, shape, dtype)
+    _on(q.get_device(), (page_table,), cache=cache, context=context, cu_q=cu_q, out=out, workspace=workspace)
     need = kv4_attention_workspace_bytes(T, seqs, most, q_heads, kv_heads, D, width * page, window, sinks)
     if workspace is not None:
         _req(workspace, "workspace", (torch.uint8,), ndim=1)
         if workspace.numel() < need:
             raise ValueError(f"workspace holds {workspace.numel()} bytes; {need} needed")
     elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    out = _alloc(out, (T, q_heads, D), q.dtype, dev)
-    lse = torch.empty((T, q_heads), dtype=torch.float32, device=dev) if return_lse else None
-    _call("kv4_attention", _ptr(q), qt, qh, _dt(q.dtype), T, q_heads, _ptr(cu_q), seqs, most, _ptr(context),
-          _ptr(page_table), width, stride, _ptr(cache), pages, kv_heads, D, page, group,
-          D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse), _ptr(workspace),
-          workspace.numel() if workspace is not None else 0, _stream(q))
+        workspace = cache.new_empty(need)
+    if out is None:
+        out = q.new_empty(shape)
+    lse = q.new_empty((T, q_heads), dtype=torch.float32) if return_lse else None
+    _call("kv4_attention", q.data_ptr(), qt, qh, _DT[dtype], T, q_heads, _ptr(cu_q), seqs, most, context.data_ptr(),
+          page_table.data_ptr(), width, stride, cache.data_ptr(), pages, kv_heads, D, page, group,
+          D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(lse), _ptr(workspace),
+          need if workspace is not None else 0, _stream(q))
     return (out, lse) if return_lse else out
 
 
@@ -931,43 +966,49 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     """Norms of each head of q [T, q_heads, D] and k [T, k_heads, D] (RMS, where its weight [D] is given, in their type
     or fp32) and the rotation of its first 2 * table.shape[1] channels at positions (int64 [T]) by the table, in halves
     or interleaved pairs; returns (q_out, k_out).  k may be None, q_out / k_out the inputs themselves (dense ones)."""
-    _req(q, "q", _HALVES, ndim=3)
-    T, q_heads, D = q.shape
-    qt, qh = _heads(q, "q", (q.dtype,), (T, q_heads, D))
-    _out(q_out, (T, q_heads, D), q.dtype, "q_out")
+    T, q_heads, D = shape = _rows(q, "q", _HALVES)
+    dtype = q.dtype
+    qt, qh = _strides(q, "q")
     k_heads = kt = kh = 0
     if k is not None:
-        kt, kh = _heads(k, "k", (q.dtype,), (T, None, D))
-        k_heads = k.shape[1]
-        _out(k_out, (T, k_heads, D), q.dtype, "k_out")
+        k_shape = _rows(k, "k", (dtype,))
+        k_heads = k_shape[1]
+        if k_shape != (T, k_heads, D):
+            _req(k, "k", (dtype,), shape=(T, None, D))
+        kt, kh = _strides(k, "k")
     elif k_weight is not None or k_out is not None:
         raise ValueError("k_weight and k_out need k")
-    w_dtype = q.dtype
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _req(w, name, (q.dtype, torch.float32), shape=(D,))
-            w_dtype = w.dtype
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError(f"q_weight has dtype {q_weight.dtype}, k_weight {k_weight.dtype}")
+    if q_out is not None or k_out is not None:
+        _out(q_out, shape, dtype, "q_out")
+        _out(k_out, (T, k_heads, D), dtype, "k_out")
+    w_dtype = dtype
+    if q_weight is not None:
+        w_dtype = torch.float32 if q_weight.dtype is torch.float32 else dtype
+        _vector(q_weight, "q_weight", w_dtype, D)
+    if k_weight is not None:
+        if q_weight is None and k_weight.dtype is torch.float32:
+            w_dtype = torch.float32
+        _vector(k_weight, "k_weight", w_dtype, D)
     if not eps >= 0.0:
         raise ValueError(f"eps must be >= 0, not {eps}")
     rows = rot = 0
     if table is not None:
-        _req(table, "table", (torch.float32,), shape=(None, None, 2))
-        rows, rot = table.shape[0], 2 * table.shape[1]
+        if type(table) is not torch.Tensor or table.dtype is not torch.float32 or table.dim() != 3 or table.shape[2] != 2:
+            _req(table, "table", (torch.float32,), shape=(None, None, 2))
+        rows, half, _ = table.shape
+        rot = 2 * half
         if rot > D:
             raise ValueError(f"table rotates {rot} channels of heads of {D}")
-        _req(positions, "positions", (torch.int64,), shape=(T,))
+        _vector(positions, "positions", torch.int64, T)
     elif positions is not None:
         raise ValueError("positions need a table")
-    dev = _place(q_weight=q_weight, k_weight=k_weight, positions=positions, table=table, q_out=q_out, k_out=k_out)
-    if not q.is_cuda:
-        raise ValueError("q must be a device tensor")
-    _same_device(dev or q.device, q=q, k=k)
-    q_out = _alloc(q_out, (T, q_heads, D), q.dtype, q.device)
-    if k is not None:
-        k_out = _alloc(k_out, (T, k_heads, D), q.dtype, q.device)
-    _call("qk_norm_rope", _ptr(q), qt, qh, q_heads, _ptr(k), kt, kh, k_heads, _dt(q.dtype), T, D, _ptr(positions),
-          _ptr(table), rows, rot, int(interleaved), _ptr(q_weight), _ptr(k_weight), _dt(w_dtype), eps, _ptr(q_out),
+    _on(q.get_device(), (k,), q_weight=q_weight, k_weight=k_weight, positions=positions, table=table, q_out=q_out,
+        k_out=k_out)
+    if q_out is None:
+        q_out = q.new_empty(shape)
+    if k is not None and k_out is None:
+        k_out = k.new_empty(k_shape)
+    _call("qk_norm_rope", q.data_ptr(), qt, qh, q_heads, _ptr(k), kt, kh, k_heads, _DT[dtype], T, D, _ptr(positions),
+          _ptr(table), rows, rot, interleaved, _ptr(q_weight), _ptr(k_weight), _DT[w_dtype], eps, q_out.data_ptr(),
           _ptr(k_out), _stream(q))
     return q_out, k_out

@@ -109,7 +109,6 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     const int row_hi = min(row_lo + 16 * NT, rows) - 1;
     const int pos_lo = sq.first + row_lo / a.ratio;
     const int pos_hi = row_hi < row_lo ? -1 : sq.first + row_hi / a.ratio;
-    auto key_of = [&](int s) { return s < s_hi ? st.key(s) : kBeyond; };
 
     // ---- queries: second operands, the block's power of two, positions
     u32x4 qv[NT][kSteps];
@@ -367,25 +366,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         }
         top2 = pk_max(top2, t * pair16(shrink[g]));
       }
+      // ---- running maximum and powers of two: one test for both
       bool grow = top2[0] > static_cast<_Float16>(1.0f) || top2[1] > static_cast<_Float16>(1.0f);
-      if (__any(grow)) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          f16x2_t t{0, 0};
-#pragma unroll
-          for (int e = 0; e < 4 * U; ++e) t = pk_max(t, sv[g][e]);
-          const float top = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
-          const float next = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(top) >> 23)) << 23));
-          const float f = next / shrink[g];
-          shrink[g] = next;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
-        }
-      }
-      // ---- running maximum
-      grow = false;
       float top[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -405,6 +387,20 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         grow |= t > base[n] + 15.0f;
       }
       if (__any(grow)) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          f16x2_t t{0, 0};
+#pragma unroll
+          for (int e = 0; e < 4 * U; ++e) t = pk_max(t, sv[g][e]);
+          const float top = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
+          const float next = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(top) >> 23)) << 23));
+          const float f = next / shrink[g];
+          shrink[g] = next;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float to = fmaxf(base[n], max_over_quads(top[n]) - 7.0f);
@@ -474,11 +470,15 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       const int holes = holes_of(now);
 #pragma unroll
       for (int c = 0; c < kPer; c += U)
-        if (now.key[c] < kBeyond) compute(now.key, holes, c, &lds[round & 1][0]);
+        if (now.key[c] != kBeyond) compute(now.key, holes, c, &lds[round & 1][0]);
       now = next;
       next = then;
       then = last;
-      __syncthreads();
+      // only LDS is shared: the codes on their way need not have come
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
     }
 
     // ---- results: column r of row 4 kb + i of every tile
