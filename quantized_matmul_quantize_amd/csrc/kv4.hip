@@ -31,40 +31,45 @@ __device__ __forceinline__ float lanes_max(float v) {
   return v;
 }
 
-// Which (token, head, word) a thread takes.  Threads run over the words of a
-// (token, head), then four consecutive tokens, then heads: a 16-lane row is
-// one token's 128 channels, and the four tokens whose V words lie side by side
-// are neighbours in a wavefront.
+// Which (token, head, word) a thread takes: the words of a token's head on
+// consecutive lanes, then four consecutive tokens (whose V words lie side by
+// side), then heads; blockIdx.x the quad of tokens, blockIdx.y heads, of keys
+// and then of values.  No division: they cost more than the quantization.
 struct Place {
   int64_t t;
   int h, w;
+  bool values;
 };
-__device__ __forceinline__ Place place_of(int64_t i, int words_log2, int heads) {
+template <int D>
+__device__ __forceinline__ Place place_of() {
+  constexpr int kWords = D / 8, kHeads = 256 / (4 * kWords);
+  const int y = static_cast<int>(blockIdx.y), i = static_cast<int>(threadIdx.x);
   Place p;
-  p.w = static_cast<int>(i & ((1 << words_log2) - 1));
-  const int64_t u = i >> words_log2;
-  const int64_t quad_head = u >> 2;
-  p.h = static_cast<int>(quad_head % heads);
-  p.t = (quad_head / heads) * 4 + (u & 3);
+  p.values = y & 1;
+  p.w = i % kWords;
+  p.t = static_cast<int64_t>(blockIdx.x) * 4 + i / kWords % 4;
+  p.h = (y >> 1) * kHeads + i / (4 * kWords);
   return p;
 }
 
 // A thread quantizes eight channels (one code word); the group's range comes
-// from its GROUP / 8 lanes.  blockIdx.y: keys, values.  Bound by memory: 2
-// bytes read and 0.5 + 4 / GROUP written per channel.
-template <int DT, int GROUP>
+// from its GROUP / 8 lanes.  The codes are those of exact division, through a
+// correctly rounded reciprocal and one correction (q0 = x y, q = q0 + (x - q0 s) y
+// is the correctly rounded quotient while nothing over- or underflows: s is
+// 2^-24 .. 65504; x is held to finite numbers first, which changes no clamped
+// code).  Bound by memory: 2 bytes read and 0.5 + 4 / GROUP written per channel.
+template <int DT, int D, int GROUP>
 __global__ __launch_bounds__(256) void kv4_append_kernel(const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs,
                                                          const uint16_t* __restrict__ v, int64_t v_ts, int64_t v_hs,
                                                          int64_t T, const int64_t* __restrict__ slots,
-                                                         uint8_t* __restrict__ cache, Kv4Shape sh, int words_log2) {
+                                                         uint8_t* __restrict__ cache, Kv4Shape sh) {
   constexpr int kLanes = GROUP / 8;
-  const bool values = blockIdx.y != 0;
-  const Place p = place_of(static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, words_log2, sh.heads);
+  const Place p = place_of<D>();
   int64_t slot = -1;
   float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (p.t < T) {
+  if (p.t < T && p.h < sh.heads) {
     slot = slots[p.t];
-    Vec8<DT>::load((values ? v + p.t * v_ts + p.h * v_hs : k + p.t * k_ts + p.h * k_hs) + 8 * p.w, x);
+    Vec8<DT>::load((p.values ? v + p.t * v_ts + p.h * v_hs : k + p.t * k_ts + p.h * k_hs) + 8 * p.w, x);
   }
   float lo = 0.0f, hi = 0.0f;
 #pragma unroll
@@ -78,22 +83,28 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const uint16_t* __restr
   const _Float16 s16 = static_cast<_Float16>(s >= kScaleMax16 ? kScaleMax16 : s);   // round to nearest even
   s = static_cast<float>(s16);
   if (s == 0.0f) s = 1.0f;
-  const float z = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
+  const float y = 1.0f / s;
+  auto quotient = [&](float a) {
+    a = __builtin_amdgcn_fmed3f(a, -3.0e38f, 3.0e38f);
+    const float q0 = a * y;
+    return fmaf(fmaf(-q0, s, a), y, q0);
+  };
+  const float z = fminf(fmaxf(rintf(quotient(-lo)), 0.0f), 15.0f);
   uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float c = fminf(fmaxf(rintf(x[i] / s) + z, 0.0f), 15.0f);
+    const float c = __builtin_amdgcn_fmed3f(rintf(quotient(x[i])) + z, 0.0f, 15.0f);
     word |= static_cast<uint32_t>(c) << (4 * code_nibble(i));
   }
   const int64_t id = slot >> sh.shift;
   if (slot < 0 || id >= sh.pages) return;
   const int t = static_cast<int>(slot) & (sh.page - 1);
   uint8_t* record = cache + (id * sh.heads + p.h) * sh.record_bytes();
-  *reinterpret_cast<uint32_t*>(record + (values ? kv4_v_word(t, p.w, sh.D, sh.page) : kv4_k_word(t, p.w, sh.D))) = word;
+  *reinterpret_cast<uint32_t*>(record + (p.values ? kv4_v_word(t, p.w, D, sh.page) : kv4_k_word(t, p.w, D))) = word;
   if (p.w % kLanes == 0) {
     const uint32_t param = f32_to_f16_bits(s) | (static_cast<uint32_t>(z) << 16);
     const int g = p.w / kLanes;
-    reinterpret_cast<uint32_t*>(record + (values ? sh.v_params() : sh.k_params()))[g * sh.page + t] = param;
+    reinterpret_cast<uint32_t*>(record + (p.values ? sh.v_params() : sh.k_params()))[g * sh.page + t] = param;
   }
 }
 
@@ -109,13 +120,12 @@ __device__ __forceinline__ void store8(void* out, int64_t i, const float x[8]) {
   }
 }
 
-template <int DT>
+template <int DT, int D>
 __global__ __launch_bounds__(256) void kv4_read_kernel(const uint8_t* __restrict__ cache, Kv4Shape sh,
                                                        const int64_t* __restrict__ slots, int64_t T,
-                                                       void* __restrict__ k, void* __restrict__ v, int words_log2) {
-  const bool values = blockIdx.y != 0;
-  const Place p = place_of(static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, words_log2, sh.heads);
-  if (p.t >= T) return;
+                                                       void* __restrict__ k, void* __restrict__ v) {
+  const Place p = place_of<D>();
+  if (p.t >= T || p.h >= sh.heads) return;
   const int64_t slot = slots[p.t];
   const int64_t id = slot >> sh.shift;
   float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -123,14 +133,15 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(const uint8_t* __restrict
     const int t = static_cast<int>(slot) & (sh.page - 1);
     const uint8_t* record = cache + (id * sh.heads + p.h) * sh.record_bytes();
     const uint32_t word = *reinterpret_cast<const uint32_t*>(
-        record + (values ? kv4_v_word(t, p.w, sh.D, sh.page) : kv4_k_word(t, p.w, sh.D)));
+        record + (p.values ? kv4_v_word(t, p.w, D, sh.page) : kv4_k_word(t, p.w, D)));
+    const int g = p.w >> (__builtin_ctz(sh.group) - 3);
     const uint32_t param = reinterpret_cast<const uint32_t*>(
-        record + (values ? sh.v_params() : sh.k_params()))[8 * p.w / sh.group * sh.page + t];
+        record + (p.values ? sh.v_params() : sh.k_params()))[g * sh.page + t];
     const float s = kv4_scale(param), z = kv4_zero(param);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = (static_cast<float>(kv4_code(word, i)) - z) * s;
   }
-  store8<DT>(values ? v : k, (p.t * sh.heads + p.h) * sh.D + 8 * p.w, x);
+  store8<DT>(p.values ? v : k, (p.t * sh.heads + p.h) * D + 8 * p.w, x);
 }
 
 // Page copies: blockIdx.z a layer, blockIdx.x a pair, blockIdx.y 16 KiB of
@@ -159,22 +170,41 @@ __global__ __launch_bounds__(256) void kv4_copy_kernel(uint8_t* __restrict__ cac
   }
 }
 
-template <int DT>
-void launch_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, int64_t T,
-                   const int64_t* slots, uint8_t* cache, const Kv4Shape& sh, dim3 grid, int words_log2,
-                   hipStream_t s) {
-  const uint16_t* kp = static_cast<const uint16_t*>(k);
-  const uint16_t* vp = static_cast<const uint16_t*>(v);
-  if (sh.group == 32)
-    kv4_append_kernel<DT, 32><<<grid, 256, 0, s>>>(kp, k_ts, k_hs, vp, v_ts, v_hs, T, slots, cache, sh, words_log2);
-  else if (sh.group == 64)
-    kv4_append_kernel<DT, 64><<<grid, 256, 0, s>>>(kp, k_ts, k_hs, vp, v_ts, v_hs, T, slots, cache, sh, words_log2);
-  else
-    kv4_append_kernel<DT, 128><<<grid, 256, 0, s>>>(kp, k_ts, k_hs, vp, v_ts, v_hs, T, slots, cache, sh, words_log2);
+// Blocks over the words of T tokens (in whole quads).
+dim3 word_grid(int64_t T, const Kv4Shape& sh) {
+  const int heads = 256 / (4 * (sh.D / 8));
+  return dim3(static_cast<unsigned>(ceil_div(T, 4)), static_cast<unsigned>(2 * ceil_div(sh.heads, heads)));
 }
 
-// Blocks of 256 threads over the words of T tokens (in whole quads); < 2^31.
-int64_t word_blocks(int64_t T, const Kv4Shape& sh) { return ceil_div(ceil_div(T, 4) * 4 * sh.heads * (sh.D / 8), 256); }
+template <int DT>
+void launch_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs, int64_t T,
+                   const int64_t* slots, uint8_t* cache, const Kv4Shape& sh, hipStream_t s) {
+  const uint16_t* kp = static_cast<const uint16_t*>(k);
+  const uint16_t* vp = static_cast<const uint16_t*>(v);
+  const dim3 grid = word_grid(T, sh);
+#define QMM_APPEND(D, G) \
+  kv4_append_kernel<DT, D, G><<<grid, 256, 0, s>>>(kp, k_ts, k_hs, vp, v_ts, v_hs, T, slots, cache, sh)
+  switch (sh.D * 1000 + sh.group) {
+    case 64032: QMM_APPEND(64, 32); break;
+    case 64064: QMM_APPEND(64, 64); break;
+    case 128032: QMM_APPEND(128, 32); break;
+    case 128064: QMM_APPEND(128, 64); break;
+    case 128128: QMM_APPEND(128, 128); break;
+    case 256032: QMM_APPEND(256, 32); break;
+    case 256064: QMM_APPEND(256, 64); break;
+    default: QMM_APPEND(256, 128); break;
+  }
+#undef QMM_APPEND
+}
+
+template <int DT>
+void launch_read(const uint8_t* cache, const Kv4Shape& sh, const int64_t* slots, int64_t T, void* k, void* v,
+                 hipStream_t s) {
+  const dim3 grid = word_grid(T, sh);
+  if (sh.D == 64) kv4_read_kernel<DT, 64><<<grid, 256, 0, s>>>(cache, sh, slots, T, k, v);
+  else if (sh.D == 128) kv4_read_kernel<DT, 128><<<grid, 256, 0, s>>>(cache, sh, slots, T, k, v);
+  else kv4_read_kernel<DT, 256><<<grid, 256, 0, s>>>(cache, sh, slots, T, k, v);
+}
 
 }  // namespace
 }  // namespace qmm
@@ -195,18 +225,15 @@ extern "C" int kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_
   Kv4Shape sh;
   if (const int st = kv4_shape(pages, kv_heads, head_dim, page, group, &sh)) return st;
   if (dtype != QMM_BF16 && dtype != QMM_F16) return QMM_EUNSUPPORTED;
-  if (T >= (int64_t{1} << 31) || word_blocks(T, sh) >= (int64_t{1} << 31)) return QMM_ERANGE;
+  if (T >= (int64_t{1} << 31)) return QMM_ERANGE;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cache, 16) || !aligned(slots, 8) ||
       (k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7)
     return QMM_EALIGN;
-  const int words_log2 = __builtin_ctz(static_cast<unsigned>(sh.D / 8));
-  const dim3 grid(static_cast<unsigned>(word_blocks(T, sh)), 2);
+  hipStream_t s = as_stream(stream);
   if (dtype == QMM_BF16)
-    launch_append<QMM_BF16>(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, T, slots, cache, sh,
-                            grid, words_log2, as_stream(stream));
+    launch_append<QMM_BF16>(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, T, slots, cache, sh, s);
   else
-    launch_append<QMM_F16>(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, T, slots, cache, sh,
-                           grid, words_log2, as_stream(stream));
+    launch_append<QMM_F16>(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, T, slots, cache, sh, s);
   return launch_status();
 }
 
@@ -219,17 +246,12 @@ extern "C" int kv4_read(const uint8_t* cache, int64_t pages, int64_t kv_heads, i
   Kv4Shape sh;
   if (const int st = kv4_shape(pages, kv_heads, head_dim, page, group, &sh)) return st;
   if (out_dtype == QMM_I32) return QMM_EUNSUPPORTED;
-  if (T >= (int64_t{1} << 31) || word_blocks(T, sh) >= (int64_t{1} << 31)) return QMM_ERANGE;
+  if (T >= (int64_t{1} << 31)) return QMM_ERANGE;
   if (!aligned(cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(slots, 8)) return QMM_EALIGN;
-  const int words_log2 = __builtin_ctz(static_cast<unsigned>(sh.D / 8));
-  const dim3 grid(static_cast<unsigned>(word_blocks(T, sh)), 2);
   hipStream_t s = as_stream(stream);
-  if (out_dtype == QMM_BF16)
-    kv4_read_kernel<QMM_BF16><<<grid, 256, 0, s>>>(cache, sh, slots, T, k_out, v_out, words_log2);
-  else if (out_dtype == QMM_F16)
-    kv4_read_kernel<QMM_F16><<<grid, 256, 0, s>>>(cache, sh, slots, T, k_out, v_out, words_log2);
-  else
-    kv4_read_kernel<QMM_F32><<<grid, 256, 0, s>>>(cache, sh, slots, T, k_out, v_out, words_log2);
+  if (out_dtype == QMM_BF16) launch_read<QMM_BF16>(cache, sh, slots, T, k_out, v_out, s);
+  else if (out_dtype == QMM_F16) launch_read<QMM_F16>(cache, sh, slots, T, k_out, v_out, s);
+  else launch_read<QMM_F32>(cache, sh, slots, T, k_out, v_out, s);
   return launch_status();
 }
 

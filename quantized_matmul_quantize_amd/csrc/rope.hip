@@ -1,6 +1,8 @@
 // rope.hip -- norms of queries and keys for each head with the rotation by
 // position in the same pass, and the table of cosines and sines it reads.
 
+#include <algorithm>
+
 #include "qmm_device.h"
 
 namespace qmm {
@@ -51,71 +53,146 @@ struct HeadRows {
 };
 
 // A head's D channels lie on `lanes` (a power of two) consecutive lanes,
-// eight channels each.  Bound by memory: 2 bytes read and 2 written per
-// channel, 4 rot bytes of table per token.
-template <int DT, int WDT>
-__global__ __launch_bounds__(256) void qk_norm_rope_kernel(HeadRows q, HeadRows k, int64_t T, int D,
+// eight channels each; a block takes one token (blockIdx.x) and `per_block`
+// of its heads (blockIdx.y), kHeads passes at a time in flight: the cosines,
+// sines and weights of a lane's channels are loaded once for all of them.
+// Bound by memory: 2 bytes read and 2 written per channel, 4 rot bytes of
+// table per token.
+constexpr int kHeads = 4;
+
+template <int DT, int WDT, bool NORM, bool INTERLEAVED>
+__global__ __launch_bounds__(256) void qk_norm_rope_kernel(HeadRows q, HeadRows k, int D,
                                                            const int64_t* __restrict__ positions,
                                                            const float* __restrict__ table, int64_t table_rows,
-                                                           int rot, int interleaved, float eps, int lanes_log2) {
-  const int lanes = 1 << lanes_log2;
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> lanes_log2;
+                                                           int rot, float eps, int lanes_log2, int per_block) {
+  const int lanes = 1 << lanes_log2, width = 256 >> lanes_log2;
   const int c = (threadIdx.x & (lanes - 1)) * 8;                // first channel of this lane
+  const int64_t t = blockIdx.x;
   const int heads = q.heads + k.heads;
-  const int64_t t = unit / heads;
-  const int h = static_cast<int>(unit % heads);
-  const bool live = t < T && c < D;
-  const HeadRows& r = h < q.heads ? q : k;
-  const int hr = h < q.heads ? h : h - q.heads;
-  float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (live) load8<DT>(r.in, t * r.token_stride + hr * r.head_stride + c, x);
-  if (r.weight) {
-    float sum = 0.0f;
+  const int first = static_cast<int>(blockIdx.y) * per_block + (static_cast<int>(threadIdx.x) >> lanes_log2);
+  const int end = min(static_cast<int>(blockIdx.y + 1) * per_block, heads);
+  const bool live = c < D, turned = c < rot;
+  const int half = rot / 2;
+  const bool low = INTERLEAVED || c < half;
+
+  float cs[8], sn[8];      // interleaved: four pairs; halves: eight, the sine negated in the first half
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-    for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor(sum, o, kWave);
-    const float inv = 1.0f / sqrtf(sum / static_cast<float>(D) + eps);
-    float w[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) load8<WDT>(r.weight, c, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * w[i];
+  for (int i = 0; i < 8; ++i) {
+    cs[i] = 1.0f;
+    sn[i] = 0.0f;
   }
-  if (rot > 0) {
-    const int half = rot / 2;
-    int64_t p = live ? positions[t] : 0;
-    const bool known = p >= 0 && p < table_rows;
-    const float2* row = reinterpret_cast<const float2*>(table) + (known ? p : 0) * half;
-    if (interleaved) {
-      if (live && c < rot) {
+  if (rot > 0 && turned) {
+    const int64_t p = positions[t];
+    if (p >= 0 && p < table_rows) {
+      const f32x4* row = reinterpret_cast<const f32x4*>(table + p * rot + (INTERLEAVED ? c : 2 * (low ? c : c - half)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 cs = row[c / 2 + i];
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = known ? a * cs.x - b * cs.y : __builtin_nanf("");
-          x[2 * i + 1] = known ? b * cs.x + a * cs.y : __builtin_nanf("");
-        }
+      for (int i = 0; i < (INTERLEAVED ? 2 : 4); ++i) {
+        const f32x4 v = row[i];
+        cs[2 * i] = v.x;
+        sn[2 * i] = INTERLEAVED || !low ? v.y : -v.y;
+        cs[2 * i + 1] = v.z;
+        sn[2 * i + 1] = INTERLEAVED || !low ? v.w : -v.w;
       }
     } else {
-      // the partner's eight channels are half a rotation away, on another lane
-      const bool low = c < half;
-      const int partner = (threadIdx.x & (kWave - 1)) + (c < rot ? (low ? half / 8 : -(half / 8)) : 0);
-      float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner, kWave);
-      if (live && c < rot) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 cs = row[(low ? c : c - half) + i];
-          const float turned = low ? x[i] * cs.x - y[i] * cs.y : x[i] * cs.x + y[i] * cs.y;
-          x[i] = known ? turned : __builtin_nanf("");
-        }
-      }
+      for (int i = 0; i < 8; ++i) cs[i] = sn[i] = __builtin_nanf("");
     }
   }
-  if (!live) return;
-  uint16_t* o = r.out + (t * r.heads + hr) * D + c;
-  *reinterpret_cast<u32x4*>(o) =
-      u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])};
+  float qw[8], kw[8];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) qw[i] = kw[i] = 0.0f;
+    if (live && q.weight) load8<WDT>(q.weight, c, qw);
+    if (live && k.weight) load8<WDT>(k.weight, c, kw);
+  }
+  // the partner's eight channels are half a rotation away, on another lane of the head
+  const int partner = (threadIdx.x & (kWave - 1)) + (turned ? (low ? half / 8 : -(half / 8)) : 0);
+  const float inv_d = 1.0f / static_cast<float>(D);
+
+  for (int h0 = first; h0 < end; h0 += kHeads * width) {
+    u32x4 raw[kHeads];
+#pragma unroll
+    for (int n = 0; n < kHeads; ++n) {
+      const int h = h0 + n * width;
+      raw[n] = u32x4{0u, 0u, 0u, 0u};
+      if (live && h < end) {
+        const HeadRows& r = h < q.heads ? q : k;
+        raw[n] = ld16_nt(r.in + t * r.token_stride + (h < q.heads ? h : h - q.heads) * r.head_stride + c);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kHeads; ++n) {
+      const int h = h0 + n * width;
+      if (h0 - first + n * width >= per_block) break;           // the same for the whole block
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = DT == QMM_BF16 ? bf16lo_to_f32(raw[n][j]) : f16lo_to_f32(raw[n][j]);
+        x[2 * j + 1] = DT == QMM_BF16 ? bf16hi_to_f32(raw[n][j]) : f16hi_to_f32(raw[n][j]);
+      }
+      const bool is_q = h < q.heads;
+      if constexpr (NORM) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+        if (lanes >= 2) sum += dpp_f<kDppXor1>(sum);
+        if (lanes >= 4) sum += dpp_f<kDppXor2>(sum);
+        if (lanes >= 8) sum += dpp_f<kDppHalfMirror>(sum);
+        if (lanes >= 16) sum += dpp_f<kDppMirror>(sum);
+        if (lanes >= 32) sum += __shfl_xor(sum, 16, kWave);
+        if (lanes >= 64) sum += __shfl_xor(sum, 32, kWave);
+        if (is_q ? q.weight != nullptr : k.weight != nullptr) {
+          const float inv = __builtin_amdgcn_rsqf(fmaf(sum, inv_d, eps));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (is_q ? qw[i] : kw[i]);
+        }
+      }
+      if (rot > 0) {
+        if constexpr (INTERLEAVED) {
+          if (turned) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = x[2 * i], b = x[2 * i + 1];
+              x[2 * i] = fmaf(a, cs[i], -(b * sn[i]));
+              x[2 * i + 1] = fmaf(b, cs[i], a * sn[i]);
+            }
+          }
+        } else {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = __shfl(x[i], partner, kWave);
+          if (turned) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
+          }
+        }
+      }
+      if (!live || h >= end) continue;
+      uint16_t* o = is_q ? q.out + (t * q.heads + h) * D + c : k.out + (t * k.heads + h - q.heads) * D + c;
+      st16_nt(o, u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
+    }
+  }
+}
+
+template <int DT, int WDT>
+void launch_rope(const HeadRows& q, const HeadRows& k, int64_t T, int D, const int64_t* positions, const float* table,
+                 int64_t rows, int rot, bool interleaved, float eps, int lanes_log2, hipStream_t s) {
+  const int heads = q.heads + k.heads, width = 256 >> lanes_log2;
+  // heads of a block: all, but for few tokens as many blocks as fill the chip
+  const int64_t passes = ceil_div(heads, width);
+  const int64_t split = std::min<int64_t>(passes, ceil_div(4 * device_cus(), T));
+  const int per_block = static_cast<int>(ceil_div(passes, split) * width);
+  const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(ceil_div(heads, per_block)));
+  const bool norm = q.weight || k.weight;
+#define QMM_ROPE(NORM, INTER) \
+  qk_norm_rope_kernel<DT, WDT, NORM, INTER><<<grid, 256, 0, s>>>(q, k, D, positions, table, rows, rot, eps, lanes_log2, \
+                                                                 per_block)
+  if (norm) {
+    if (interleaved) QMM_ROPE(true, true); else QMM_ROPE(true, false);
+  } else {
+    if (interleaved) QMM_ROPE(false, true); else QMM_ROPE(false, false);
+  }
+#undef QMM_ROPE
 }
 
 }  // namespace
@@ -153,9 +230,7 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_hea
   if (q_heads > 65535 || k_heads > 65535) return QMM_ERANGE;
   int lanes_log2 = 0;
   while ((8 << lanes_log2) < head_dim) ++lanes_log2;
-  const int64_t units = T < (int64_t{1} << 31) ? T * (q_heads + k_heads) : (int64_t{1} << 62);
-  const int64_t blocks = ceil_div(units, 256 >> lanes_log2);
-  if (blocks >= (int64_t{1} << 31)) return QMM_ERANGE;
+  if (T >= (int64_t{1} << 31)) return QMM_ERANGE;
   if (!aligned(q, 16) || !aligned(q_out, 16) || (k_heads > 0 && (!aligned(k, 16) || !aligned(k_out, 16))) ||
       !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 8) || !aligned(table, 16) ||
       ((q_token_stride | q_head_stride) & 7) || (k_heads > 0 && ((k_token_stride | k_head_stride) & 7)))
@@ -164,18 +239,15 @@ extern "C" int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_hea
                     static_cast<uint16_t*>(q_out), static_cast<int32_t>(q_heads)};
   const HeadRows kr{static_cast<const uint16_t*>(k), k_token_stride, k_head_stride, k_weight,
                     static_cast<uint16_t*>(k_out), static_cast<int32_t>(k_heads)};
-  const unsigned grid = static_cast<unsigned>(blocks);
   const int D = static_cast<int>(head_dim), r = static_cast<int>(rot);
   hipStream_t s = as_stream(stream);
-  const bool f32w = w_dtype == QMM_F32;
-#define QMM_LAUNCH(DT, WDT) \
-  qk_norm_rope_kernel<DT, WDT><<<grid, 256, 0, s>>>(qr, kr, T, D, positions, table, table_rows, r, interleaved != 0, \
-                                                    eps, lanes_log2)
+  const bool f32w = weights && w_dtype == QMM_F32, inter = interleaved != 0;
   if (dtype == QMM_BF16) {
-    if (f32w) QMM_LAUNCH(QMM_BF16, QMM_F32); else QMM_LAUNCH(QMM_BF16, QMM_BF16);
+    if (f32w) launch_rope<QMM_BF16, QMM_F32>(qr, kr, T, D, positions, table, table_rows, r, inter, eps, lanes_log2, s);
+    else launch_rope<QMM_BF16, QMM_BF16>(qr, kr, T, D, positions, table, table_rows, r, inter, eps, lanes_log2, s);
   } else {
-    if (f32w) QMM_LAUNCH(QMM_F16, QMM_F32); else QMM_LAUNCH(QMM_F16, QMM_F16);
+    if (f32w) launch_rope<QMM_F16, QMM_F32>(qr, kr, T, D, positions, table, table_rows, r, inter, eps, lanes_log2, s);
+    else launch_rope<QMM_F16, QMM_F16>(qr, kr, T, D, positions, table, table_rows, r, inter, eps, lanes_log2, s);
   }
-#undef QMM_LAUNCH
   return launch_status();
 }
