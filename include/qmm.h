@@ -515,7 +515,8 @@ size_t kv4_page_bytes(int64_t kv_heads, int64_t head_dim, int64_t page, int grou
 
 /* Quantize the keys and values of T tokens into their slots.
  * k, v  : [T, kv_heads, D] of dtype, channels consecutive; token and head
- *         strides in elements, multiples of 8; 16-byte aligned.
+ *         strides in elements, multiples of 8, token strides below 2^26;
+ *         16-byte aligned.  Infinities saturate, NaN is stored as code 0.
  * slots : int64 [T], device, distinct; a slot outside [0, pages * page) (such
  *         as -1 for padding) writes nothing. */
 int kv4_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,

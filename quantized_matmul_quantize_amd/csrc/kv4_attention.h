@@ -657,7 +657,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
             if (c0 == 0) a.part_ml[rh * a.splits + split] = make_float2(M, sum);
           } else {
             v *= sum > 0.0f ? 1.0f / sum : 0.0f;
-            *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w)};
+            *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack_pair<DT>(v.x, v.y), pack_pair<DT>(v.z, v.w)};
             if (a.lse && c0 == 0) a.lse[rh] = lse_of(M, sum);
           }
         }
@@ -685,7 +685,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           for (int c = 0; c < D / 4; c += 8) {
             const float* v = own + r * kPad + kb * (D / 4) + c;
             *reinterpret_cast<u32x4*>(a.out + rh * D + kb * (D / 4) + c) =
-                u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+                u32x4{pack_pair<DT>(v[0], v[1]), pack_pair<DT>(v[2], v[3]), pack_pair<DT>(v[4], v[5]), pack_pair<DT>(v[6], v[7])};
           }
         }
         asm volatile("" ::: "memory");
@@ -737,7 +737,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int row
 #pragma unroll
       for (int g = 1; g < kGroups; ++g) o += sums[g * kWide + c4];
       o *= l > 0.0f ? 1.0f / l : 0.0f;
-      *reinterpret_cast<u32x2*>(a.out + rh * D + 4 * c4) = u32x2{pack2<DT>(o.x, o.y), pack2<DT>(o.z, o.w)};
+      *reinterpret_cast<u32x2*>(a.out + rh * D + 4 * c4) = u32x2{pack_pair<DT>(o.x, o.y), pack_pair<DT>(o.z, o.w)};
       if (a.lse && c4 == 0) a.lse[rh] = lse_of(m, l);
     }
   }

@@ -150,7 +150,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         for (int j = 0; j < kSteps; ++j)
 #pragma unroll
           for (int w = 0; w < 4; ++w)
-            qv[n][j][w] = pack2<QMM_F16>(bf16lo_to_f32(qv[n][j][w]) * down, bf16hi_to_f32(qv[n][j][w]) * down);
+            qv[n][j][w] = pack_pair<QMM_F16>(bf16lo_to_f32(qv[n][j][w]) * down, bf16hi_to_f32(qv[n][j][w]) * down);
     }
     const float key_scale = a.scale_log2 * unscale;
 
@@ -500,7 +500,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           if (chunks > 1)
             *reinterpret_cast<f32x4*>(a.part_o + (rh * a.splits + split) * D + c0) = v;
           else
-            *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w)};
+            *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack_pair<DT>(v.x, v.y), pack_pair<DT>(v.z, v.w)};
         }
       }
       if (kb == 0) {

@@ -76,6 +76,18 @@ __device__ __forceinline__ uint32_t pack2<QMM_F16>(float a, float b) {
   return f32_to_f16_bits(a) | (f32_to_f16_bits(b) << 16);
 }
 
+// The same by the hardware's pair conversion (one instruction; keeps NaN).
+template <int DT>
+__device__ __forceinline__ uint32_t pack_pair(float a, float b) {
+  if constexpr (DT == QMM_BF16) {
+    const bf16x2_t p{static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, p);
+  } else {
+    const f16x2_t p{static_cast<_Float16>(a), static_cast<_Float16>(b)};
+    return __builtin_bit_cast(uint32_t, p);
+  }
+}
+
 // Eight consecutive elements of a 16/32-bit float row as fp32.
 template <int DT>
 struct Vec8;

@@ -169,7 +169,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(HeadRows q, HeadRows 
       }
       if (!live || h >= end) continue;
       uint16_t* o = is_q ? q.out + (t * q.heads + h) * D + c : k.out + (t * k.heads + h - q.heads) * D + c;
-      st16_nt(o, u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])});
+      st16_nt(o, u32x4{pack_pair<DT>(x[0], x[1]), pack_pair<DT>(x[2], x[3]), pack_pair<DT>(x[4], x[5]), pack_pair<DT>(x[6], x[7])});
     }
   }
 }

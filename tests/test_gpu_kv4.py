@@ -77,6 +77,27 @@ def test_append_bytes_and_read_values(dtype, D, group, T, page, heads):
             assert torch.equal(y.cpu(), torch.from_numpy(val).float().to(out_dtype))
 
 
+@pytest.mark.parametrize("D,group,heads,T", [(64, 32, 8, 4099), (128, 64, 5, 2050), (256, 128, 3, 2049)])
+def test_append_of_many_tokens(D, group, heads, T):
+    """Enough tokens for the form that takes several a thread, their count no multiple of what a thread takes."""
+    note(f"kv4 append of many tokens D={D} group={group} heads={heads} T={T}")
+    g, page = rng(T), 64
+    pages = -(-T // page)
+    k, v = (half(g.standard_normal((T, heads, D)), F16) for _ in range(2))
+    slots = torch.from_numpy(g.permutation(pages * page)[:T].astype(np.int64))
+    slots[7] = -1
+    cache = dirty(pages, heads, D, page, group)
+    want = cache.cpu().numpy().copy()
+    qmm.kv4_append(k.cuda(), v.cuda(), slots.cuda(), cache)
+    ref.store(want, k.float().numpy(), v.float().numpy(), slots.tolist())
+    assert np.array_equal(cache.cpu().numpy(), want)
+    kr, vr = qmm.kv4_read(cache, slots.cuda(), D, dtype=F32)
+    for x, y in ((k, kr), (v, vr)):
+        val = ref.values(*ref.quantize(x.float().numpy(), group))
+        val[7] = 0
+        assert np.array_equal(y.cpu().numpy(), val.astype(np.float32))
+
+
 def test_append_infinities_and_nan_stay_in_their_group():
     D, group, page = 128, 32, 16
     k = half(rng(3).standard_normal((4, 2, D)), BF16)
