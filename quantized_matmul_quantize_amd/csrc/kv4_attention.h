@@ -31,11 +31,12 @@
 //
 // What bounds decode is the vector unit, not the matrix cores: two operations
 // a pair of codes to make operands of them, and then the arithmetic on the
-// scores, of which few rows leave most columns idle.  So with 8 (4) rows or
-// fewer a wavefront takes 2 (4) steps at once (PK): every group of 16 / PK
-// columns holds the same rows but keeps the scores, maxima, sums and results
-// of a step of its own, and the groups are joined at the end, as the
-// wavefronts are.
+// scores, of which few rows leave most columns idle.  So with 8 rows or fewer
+// a wavefront takes two steps at once (PK = 2): both halves of the columns
+// hold the same rows but keep the scores, maxima, sums and results of a step
+// of their own, and are joined at the end, as the wavefronts are.  (Four steps
+// at once for 4 rows: 220 instead of 250 vector operations a step, but 70 KiB
+// of LDS a block and 58 instead of 54 us for 64 sequences of 4096 tokens.)
 #pragma once
 
 #include "kv4_attention_args.h"
@@ -89,6 +90,12 @@ __device__ __forceinline__ float max_over_quads(float v) {
 __device__ __forceinline__ float sum_over_quads(float v) {
   v += __shfl_xor(v, 16, kWave);
   return v + __shfl_xor(v, 32, kWave);
+}
+// The compiler's maximum quiets each operand first; these are products already.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
 }
 __device__ __forceinline__ f16x2_t pk_max(f16x2_t a, f16x2_t b) { return __builtin_elementwise_max(a, b); }
 __device__ __forceinline__ f16x2_t pair16(float v) {
@@ -171,7 +178,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
     k_per = 4;
   }
   const int record = static_cast<int>(a.sh.record_bytes());
-  const int64_t page_bytes = static_cast<int64_t>(a.sh.heads) * record;
+  const uint32_t page_bytes = static_cast<uint32_t>(a.sh.heads) * static_cast<uint32_t>(record);
   const uint8_t* head = a.cache + static_cast<int64_t>(kvh) * record;
   uint8_t* const mine = lds + wave * L::kWaveBytes;
   const uint32_t mine_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(mine));
@@ -180,10 +187,12 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 
   // A 16-key tile past the context, or whose page is not of this cache, is
   // read through an empty resource: zeros, so scales of 0.
+  const uint32_t pages = static_cast<uint32_t>(a.sh.pages);
   auto tile_of = [&](int page) {
-    const bool here = page >= 0 && page < a.sh.pages;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(head + (here ? page * page_bytes : 0)), 0,
-                                             here ? record : 0, kBufferWord3);
+    const bool here = static_cast<uint32_t>(page) < pages;
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(head + static_cast<uint64_t>(static_cast<uint32_t>(here ? page : 0)) * page_bytes), 0,
+        here ? record : 0, kBufferWord3);
   };
   struct Unit {           // the steps of a unit: their first keys and the pages of their 16-key tiles
     int key[PK], page[2 * PK];
@@ -210,33 +219,36 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int t = x.key[c] + 16 * u;
-          x.page[2 * c + u] = t < sq.ctx ? table[t >> a.sh.shift] : -1;
+          const int page = table[max(min(t, sq.ctx - 1), 0) >> a.sh.shift];
+          x.page[2 * c + u] = t < sq.ctx ? page : -1;
         }
       }
       return x;
     };
     auto issue_keys = [&](const Unit& x, int slot) {
+      const uint32_t dst = mine_at + slot * L::kKSlot;
 #pragma unroll
-      for (int c = 0; c < PK; ++c)
+      for (int i = 0; i < 2 * PK; ++i) {
+        const __amdgpu_buffer_rsrc_t rs = tile_of(x.page[i]);
+        const int place = (x.key[i / 2] + 16 * (i % 2)) & (a.sh.page - 1);
+        if constexpr (D == 64) {
+          if (lane < 32 + 8 * G)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(dst + i * L::kKTile), 16,
+                                                     k_at[0] + place * k_per, 0, 0, 0);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const __amdgpu_buffer_rsrc_t rs = tile_of(x.page[2 * c + u]);
-          const int place = (x.key[c] + 16 * u) & (a.sh.page - 1);
-          const uint32_t dst = mine_at + slot * L::kKSlot + (2 * c + u) * L::kKTile;
-          if constexpr (D == 64) {
-            if (lane < 32 + 8 * G)
-              __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)dst, 16, k_at[0] + place * k_per, 0, 0,
-                                                       0);
-          } else {
-#pragma unroll
-            for (int n = 0; n < L::kCodeLoads; ++n)
-              __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(dst + n * 1024), 16, k_at[n],
-                                                       place * (D / 2), 0, 0);
-            if (lane < 8 * G)
-              __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(dst + 8 * D), 16, p_at, place * 4, 0,
-                                                       0);
-          }
+          for (int n = 0; n < L::kCodeLoads; ++n)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(dst + i * L::kKTile + n * 1024), 16,
+                                                     k_at[n], place * (D / 2), 0, 0);
         }
+      }
+      if (D != 64 && lane < 8 * G) {
+#pragma unroll
+        for (int i = 0; i < 2 * PK; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_of(x.page[i]),
+                                                   (lds_ptr_t)(uintptr_t)(dst + i * L::kKTile + 8 * D), 16, p_at,
+                                                   ((x.key[i / 2] + 16 * (i % 2)) & (a.sh.page - 1)) * 4, 0, 0);
+      }
     };
     auto issue_values = [&](const Unit& x, int slot) {
 #pragma unroll
@@ -367,16 +379,17 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       for (int c = 1; c < PK; ++c) t0 = bank == c ? unit.key[c] : t0;
       int holes = 0;
 #pragma unroll
-      for (int i = 0; i < 2 * PK; ++i) holes |= unit.page[i] < 0 || unit.page[i] >= a.sh.pages ? 1 << i : 0;
+      for (int i = 0; i < 2 * PK; ++i) holes |= static_cast<uint32_t>(unit.page[i]) < pages ? 0 : 1 << i;
       const int first = unit.key[0], end = unit.key[PK - 1] + kStep;
       const bool whole = holes == 0 && end - first == PK * kStep && end - 1 <= pos_lo &&
                          (a.window == 0 || first > pos_hi - a.window || end <= a.sinks);
-      bool stored[8];      // memory past the context may hold anything
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
+      const int mine_missing = holes >> (2 * bank);
+      // memory past the context may hold anything: scales and zero-points of 0
+      auto clean = [&](u32x4& par, int u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          stored[4 * u + i] = whole || (t0 + 16 * u + 4 * kb + i < sq.ctx && !((holes >> (2 * bank + u)) & 1));
+          par[i] = t0 + 16 * u + 4 * kb + i < sq.ctx && !((mine_missing >> u) & 1) ? par[i] : 0u;
+      };
       // ---- scores
       const uint8_t* params = slot + 2 * bank * L::kKTile + 8 * D + 16 * kb;
       f32x4 x[NT][2];
@@ -385,10 +398,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           u32x4 par = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + g * 64);
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) par[i] = stored[4 * u + i] ? par[i] : 0u;
-          }
+          if (!whole) clean(par, u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float sc = kv4_scale(par[i]) * a.scale_log2, z = kv4_zero(par[i]);
@@ -407,7 +417,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
             const int t = t0 + 16 * u + 4 * kb + i;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              const bool seen = stored[4 * u + i] && t <= pos[n] &&
+              const bool seen = !((mine_missing >> u) & 1) && t <= pos[n] &&
                                 (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
               x[n][u][i] = seen ? x[n][u][i] : -INFINITY;
             }
@@ -422,8 +432,8 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
         for (int u = 0; u < 2; ++u)
           par[u] = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + G * 64 + g * 64);
         if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) par[e >> 2][e & 3] = stored[e] ? par[e >> 2][e & 3] : 0u;
+          clean(par[0], 0);
+          clean(par[1], 1);
         }
         f16x2_t top{0, 0};
 #pragma unroll
@@ -435,8 +445,19 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
         }
         most = pk_max(most, top * pair16(shrink[g]));
       }
+      // ---- running maximum and powers of two: one test for both
       bool grow = most[0] > static_cast<_Float16>(1.0f) || most[1] > static_cast<_Float16>(1.0f);
-      if (__any(grow)) {       // some scale passed its 2^e
+      float top[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float t = max3(x[n][0][0], x[n][0][1], x[n][0][2]);
+        t = max3(t, x[n][0][3], x[n][1][0]);
+        t = max3(t, x[n][1][1], x[n][1][2]);
+        t = max3(t, x[n][1][3], x[n][1][3]);
+        top[n] = t;
+        grow |= t > base[n] + 15.0f;
+      }
+      if (__any(grow)) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           f16x2_t t{0, 0};
@@ -454,23 +475,6 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
             for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
           }
         }
-      }
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sv[g][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, sv[g][e]) * pair16(shrink[g]));
-      // ---- running maximum
-      grow = false;
-      float top[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float t = fmaxf(fmaxf(x[n][0][0], x[n][0][1]), fmaxf(x[n][0][2], x[n][0][3]));
-        t = fmaxf(t, fmaxf(fmaxf(x[n][1][0], x[n][1][1]), fmaxf(x[n][1][2], x[n][1][3])));
-        top[n] = t;
-        grow |= t > base[n] + 15.0f;
-      }
-      if (__any(grow)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           // 2^7 at the new maximum; columns that have seen no key stay at -inf
@@ -486,6 +490,11 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           }
         }
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sv[g][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, sv[g][e]) * pair16(shrink[g]));
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float from = base[n] == -INFINITY ? 0.0f : base[n];
@@ -695,8 +704,12 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
   }
 }
 
+// Two blocks a compute unit or more, in ordinary registers alone (in the
+// accumulator form every round copied the sums out and back for the test of
+// the maximum: 35 instead of 25 us for 7 sequences of 32 heads in groups of
+// 32), where the sums (NT D / 16) and a group's products and scales fit 256.
 template <int DT, int D, int GROUP, int PK, int NT, bool WS>
-__global__ __launch_bounds__(256) void attention_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, NT * D + 16 * (D / GROUP) * PK * NT <= 320 ? 2 : 1) void attention_kernel(AttnArgs a) {
   attention_block<DT, D, GROUP, PK, NT, WS>(a);
 }
 

@@ -17,7 +17,7 @@ AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, i
   p.max_q = max_q;
   const int64_t rows = max_q * ratio;
   p.ws = rows <= 64;
-  p.pk = rows <= 4 && D < 256 ? 4 : rows <= 8 ? 2 : 1;
+  p.pk = rows <= 8 ? 2 : 1;
   p.nt = rows <= 16 || D == 256 ? 1 : 2;
   p.rows = 16 / p.pk * p.nt * (p.ws ? 1 : kWaves);
   p.row_tiles = std::min<int64_t>(ceil_div(rows, p.rows), 65535);
@@ -25,11 +25,18 @@ AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, i
   if (window > 0)
     steps = std::min(steps, ceil_div(std::min(window, max_context) + p.rows / ratio + 1, kStep) + 1 +
                                 ceil_div(std::min(sinks, max_context), kStep));
-  const int64_t want = std::max<int64_t>(1, 512 / (seqs * kv_heads * p.row_tiles));
+  // Two blocks a compute unit, and no fewer than 24 steps each: the join of
+  // the chunks is a launch of its own (one sequence of 700 tokens: 13 us whole,
+  // 17 in three), and ragged contexts even out less in larger ones (7 sequences
+  // of up to 2301: 29 us in two chunks, 25 in four; two of 131072: 76 us in
+  // 16, 65 in 32, 73 in 64).
+  const int64_t blocks = seqs * kv_heads * p.row_tiles, fill = 2 * device_cus();
+  const int64_t want = 4 * blocks >= 3 * fill ? 1 : std::max<int64_t>(1, std::min(ceil_div(fill, blocks), steps / 24));
   const int64_t round = p.ws ? kWaves * p.pk : 8;         // steps of a round of the wavefronts, or two of a block
-  p.chunk = ceil_div(ceil_div(steps, want), round) * round;
+  p.chunk = want == 1 ? std::max<int64_t>(steps, 1)
+                      : std::max<int64_t>(1, (ceil_div(steps, want) + round / 2) / round) * round;
   p.splits = std::max<int64_t>(1, ceil_div(steps, p.chunk));
-  p.blocks = seqs * kv_heads * p.row_tiles * p.splits;
+  p.blocks = blocks * p.splits;
   return p;
 }
 

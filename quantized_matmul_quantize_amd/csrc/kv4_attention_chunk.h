@@ -40,13 +40,6 @@ struct Chunk {
 // are mapped so that any 16 lanes write 16 different rows: no bank conflicts.
 __device__ __forceinline__ int op_at(int r, int kb) { return 16 * (16 * kb + r); }
 
-// The compiler's maximum quiets each operand first; these are products already.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
-  return d;
-}
-
 template <int DT, int D, int GROUP, int NT>
 __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   using L = Chunk<D, GROUP, NT>;
@@ -71,7 +64,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   const int rows = sq.n * a.ratio;
   const int tiles = (rows + L::kRows - 1) / L::kRows;
   const int record = static_cast<int>(a.sh.record_bytes());
-  const int64_t page_bytes = static_cast<int64_t>(a.sh.heads) * record;
+  const uint32_t page_bytes = static_cast<uint32_t>(a.sh.heads) * static_cast<uint32_t>(record);
+  const uint32_t pages = static_cast<uint32_t>(a.sh.pages);
   const uint8_t* head = a.cache + static_cast<int64_t>(kvh) * record;
   typedef const __attribute__((address_space(4))) int32_t* table_t;
   const table_t table = (table_t)(a.table + b * a.table_stride);
@@ -170,7 +164,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int t = x.key[c] + 16 * u;
-          x.page[2 * c + u] = t < sq.ctx ? table[t >> a.sh.shift] : -1;
+          const int page = table[max(min(t, sq.ctx - 1), 0) >> a.sh.shift];
+          x.page[2 * c + u] = t < sq.ctx ? page : -1;
         }
       }
       return x;
@@ -178,7 +173,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     auto holes_of = [&](const Round& x) {
       int h = 0;
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) h |= x.page[t] < 0 || x.page[t] >= a.sh.pages ? 1 << t : 0;
+      for (int t = 0; t < kTiles; ++t) h |= static_cast<uint32_t>(x.page[t]) < pages ? 0 : 1 << t;
       return h;
     };
     auto fetch = [&](const Round& x) {
@@ -197,9 +192,10 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
             t0 = tile_n == t ? x.key[t / 2] + 16 * (t % 2) : t0;
           }
           if (D != 64 || (lane >> 5) == pass) {
-            const bool here = page >= 0 && page < a.sh.pages;
+            const bool here = static_cast<uint32_t>(page) < pages;
             const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<uint8_t*>(head + (here ? page * page_bytes : 0)), 0, here ? record : 0, kBufferWord3);
+                const_cast<uint8_t*>(head + static_cast<uint64_t>(static_cast<uint32_t>(here ? page : 0)) * page_bytes),
+                0, here ? record : 0, kBufferWord3);
             const int place = t0 & (a.sh.page - 1);
             raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                    rs, raw_at + (values ? 0 : 16 * k_piece[i]), place * (D / 2), 0));

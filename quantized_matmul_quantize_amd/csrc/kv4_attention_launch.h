@@ -17,8 +17,6 @@ void launch_shape(const AttnArgs& a, AttnPlan& p, hipStream_t s) {
   }
   if (!p.ws) {
     attention_chunk_kernel<DT, D, GROUP, kMost><<<grid, 256, 0, s>>>(a);
-  } else if (p.pk == 4) {
-    if constexpr (D < 256) attention_kernel<DT, D, GROUP, 4, 1, true><<<grid, 256, 0, s>>>(a);
   } else if (p.pk == 2) {
     if constexpr (D < 256 || GROUP > 32) attention_kernel<DT, D, GROUP, 2, 1, true><<<grid, 256, 0, s>>>(a);
   } else if (p.nt == 1) {

@@ -26,7 +26,7 @@ inline int kv4_shape(int64_t pages, int64_t heads, int64_t D, int64_t page, int 
   if (D != 64 && D != 128 && D != 256) return QMM_EUNSUPPORTED;
   if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256) return QMM_EUNSUPPORTED;
   if ((group != 32 && group != 64 && group != 128) || D % group != 0) return QMM_EUNSUPPORTED;
-  // page ids travel as int32; byte offsets are 64-bit
+  // page ids travel as int32, in unsigned comparisons; byte offsets are 64-bit
   if (heads > 4096 || pages >= (int64_t{1} << 31)) return QMM_ERANGE;
   *s = Kv4Shape{pages, static_cast<int32_t>(heads), static_cast<int32_t>(D), static_cast<int32_t>(page), group,
                 __builtin_ctz(static_cast<unsigned>(page))};
