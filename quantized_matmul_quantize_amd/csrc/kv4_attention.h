@@ -16,18 +16,19 @@
 //                 leave their lane, and the running statistics of column r
 //                 belong to the lanes that hold column r of O^T.
 //
-// The codes enter the matrix cores as they are, as the 16-bit floats off + c
-// (128 + c where q is bf16, 64 + c where it is binary16), exactly; offset,
-// zero-point and scale are applied around the products:
-//   x[t] = sum_g s[t,g] ((sum_{d in g} q_d (off + c)) - (off + z[t,g]) sum_{d in g} q_d)
+// The codes enter the matrix cores as they are, as the binary16 numbers
+// off + c, exactly; offset, zero-point and scale are applied around the products:
+//   x[t] = sum_g s[t,g] ((sum_{d in g} q_d (16 + c)) - (16 + z[t,g]) sum_{d in g} q_d)
 //   o[d] = 2^e[g] (sum_t p'[t] (64 + c) - sum_t p'[t] (64 + z[t,g])),  p' = p s[t,g] 2^-e[g]
-// with the second sum of o one more product whose first operand is 64 + z.
-// p and p' are rounded to binary16 (2^-12 each; both sums see the same p'), for
-// either type of q: bf16 would cost 2^-9.  Its range is kept by the two powers
-// of two that are moved only when they must be: p lies below 2^15 (and reaches
-// 2^7 where the maximum was last moved, so that what is lost below 2^-25 is
-// 2^-32 of the largest), s 2^-e below 1.  The scores, maxima and sums of p
-// stay in fp32.
+// with the second sum of o one more product whose first operand is 64 + z.  (An
+// offset of 64 takes one shift a word less than 16, but its rounding is the
+// scores' largest error; bf16 operands would need 128.)  bf16 queries are first
+// scaled by a power of two, their largest to 2^14 .. 2^15: exact but for what
+// lies 2^38 below it.  p' is rounded to binary16 (2^-12) for either type of q:
+// bf16 would cost 2^-9.  Its range is kept by the two powers of two that are
+// moved only when they must be: p lies below 2^15 (and reaches 2^7 where the
+// maximum was last moved, so that what is lost below 2^-25 is 2^-32 of the
+// largest), s 2^-e below 1.  The scores, maxima and sums of p stay in fp32.
 //
 // What bounds decode is the vector unit, not the matrix cores: two operations
 // a pair of codes to make operands of them, and then the arithmetic on the
@@ -44,21 +45,10 @@
 namespace qmm {
 namespace {
 
-template <int DT>
-struct Codes;        // eight codes of a word as four pairs of 16-bit floats
-template <>
-struct Codes<QMM_BF16> {
-  static constexpr float offset = 128.0f;
-  static constexpr uint32_t magic = 0x43004300u;
-  static __device__ __forceinline__ void unpack(uint32_t w, uint32_t m, uint32_t p[4]) {
-    Int4Magic<QMM_BF16>::unpack(w, m, p);
-  }
-};
-// Bits 4-7 of 0x5400 (64.0) are worth 1: one of the four pairs needs no shift
-// (16 + c, nibbles at bits 6-9, needs four).
-template <>
-struct Codes<QMM_F16> {
-  static constexpr float offset = 64.0f;
+// Eight codes of a word as four pairs 64 + c: bits 4-7 of 0x5400 (64.0) are
+// worth 1, so one of the pairs needs no shift.  (16 + c, nibbles at bits 6-9:
+// Int4Magic<QMM_F16>.)
+struct Codes64 {
   static constexpr uint32_t magic = 0x54005400u;
   static constexpr uint32_t mask = 0x00F000F0u;
   template <int N>
@@ -73,14 +63,42 @@ struct Codes<QMM_F16> {
   }
 };
 
-template <int DT>
+// Queries as second operands.  The power of two that takes the largest of them
+// to 2^14 .. 2^15 (held to normal numbers), and its inverse.
+struct QueryScale {
+  float down, up;
+};
+template <int N>
+__device__ __forceinline__ float largest_bf16(const u32x4 (&q)[N], float most) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      most = fmaxf(most, fmaxf(fabsf(bf16lo_to_f32(q[j][w])), fabsf(bf16hi_to_f32(q[j][w]))));
+  return most;
+}
+__device__ __forceinline__ QueryScale query_scale(float most) {
+  const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 27), 254);
+  return {__uint_as_float(static_cast<uint32_t>(268 - e) << 23), __uint_as_float(static_cast<uint32_t>(e - 14) << 23)};
+}
+template <int N>
+__device__ __forceinline__ void to_f16(u32x4 (&q)[N], float down) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      q[j][w] = pack_pair<QMM_F16>(bf16lo_to_f32(q[j][w]) * down, bf16hi_to_f32(q[j][w]) * down);
+}
+
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
-  if constexpr (DT == QMM_BF16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
-                                                   0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
-                                                  0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0,
+                                                0);
+}
+// p s of a pair of keys, each rounded once
+__device__ __forceinline__ uint32_t weighted(float p0, float p1, f16x2_t s) {
+  const f16x2_t w{static_cast<_Float16>(p0 * static_cast<float>(s[0])),
+                  static_cast<_Float16>(p1 * static_cast<float>(s[1]))};
+  return __builtin_bit_cast(uint32_t, w);
 }
 
 __device__ __forceinline__ float max_over_quads(float v) {
@@ -144,7 +162,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
   static_assert(PK == 1 || (WS && NT == 1), "steps are taken together for few rows only");
   using L = Shape<D, GROUP, PK, NT, WS>;
   constexpr int G = L::kG, MT = L::kMTiles, kSteps = L::kSteps;
-  constexpr float kOff = Codes<DT>::offset;
+  constexpr float kOff = Int4Magic<QMM_F16>::offset;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * L::kWaveBytes];
 
   const int lane = threadIdx.x & (kWave - 1);
@@ -290,18 +308,28 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * kb;
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
+    }
+    float key_scale = a.scale_log2;
+    if constexpr (DT == QMM_BF16) {
+      float most = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) most = largest_bf16(qv[n], most);
+      const QueryScale qs = query_scale(wave_max(most));
+      key_scale *= qs.up;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) to_f16(qv[n], qs.down);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float s = 0.0f;
 #pragma unroll
         for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j)
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            s += DT == QMM_BF16 ? bf16lo_to_f32(qv[n][j][w]) + bf16hi_to_f32(qv[n][j][w])
-                                : f16lo_to_f32(qv[n][j][w]) + f16hi_to_f32(qv[n][j][w]);
+          for (int w = 0; w < 4; ++w) s += f16lo_to_f32(qv[n][j][w]) + f16hi_to_f32(qv[n][j][w]);
         qsum[n][g] = sum_over_quads(s);
       }
-    }
 
     f32x4 o[NT][G][MT], corr[NT][G];
     // p = 2^(x - base); base is -inf until a key is seen, then at least 2^-15
@@ -321,10 +349,10 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
         for (int x = 0; x < MT; ++x) o[n][g][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
     }
-    const uint32_t magic_q = vgpr_const(Codes<DT>::magic);
-    const uint32_t magic_v = vgpr_const(Codes<QMM_F16>::magic);
+    const uint32_t magic_q = vgpr_const(Int4Magic<QMM_F16>::kMagic);
+    const uint32_t magic_v = vgpr_const(Codes64::magic);
 
-    f16x2_t p[NT][4];              // probabilities of a unit, and the pairs of scales and zero-points of its values
+    float p[NT][8];                // probabilities of a unit, and the pairs of scales and zero-points of its values
     uint32_t sv[G][4], zv[G][4];
 
     auto scores = [&](int s, const Unit& unit, int slot_n) {
@@ -363,9 +391,9 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 #pragma unroll
             for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j) {
               uint32_t av[4];
-              Codes<DT>::unpack(w[j], magic_q, av);
+              Int4Magic<QMM_F16>::unpack(w[j], magic_q, av);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) acc[n] = mfma<DT>(u32x4{av[0], av[1], av[2], av[3]}, qv[n][j], acc[n]);
+              for (int n = 0; n < NT; ++n) acc[n] = mfma(u32x4{av[0], av[1], av[2], av[3]}, qv[n][j], acc[n]);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -401,7 +429,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           if (!whole) clean(par, u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float sc = kv4_scale(par[i]) * a.scale_log2, z = kv4_zero(par[i]);
+            const float sc = kv4_scale(par[i]) * key_scale, z = kv4_zero(par[i]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const float v = fmaf(-z, qsum[n][g], prod[n][g][u][i]);
@@ -500,10 +528,9 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
         const float from = base[n] == -INFINITY ? 0.0f : base[n];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float p0 = exp2_fast(x[n][e >> 1][2 * (e & 1)] - from);
-          const float p1 = exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - from);
-          l[n] += p0 + p1;
-          p[n][e] = f16x2_t{static_cast<_Float16>(p0), static_cast<_Float16>(p1)};
+          p[n][2 * e] = exp2_fast(x[n][e >> 1][2 * (e & 1)] - from);
+          p[n][2 * e + 1] = exp2_fast(x[n][e >> 1][2 * (e & 1) + 1] - from);
+          l[n] += p[n][2 * e] + p[n][2 * e + 1];
         }
       }
     };
@@ -517,10 +544,10 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            pv[n][e] = __builtin_bit_cast(uint32_t, p[n][e] * __builtin_bit_cast(f16x2_t, sv[g][e]));
+            pv[n][e] = weighted(p[n][2 * e], p[n][2 * e + 1], __builtin_bit_cast(f16x2_t, sv[g][e]));
           // row m of the first operand holds the zero-points of m's own step,
           // so column r finds its sum where 4 kb + i belongs to r's step
-          corr[n][g] = mfma<QMM_F16>(u32x4{zv[g][0], zv[g][1], zv[g][2], zv[g][3]}, pv[n], corr[n][g]);
+          corr[n][g] = mfma(u32x4{zv[g][0], zv[g][1], zv[g][2], zv[g][3]}, pv[n], corr[n][g]);
         }
 #pragma unroll
         for (int c = 0; c < PK; ++c) {
@@ -550,10 +577,10 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
               u32x4 av;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                av[e] = ((y == 0 ? unit[e] << 4 : unit[e] >> (4 * y - 4)) & Codes<QMM_F16>::mask) | magic_v;
+                av[e] = ((y == 0 ? unit[e] << 4 : unit[e] >> (4 * y - 4)) & Codes64::mask) | magic_v;
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                o[n][g][part * (MT / kParts) + y] = mfma<QMM_F16>(av, pc[n], o[n][g][part * (MT / kParts) + y]);
+                o[n][g][part * (MT / kParts) + y] = mfma(av, pc[n], o[n][g][part * (MT / kParts) + y]);
             }
           }
         }

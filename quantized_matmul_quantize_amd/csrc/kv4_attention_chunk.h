@@ -10,9 +10,7 @@
 // key's scale (with the running base in the same operation where a head is one
 // group), the exponential, a conversion and half a packed product with the
 // value's scale; the sums of the probabilities come from the matrix cores too.
-// q is binary16 here: bf16 queries are first scaled by a power of two per
-// block (their largest to 2^14 .. 2^15), exactly but for what lies 2^38 below
-// the largest.
+// (The power of two of bf16 queries is the block's.)
 #pragma once
 
 #include "kv4_attention.h"
@@ -116,14 +114,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       pos[n] = live ? sq.first + tok : -1;
       const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * kb;
 #pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
-        if constexpr (DT == QMM_BF16) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            most = fmaxf(most, fmaxf(fabsf(bf16lo_to_f32(qv[n][j][w])), fabsf(bf16hi_to_f32(qv[n][j][w]))));
-        }
-      }
+      for (int j = 0; j < kSteps; ++j) qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
+      if constexpr (DT == QMM_BF16) most = largest_bf16(qv[n], most);
     }
     float unscale = 1.0f;
     __syncthreads();                               // LDS is free: the rows before are done
@@ -132,19 +124,11 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       most = wave_max(most);
       if (lane == 0) stat[wave] = most;
       __syncthreads();
-      most = fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3]));
+      const QueryScale qs = query_scale(fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3])));
       __syncthreads();
-      // 2^(14 - exponent) of the largest, held to normal numbers
-      const int e = min(max(static_cast<int>(__float_as_uint(most) >> 23), 27), 254);
-      const float down = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-      unscale = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+      unscale = qs.up;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            qv[n][j][w] = pack_pair<QMM_F16>(bf16lo_to_f32(qv[n][j][w]) * down, bf16hi_to_f32(qv[n][j][w]) * down);
+      for (int n = 0; n < NT; ++n) to_f16(qv[n], qs.down);
     }
     const float key_scale = a.scale_log2 * unscale;
 
@@ -224,7 +208,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         for (int g = 0; g < G; ++g) kpar[i][g] = key < sq.ctx ? kpar[i][g] : 0u;
       }
     };
-    const uint32_t magic = vgpr_const(Codes<QMM_F16>::magic);
+    const uint32_t magic = vgpr_const(Codes64::magic);
     auto less = [](uint32_t p, uint32_t z) {       // pairs: (64 + c) + -(64 + z)
       return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, p) + __builtin_bit_cast(f16x2_t, z));
     };
@@ -241,7 +225,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
             for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? kpar[i][g] : par;
             const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
             uint32_t p[4];
-            Codes<QMM_F16>::unpack(raw[i][x], magic, p);
+            Codes64::unpack(raw[i][x], magic, p);
             *reinterpret_cast<u32x4*>(buf + (my_tile[i] * kSteps + j) * 1024 + op_at(r, (first + x) / kSteps)) =
                 u32x4{less(p[0], z), less(p[1], z), less(p[2], z), less(p[3], z)};
           }
@@ -270,7 +254,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
             u32x4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              v[e] = less(((y == 0 ? w[e] << 4 : w[e] >> (4 * y - 4)) & Codes<QMM_F16>::mask) | magic, z[e]);
+              v[e] = less(((y == 0 ? w[e] << 4 : w[e] >> (4 * y - 4)) & Codes64::mask) | magic, z[e]);
             const int row = 8 * (v_word & 1) + 2 * y + part;
             *reinterpret_cast<u32x4*>(buf + L::kVAt + (v_step * (D / 16) + v_word / 2) * L::kVStride +
                                       op_at(row, v_quad)) = v;
@@ -318,7 +302,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j) {
             const u32x4 k = *reinterpret_cast<const u32x4*>(buf + ((2 * c0 + u) * kSteps + j) * 1024 + op_at(r, kb));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n] = mfma<QMM_F16>(k, qv[n][j], acc[n]);
+            for (int n = 0; n < NT; ++n) acc[n] = mfma(k, qv[n][j], acc[n]);
           }
           const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + 32 * c0 + 16 * u + 4 * kb) * 4);
 #pragma unroll
@@ -411,7 +395,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       }
 #pragma unroll
       for (int c = 0; c < U; ++c) {
-        f16x2_t p[NT][4];
+        float p[NT][8];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float from = base[n] == -INFINITY ? 0.0f : base[n];
@@ -419,11 +403,11 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const f32x4& xs = x[n][2 * c + (e >> 1)];
-            p[n][e] = f16x2_t{static_cast<_Float16>(exp2_fast(xs[2 * (e & 1)] - from)),
-                              static_cast<_Float16>(exp2_fast(xs[2 * (e & 1) + 1] - from))};
-            pw[e] = __builtin_bit_cast(uint32_t, p[n][e]);
+            p[n][2 * e] = exp2_fast(xs[2 * (e & 1)] - from);
+            p[n][2 * e + 1] = exp2_fast(xs[2 * (e & 1) + 1] - from);
+            pw[e] = pack_pair<QMM_F16>(p[n][2 * e], p[n][2 * e + 1]);
           }
-          l[n] = mfma<QMM_F16>(ones, pw, l[n]);
+          l[n] = mfma(ones, pw, l[n]);
         }
         // ---- values
 #pragma unroll
@@ -433,14 +417,14 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           for (int e = 0; e < 4; ++e) {
             const f16x2_t s2 = sv[g][4 * c + e] * pair16(shrink[g]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) pv[n][e] = __builtin_bit_cast(uint32_t, p[n][e] * s2);
+            for (int n = 0; n < NT; ++n) pv[n][e] = weighted(p[n][2 * e], p[n][2 * e + 1], s2);
           }
 #pragma unroll
           for (int y = 0; y < MT; ++y) {
             const u32x4 v = *reinterpret_cast<const u32x4*>(
                 buf + L::kVAt + ((c0 + c) * (D / 16) + g * MT + y) * L::kVStride + op_at(r, kb));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[n][g][y] = mfma<QMM_F16>(v, pv[n], o[n][g][y]);
+            for (int n = 0; n < NT; ++n) o[n][g][y] = mfma(v, pv[n], o[n][g][y]);
           }
         }
       }
