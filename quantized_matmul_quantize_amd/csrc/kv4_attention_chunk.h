@@ -22,16 +22,18 @@ template <int D, int GROUP, int NT>
 struct Chunk {
   static constexpr int kG = D / GROUP;
   static constexpr int kRows = 16 * NT * kWaves;
-  static constexpr int kKeys = 8192 / D;                    // of a round: two 16-byte pieces of codes a producing lane
+  static constexpr int kKeys = D == 256 ? 32 : 64;          // of a round
   static constexpr int kSteps = D / 32;
-  // operands of 1 KiB: [16-key tile][k-extent] of keys, [step][16 channels] of values
+  // operands of 1 KiB: [16-key tile][k-extent] of keys, [step][16 channels] of values; two buffers of each
   static constexpr int kKOps = kKeys / 16 * kSteps, kVOps = kKeys / kStep * (D / 16);
   static constexpr int kVStride = 1024 + 80;                // a value's eight channels go to 16 operand rows: no bank twice
-  static constexpr int kVAt = kKOps * 1024;
-  static constexpr int kKScales = kVAt + kVOps * kVStride;  // fp32 [group][key]
-  static constexpr int kVScales = kKScales + kG * kKeys * 4;  // binary16 [group][key]
-  static constexpr int kBuffer = kVScales + kG * kKeys * 2;
-  static_assert(kBuffer % 16 == 0, "alignment");
+  static constexpr int kKScales = kKOps * 1024;             // fp32 [group][key]
+  static constexpr int kKBuffer = kKScales + kG * kKeys * 4;
+  static constexpr int kVScales = kVOps * kVStride;         // binary16 [group][key]
+  static constexpr int kVBuffer = kVScales + kG * kKeys * 2;
+  static_assert(kKBuffer % 16 == 0 && kVBuffer % 16 == 0, "alignment");
+  // what a producing lane expands: words of a key's codes, and pairs of channels' nibbles of a word of values
+  static constexpr int kWords = kKeys * D / 8 / 256, kNibbles = kKeys * D / 8 / 256;
 };
 
 // Lane (r, kb) finds its 16 bytes of an operand in lane order, and producers
@@ -42,11 +44,11 @@ template <int DT, int D, int GROUP, int NT>
 __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   using L = Chunk<D, GROUP, NT>;
   constexpr int G = L::kG, MT = GROUP / 16, KEYS = L::kKeys, kSteps = L::kSteps;
-  constexpr int kPer = KEYS / kStep;               // steps of a round
-  constexpr int kPieces = D / 32;                  // 16-byte pieces of a key
+  constexpr int U = KEYS / kStep;                  // steps of a round
   constexpr int kTiles = KEYS / 16;                // 16-key tiles of a round
-  constexpr int U = kPer < 2 ? 1 : 2;              // steps whose scores are taken together
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][L::kBuffer];
+  constexpr int kWords = L::kWords;
+  __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][L::kKBuffer];
+  __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][L::kVBuffer];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
@@ -68,26 +70,20 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   typedef const __attribute__((address_space(4))) int32_t* table_t;
   const table_t table = (table_t)(a.table + b * a.table_stride);
 
-  // Producers: wavefronts 0 and 1 keys, 2 and 3 values.  Of a round a lane
-  // takes two pieces of 16 bytes: of keys the lane's (lane & 15) in one or two
-  // 16-key tiles, or of both tiles of a step the same word of the same quad of
-  // keys.
-  const bool values = wave >= 2;
-  const int half = wave & 1;
-  const int unit = 64 * half + lane;
-  const int v_word = unit % (D / 8), v_quad = unit / (D / 8) % 4, v_step = unit / (D / 2);
+  // What a lane expands of a round.  Keys: kWords words of key r of a 16-key
+  // tile (the wavefront's; D 256: two wavefronts a tile).  Values: of one word
+  // of both quads `v_quad` of a step, half of the channels (`part`; D 64: a
+  // quarter).
+  const int k_tile = D == 256 ? wave >> 1 : wave;
+  const int k_piece = D == 256 ? 4 * (wave & 1) + kb : kb;          // of 4 kWords bytes
+  const int v_unit = D == 256 ? 64 * (wave >> 1) + lane : lane;
+  const int v_word = v_unit % (D / 8), v_quad = v_unit / (D / 8) % 4;
+  const int v_step = D == 64 ? lane >> 5 : D == 128 ? wave >> 1 : 0;
+  const int part = wave & 1, v_first = D == 64 ? 2 * (wave >> 1) : 0;   // first of its nibbles of a half word
   const int v_group = v_word / (GROUP / 8);
-  int k_piece[2], my_tile[2];                      // my_tile: the 16-key tile of a piece
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = 4 * (2 * i + half) + (lane >> 4);
-    k_piece[i] = m % kPieces;
-    my_tile[i] = values ? 2 * v_step + i : m / kPieces;
-  }
-  const int first_key = values ? 4 * v_quad : r;   // of the lane's in a tile
-  // byte offsets in a record: at + place * per (codes), params likewise
-  const int raw_at = values ? a.sh.page * (D / 2) + 16 * v_word + v_quad * (2 * D) : r * (D / 2);
-  const int par_at = values ? a.sh.page * (D + 4 * G) + v_group * a.sh.page * 4 + 16 * v_quad : a.sh.page * D + 4 * r;
+  const int k_at = r * (D / 2) + 4 * kWords * k_piece, kp_at = a.sh.page * D + 4 * r;
+  const int v_at = a.sh.page * (D / 2) + 16 * v_word + v_quad * (2 * D);
+  const int vp_at = a.sh.page * (D + 4 * G) + v_group * a.sh.page * 4 + 16 * v_quad;
 
   // the last tiles see the most keys and go first
   for (int tile = tiles - 1 - order; tile >= 0; tile -= a.row_tiles) {
@@ -96,7 +92,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     const int chunks = max(1, (st.count + a.chunk - 1) / a.chunk);
     if (split >= chunks) continue;
     const int s_lo = split * a.chunk, s_hi = min(s_lo + a.chunk, st.count);
-    const int rounds = (s_hi - s_lo + kPer - 1) / kPer;
+    const int rounds = (s_hi - s_lo + U - 1) / U;
     const int row_lo = tile * L::kRows + wave * 16 * NT;
     const int row_hi = min(row_lo + 16 * NT, rows) - 1;
     const int pos_lo = sq.first + row_lo / a.ratio;
@@ -120,7 +116,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     float unscale = 1.0f;
     __syncthreads();                               // LDS is free: the rows before are done
     if constexpr (DT == QMM_BF16) {
-      float* stat = reinterpret_cast<float*>(&lds[0][0]);
+      float* stat = reinterpret_cast<float*>(&k_lds[0][0]);
       most = wave_max(most);
       if (lane == 0) stat[wave] = most;
       __syncthreads();
@@ -132,18 +128,15 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     }
     const float key_scale = a.scale_log2 * unscale;
 
-    // ---- producers
-    u32x4 raw[2];
-    uint32_t kpar[2][G];                           // keys: params of the two pieces' keys
-    u32x4 vpar[2];                                 // values: params of the two quads' keys
-    struct Round {                                 // first keys of its steps, pages of its tiles
-      int key[kPer], page[kTiles];
+    // ---- rounds: first keys of their steps, pages of their tiles
+    struct Round {
+      int key[U], page[kTiles];
     };
     auto round_of = [&](int round) {
       Round x;
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        const int at = s_lo + round * kPer + c;
+      for (int c = 0; c < U; ++c) {
+        const int at = s_lo + round * U + c;
         x.key[c] = at < s_hi ? st.key(at) : kBeyond;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -160,113 +153,123 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       for (int t = 0; t < kTiles; ++t) h |= static_cast<uint32_t>(x.page[t]) < pages ? 0 : 1 << t;
       return h;
     };
-    auto fetch = [&](const Round& x) {
+    // A 16-key tile past the context, or whose page is not of this cache, is
+    // read through an empty resource: zeros, so scales of 0.
+    auto tile_of = [&](int page) {
+      const bool here = static_cast<uint32_t>(page) < pages;
+      return __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(head + static_cast<uint64_t>(static_cast<uint32_t>(here ? page : 0)) * page_bytes), 0,
+          here ? record : 0, kBufferWord3);
+    };
+    // ---- producers
+    uint32_t k_raw[kWords], k_par[G];
+    u32x4 v_raw[2], v_par[2];
+    // first key of the wavefront's tile of keys, and its page
+    struct Mine {
+      int key, page;
+    };
+    auto mine_of = [&](int round) {
+      const int at = s_lo + round * U + (U == 1 ? 0 : k_tile >> 1);
+      Mine x;
+      x.key = (at < s_hi ? st.key(at) : kBeyond) + 16 * (k_tile & 1);
+      const int page = table[max(min(x.key, sq.ctx - 1), 0) >> a.sh.shift];
+      x.page = x.key < sq.ctx ? page : -1;
+      return x;
+    };
+    auto fetch_keys = [&](Mine x) {
+      const int t0 = x.key;
+      const __amdgpu_buffer_rsrc_t rs = tile_of(x.page);
+      const int place = t0 & (a.sh.page - 1);
+      if constexpr (kWords == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, k_at, place * (D / 2), 0));
+        k_raw[0] = v.x;
+        k_raw[1] = v.y;
+      } else {
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, k_at, place * (D / 2), 0));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // D 128 and 256: the tile is the wavefront's; D 64: two tiles of 32 lanes each, with a part of the lanes each
-        constexpr int kPasses = D == 64 ? 2 : 1;
-#pragma unroll
-        for (int pass = 0; pass < kPasses; ++pass) {
-          const int tile_n = D == 64 ? (values ? 4 * half + 2 * pass + i : 2 * (2 * i + half) + pass)
-                             : D == 128 ? (values ? 2 * half + i : 2 * i + half) : i;
-          int page = x.page[0], t0 = x.key[0];
-#pragma unroll
-          for (int t = 1; t < kTiles; ++t) {
-            page = tile_n == t ? x.page[t] : page;
-            t0 = tile_n == t ? x.key[t / 2] + 16 * (t % 2) : t0;
-          }
-          if (D != 64 || (lane >> 5) == pass) {
-            const bool here = static_cast<uint32_t>(page) < pages;
-            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<uint8_t*>(head + static_cast<uint64_t>(static_cast<uint32_t>(here ? page : 0)) * page_bytes),
-                0, here ? record : 0, kBufferWord3);
-            const int place = t0 & (a.sh.page - 1);
-            raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                   rs, raw_at + (values ? 0 : 16 * k_piece[i]), place * (D / 2), 0));
-            if (values) {
-              vpar[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, par_at, place * 4, 0));
-            } else {
-#pragma unroll
-              for (int g = 0; g < G; ++g)
-                kpar[i][g] = __builtin_amdgcn_raw_buffer_load_b32(rs, par_at + g * a.sh.page * 4, place * 4, 0);
-            }
-          }
-        }
+        for (int w = 0; w < 4; ++w) k_raw[w] = v[w];
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        k_par[g] = __builtin_amdgcn_raw_buffer_load_b32(rs, kp_at + g * a.sh.page * 4, place * 4, 0);
     };
     // Memory past the context may hold anything: its scales and zero-points are taken as 0.
-    auto clean = [&](const Round& x) {
+    auto clean_keys = [&](Mine x) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int t0 = x.key[0];
+      for (int g = 0; g < G; ++g) k_par[g] = x.key + r < sq.ctx ? k_par[g] : 0u;
+    };
+    auto fetch_values = [&](const Round& x) {
 #pragma unroll
-        for (int t = 1; t < kTiles; ++t) t0 = my_tile[i] == t ? x.key[t / 2] + 16 * (t % 2) : t0;
-        const int key = t0 + first_key;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vpar[i][e] = key + e < sq.ctx ? vpar[i][e] : 0u;
+        for (int c = 0; c < U; ++c) {
+          // D 128: the wavefront's step; D 64: the steps of its halves
+          if (D == 64 ? v_step == c : U == 1 || v_step == c) {
+            const __amdgpu_buffer_rsrc_t rs = tile_of(x.page[2 * c + i]);
+            const int place = (x.key[c] + 16 * i) & (a.sh.page - 1);
+            v_raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, v_at, place * (D / 2), 0));
+            v_par[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, vp_at, place * 4, 0));
+          }
+        }
+    };
+    auto clean_values = [&](const Round& x) {
+      int t0 = x.key[0];
 #pragma unroll
-        for (int g = 0; g < G; ++g) kpar[i][g] = key < sq.ctx ? kpar[i][g] : 0u;
-      }
+      for (int c = 1; c < U; ++c) t0 = v_step == c ? x.key[c] : t0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v_par[i][e] = t0 + 16 * i + 4 * v_quad + e < sq.ctx ? v_par[i][e] : 0u;
     };
     const uint32_t magic = vgpr_const(Codes64::magic);
     auto less = [](uint32_t p, uint32_t z) {       // pairs: (64 + c) + -(64 + z)
       return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, p) + __builtin_bit_cast(f16x2_t, z));
     };
-    auto expand = [&](uint8_t* buf) {
-      if (!values) {
+    auto expand_keys = [&](uint8_t* buf) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int first = 4 * k_piece[i];
+      for (int w = 0; w < kWords; ++w) {
+        const int word = kWords * k_piece + w;     // k-extent j of lane quarter kb is word kSteps kb + j
+        const int j = kWords == 2 ? w : kSteps == 4 ? w : word % kSteps;
+        uint32_t par = k_par[0];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int j = (first + x) % kSteps;    // the word's k-extent and eight channels of it
-            uint32_t par = kpar[i][0];
+        for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? k_par[g] : par;
+        const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
+        uint32_t p[4];
+        Codes64::unpack(k_raw[w], magic, p);
+        *reinterpret_cast<u32x4*>(buf + (k_tile * kSteps + j) * 1024 + op_at(r, word / kSteps)) =
+            u32x4{less(p[0], z), less(p[1], z), less(p[2], z), less(p[3], z)};
+      }
+      if (k_piece == 0) {
 #pragma unroll
-            for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? kpar[i][g] : par;
-            const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
-            uint32_t p[4];
-            Codes64::unpack(raw[i][x], magic, p);
-            *reinterpret_cast<u32x4*>(buf + (my_tile[i] * kSteps + j) * 1024 + op_at(r, (first + x) / kSteps)) =
-                u32x4{less(p[0], z), less(p[1], z), less(p[2], z), less(p[3], z)};
-          }
-          if (k_piece[i] == 0) {
+        for (int g = 0; g < G; ++g)
+          *reinterpret_cast<float*>(buf + L::kKScales + (g * KEYS + 16 * k_tile + r) * 4) =
+              kv4_scale(k_par[g]) * key_scale;
+      }
+    };
+    auto expand_values = [&](uint8_t* buf) {
+      uint32_t z[4], w[4];
+      const uint32_t sel = part ? 0x07060302u : 0x05040100u;
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-              *reinterpret_cast<float*>(buf + L::kKScales + (g * KEYS + 16 * my_tile[i] + r) * 4) =
-                  kv4_scale(kpar[i][g]) * key_scale;
-          }
-        }
-      } else {
-        uint32_t z[4];
+      for (int e = 0; e < 4; ++e) {
+        z[e] = (__builtin_amdgcn_perm(v_par[e >> 1][2 * (e & 1) + 1], v_par[e >> 1][2 * (e & 1)], 0x0c060c02u) << 4 &
+                0x00F000F0u) | 0xD400D400u;
+        w[e] = __builtin_amdgcn_perm(v_raw[e >> 1][2 * (e & 1) + 1], v_raw[e >> 1][2 * (e & 1)], sel) >> (4 * v_first);
+      }
+#pragma unroll
+      for (int y = 0; y < L::kNibbles; ++y) {
+        u32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          z[e] = (__builtin_amdgcn_perm(vpar[e >> 1][2 * (e & 1) + 1], vpar[e >> 1][2 * (e & 1)], 0x0c060c02u) << 4 &
-                  0x00F000F0u) | 0xD400D400u;
+          v[e] = less(((y == 0 ? w[e] << 4 : w[e] >> (4 * y - 4)) & Codes64::mask) | magic, z[e]);
+        const int row = 8 * (v_word & 1) + 2 * (v_first + y) + part;
+        *reinterpret_cast<u32x4*>(buf + (v_step * (D / 16) + v_word / 2) * L::kVStride + op_at(row, v_quad)) = v;
+      }
+      if (part == 0 && v_first == 0 && v_word % (GROUP / 8) == 0) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = __builtin_amdgcn_perm(raw[e >> 1][2 * (e & 1) + 1], raw[e >> 1][2 * (e & 1)],
-                                         part ? 0x07060302u : 0x05040100u);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            u32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = less(((y == 0 ? w[e] << 4 : w[e] >> (4 * y - 4)) & Codes64::mask) | magic, z[e]);
-            const int row = 8 * (v_word & 1) + 2 * y + part;
-            *reinterpret_cast<u32x4*>(buf + L::kVAt + (v_step * (D / 16) + v_word / 2) * L::kVStride +
-                                      op_at(row, v_quad)) = v;
-          }
-        }
-        if (v_word % (GROUP / 8) == 0) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<u32x2*>(buf + L::kVScales + (v_group * KEYS + v_step * kStep + 16 * i + 4 * v_quad) * 2) =
-                u32x2{__builtin_amdgcn_perm(vpar[i][1], vpar[i][0], 0x05040100u),
-                      __builtin_amdgcn_perm(vpar[i][3], vpar[i][2], 0x05040100u)};
-        }
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<u32x2*>(buf + L::kVScales + (v_group * KEYS + v_step * kStep + 16 * i + 4 * v_quad) * 2) =
+              u32x2{__builtin_amdgcn_perm(v_par[i][1], v_par[i][0], 0x05040100u),
+                    __builtin_amdgcn_perm(v_par[i][3], v_par[i][2], 0x05040100u)};
       }
     };
 
@@ -287,10 +290,17 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     const uint32_t one2 = 0x3C003C00u;
     const u32x4 ones{one2, one2, one2, one2};
 
-    // U steps from the c0-th of a round on
-    auto compute = [&](const int (&key)[kPer], int holes, int c0, const uint8_t* buf) {
-      // ---- scores: products of c - z, then the keys' scales
-      f32x4 x[NT][2 * U];
+    // Scores of a round, less the base they were taken at (0 before the first
+    // key): products of c - z, then the keys' scales, the base in the same
+    // operation.
+    f32x4 x[NT][2 * U];
+    float from[NT], limit[NT];                     // the base or 0; where the maximum has to move
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      from[n] = 0.0f;
+      limit[n] = -INFINITY;
+    }
+    auto scores = [&](const uint8_t* buf, f32x4 (&to)[NT][2 * U]) {
 #pragma unroll
       for (int u = 0; u < 2 * U; ++u)
 #pragma unroll
@@ -300,28 +310,30 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(buf + ((2 * c0 + u) * kSteps + j) * 1024 + op_at(r, kb));
+            const u32x4 k = *reinterpret_cast<const u32x4*>(buf + (u * kSteps + j) * 1024 + op_at(r, kb));
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[n] = mfma(k, qv[n][j], acc[n]);
           }
-          const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + 32 * c0 + 16 * u + 4 * kb) * 4);
+          const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + 16 * u + 4 * kb) * 4);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[n][u][i] = g == 0 ? acc[n][i] * sc[i] : fmaf(acc[n][i], sc[i], x[n][u][i]);
+            for (int i = 0; i < 4; ++i) to[n][u][i] = fmaf(acc[n][i], sc[i], g == 0 ? -from[n] : to[n][u][i]);
         }
-      // ---- masks
-      const int first = key[c0], end = key[c0 + U - 1] + kStep;
-      const int miss = (holes >> (2 * c0)) & ((1 << (2 * U)) - 1);
-      const bool whole = miss == 0 && end - first == U * kStep && end - 1 <= pos_lo &&
+    };
+    float top[NT];
+    // masks of a round's scores, their maxima
+    auto mask = [&](const Round& now) {
+      const int first = now.key[0], end = now.key[U - 1] + kStep, holes = holes_of(now);
+      const bool whole = holes == 0 && end - first == U * kStep && end - 1 <= pos_lo &&
                          (a.window == 0 || first > pos_hi - a.window || end <= a.sinks);
       if (!whole) {
 #pragma unroll
         for (int u = 0; u < 2 * U; ++u) {
-          const bool here = !((miss >> u) & 1);
+          const bool here = !((holes >> u) & 1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = key[c0 + u / 2] + 16 * (u % 2) + 4 * kb + i;
+            const int t = now.key[u / 2] + 16 * (u % 2) + 4 * kb + i;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const bool seen = here && t <= pos[n] && (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
@@ -330,25 +342,6 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           }
         }
       }
-      // ---- scales of the values, pairs of keys
-      f16x2_t sv[G][4 * U];
-      f16x2_t top2{0, 0};
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        f16x2_t t{0, 0};
-#pragma unroll
-        for (int u = 0; u < 2 * U; ++u) {
-          const u32x2 v = *reinterpret_cast<const u32x2*>(buf + L::kVScales + (g * KEYS + 32 * c0 + 16 * u + 4 * kb) * 2);
-          const uint32_t v0 = v.x, v1 = v.y;
-          sv[g][2 * u] = __builtin_bit_cast(f16x2_t, v0);
-          sv[g][2 * u + 1] = __builtin_bit_cast(f16x2_t, v1);
-          t = pk_max(t, pk_max(sv[g][2 * u], sv[g][2 * u + 1]));
-        }
-        top2 = pk_max(top2, t * pair16(shrink[g]));
-      }
-      // ---- running maximum and powers of two: one test for both
-      bool grow = top2[0] > static_cast<_Float16>(1.0f) || top2[1] > static_cast<_Float16>(1.0f);
-      float top[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float t = max3(x[n][0][0], x[n][0][1], x[n][0][2]);
@@ -364,18 +357,69 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           t = max3(t, x[n][3][3], x[n][3][3]);
         }
         top[n] = t;
-        grow |= t > base[n] + 15.0f;
       }
+    };
+
+    // ---- rounds.  Of round n its scores are taken (and its keys' operands
+    // replaced) in round n - 1, its sums in round n: while the scores of the
+    // next round are in the matrix cores the vector unit takes this one's
+    // exponentials, and under the sums it expands the keys of the round after
+    // next and the values of the next.  One barrier a round.
+    Round next = round_of(1), third = round_of(2);
+    Mine k_now = mine_of(2), k_next = mine_of(3);   // of the keys that are on their way, and of the ones after
+    if (rounds > 0) {
+      const Round first = round_of(0);
+      const Mine k0 = mine_of(0), k1 = mine_of(1);
+      fetch_keys(k0);
+      fetch_values(first);
+      clean_keys(k0);
+      clean_values(first);
+      expand_keys(&k_lds[0][0]);
+      expand_values(&v_lds[0][0]);
+      fetch_keys(k1);
+      fetch_values(next);
+      clean_keys(k1);
+      expand_keys(&k_lds[1][0]);
+      fetch_keys(k_now);
+      __syncthreads();
+      scores(&k_lds[0][0], x);
+      mask(first);
+      __syncthreads();                             // the keys of round 0 may be replaced
+    }
+    for (int round = 0; round < rounds; ++round) {
+      const uint8_t* vb = &v_lds[round & 1][0];
+      const Round fourth = round_of(round + 3);
+      const Mine k_fifth = mine_of(round + 4);
+      // ---- scales of the values, pairs of keys
+      f16x2_t sv[G][4 * U];
+      f16x2_t top2{0, 0};
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        f16x2_t t{0, 0};
+#pragma unroll
+        for (int u = 0; u < 2 * U; ++u) {
+          const u32x2 v = *reinterpret_cast<const u32x2*>(vb + L::kVScales + (g * KEYS + 16 * u + 4 * kb) * 2);
+          const uint32_t v0 = v.x, v1 = v.y;
+          sv[g][2 * u] = __builtin_bit_cast(f16x2_t, v0);
+          sv[g][2 * u + 1] = __builtin_bit_cast(f16x2_t, v1);
+          t = pk_max(t, pk_max(sv[g][2 * u], sv[g][2 * u + 1]));
+        }
+        top2 = pk_max(top2, t * pair16(shrink[g]));
+      }
+      // ---- running maximum and powers of two: one test for both
+      bool grow = top2[0] > static_cast<_Float16>(1.0f) || top2[1] > static_cast<_Float16>(1.0f);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) grow |= top[n] > limit[n];
       if (__any(grow)) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           f16x2_t t{0, 0};
 #pragma unroll
           for (int e = 0; e < 4 * U; ++e) t = pk_max(t, sv[g][e]);
-          const float top = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
-          const float next = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(top) >> 23)) << 23));
-          const float f = next / shrink[g];
-          shrink[g] = next;
+          const float most_s = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
+          const float to = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(most_s) >> 23)) << 23));
+          const float f = to / shrink[g];
+          shrink[g] = to;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -383,8 +427,13 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float to = fmaxf(base[n], max_over_quads(top[n]) - 7.0f);
+          const float to = fmaxf(base[n], max_over_quads(top[n]) + from[n] - 7.0f);
           const float fade = to == -INFINITY ? 1.0f : exp2_fast(base[n] - to);
+          const float now_from = to == -INFINITY ? 0.0f : to;
+#pragma unroll
+          for (int u = 0; u < 2 * U; ++u) x[n][u] += from[n] - now_from;
+          from[n] = now_from;
+          limit[n] = to == -INFINITY ? -INFINITY : 15.0f;
           base[n] = to;
           l[n] *= fade;
 #pragma unroll
@@ -393,23 +442,32 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
             for (int y = 0; y < MT; ++y) o[n][g][y] *= fade;
         }
       }
+      // ---- the next round's scores, this one's probabilities (where the
+      // output is bf16, rounded to binary16 before the values' scale as well)
+      u32x4 p[NT][U];
+      f32x4 ahead[NT][2 * U];
+      scores(&k_lds[(round + 1) & 1][0], ahead);
 #pragma unroll
-      for (int c = 0; c < U; ++c) {
-        float p[NT][8];
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float from = base[n] == -INFINITY ? 0.0f : base[n];
+        for (int c = 0; c < U; ++c) {
           u32x4 pw;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const f32x4& xs = x[n][2 * c + (e >> 1)];
-            p[n][2 * e] = exp2_fast(xs[2 * (e & 1)] - from);
-            p[n][2 * e + 1] = exp2_fast(xs[2 * (e & 1) + 1] - from);
-            pw[e] = pack_pair<QMM_F16>(p[n][2 * e], p[n][2 * e + 1]);
+            f32x4& xs = x[n][2 * c + (e >> 1)];
+            xs[2 * (e & 1)] = exp2_fast(xs[2 * (e & 1)]);
+            xs[2 * (e & 1) + 1] = exp2_fast(xs[2 * (e & 1) + 1]);
+            pw[e] = pack_pair<QMM_F16>(xs[2 * (e & 1)], xs[2 * (e & 1) + 1]);
           }
+          if constexpr (DT == QMM_BF16) p[n][c] = pw;
           l[n] = mfma(ones, pw, l[n]);
         }
-        // ---- values
+      }
+      if (k_now.key + 16 > sq.ctx) clean_keys(k_now);
+      if (next.key[U - 1] + kStep > sq.ctx) clean_values(next);
+      // ---- sums; operands of the next rounds
+#pragma unroll
+      for (int c = 0; c < U; ++c)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           u32x4 pv[NT];
@@ -417,43 +475,37 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           for (int e = 0; e < 4; ++e) {
             const f16x2_t s2 = sv[g][4 * c + e] * pair16(shrink[g]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) pv[n][e] = weighted(p[n][2 * e], p[n][2 * e + 1], s2);
+            for (int n = 0; n < NT; ++n) {
+              if constexpr (DT == QMM_BF16) {
+                const uint32_t pair = p[n][c][e];
+                pv[n][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, pair) * s2);
+              } else {
+                const f32x4& xs = x[n][2 * c + (e >> 1)];
+                pv[n][e] = weighted(xs[2 * (e & 1)], xs[2 * (e & 1) + 1], s2);
+              }
+            }
           }
 #pragma unroll
           for (int y = 0; y < MT; ++y) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(
-                buf + L::kVAt + ((c0 + c) * (D / 16) + g * MT + y) * L::kVStride + op_at(r, kb));
+            const u32x4 v =
+                *reinterpret_cast<const u32x4*>(vb + (c * (D / 16) + g * MT + y) * L::kVStride + op_at(r, kb));
 #pragma unroll
             for (int n = 0; n < NT; ++n) o[n][g][y] = mfma(v, pv[n], o[n][g][y]);
           }
         }
-      }
-    };
-
-    // ---- rounds: this one's products, the next one's operands, the codes of
-    // the one after, and the pages of the one after that
-    Round now = round_of(0), next = round_of(1), then = round_of(2);
-    if (rounds > 0) {
-      fetch(now);
-      if (now.key[kPer - 1] + kStep > sq.ctx) clean(now);
-      expand(&lds[0][0]);
-      if (rounds > 1) fetch(next);
-    }
-    __syncthreads();
-    for (int round = 0; round < rounds; ++round) {
-      if (round + 1 < rounds) {
-        if (next.key[kPer - 1] + kStep > sq.ctx) clean(next);
-        expand(&lds[(round + 1) & 1][0]);
-      }
-      if (round + 2 < rounds) fetch(then);
-      const Round last = round_of(round + 3);
-      const int holes = holes_of(now);
+      expand_keys(&k_lds[round & 1][0]);
+      expand_values(&v_lds[(round + 1) & 1][0]);
+      fetch_keys(k_next);
+      fetch_values(third);
 #pragma unroll
-      for (int c = 0; c < kPer; c += U)
-        if (now.key[c] != kBeyond) compute(now.key, holes, c, &lds[round & 1][0]);
-      now = next;
-      next = then;
-      then = last;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int u = 0; u < 2 * U; ++u) x[n][u] = ahead[n][u];
+      mask(next);
+      next = third;
+      third = fourth;
+      k_now = k_next;
+      k_next = k_fifth;
       // only LDS is shared: the codes on their way need not have come
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0xc07f);
