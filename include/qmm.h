@@ -567,11 +567,16 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  * workspace : device memory of at least kv4_attention_workspace_bytes bytes
  *           with the same arguments (max_context = table_width * page), which
  *           may be 0; 16-byte aligned, no clearing needed.
- * Arithmetic: fp32 scores, maxima and sums; see the kernels for the roundings
- * of matrix-core operands.  Results do not depend on timing (no atomics).
+ * Arithmetic: fp32 scores, maxima and sums; probabilities times the values'
+ * scales are rounded to binary16 once.  Two ranges are shared by the rows of a
+ * tile (at most 128 rows of one sequence and kv head): bf16 queries 2^31 below
+ * the largest of the tile, and values whose scale lies 2^11 below the largest
+ * of their channel group, lose bits of their own size.  Infinities and NaN of
+ * a query stay in its row.  Results do not depend on timing (no atomics).
  * ------------------------------------------------------------------------- */
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t q_heads, int64_t kv_heads,
-                                     int64_t head_dim, int64_t max_context, int64_t window, int64_t sinks);
+                                     int64_t head_dim, int group, int64_t max_context, int64_t window,
+                                     int64_t sinks);
 int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, int64_t T, int64_t q_heads,
                   const int32_t* cu_q, int64_t seqs, int64_t max_q, const int32_t* context, const int32_t* page_table,
                   int64_t table_width, int64_t table_stride, const uint8_t* cache, int64_t pages, int64_t kv_heads,

@@ -94,7 +94,7 @@ _SIGS = {
     "kv4_append": ([_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _I64, _I64, _I, _P], _I),
     "kv4_read": ([_P, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _I, _P], _I),
     "kv4_copy_pages": ([_P, _I64, _I64, _I64, _P, _P, _I64, _P], _I),
-    "kv4_attention_workspace_bytes": ([_I64] * 9, _SZ),
+    "kv4_attention_workspace_bytes": ([_I64] * 6 + [_I] + [_I64] * 3, _SZ),
     "kv4_attention": ([_P, _I64, _I64, _I, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64,
                        _I, _F, _I64, _I64, _P, _P, _P, _SZ, _P], _I),
     "qk_norm_rope": ([_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I64, _I64, _P, _P, _I64, _I64, _I, _P, _P, _I,
@@ -845,9 +845,10 @@ def kv4_copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) ->
 
 @functools.lru_cache(maxsize=4096)      # of sizes alone
 def kv4_attention_workspace_bytes(T: int, seqs: int, max_q: int, q_heads: int, kv_heads: int, head_dim: int,
-                                  max_context: int, window: int = 0, sinks: int = 0) -> int:
-    return int(lib().kv4_attention_workspace_bytes(T, seqs, max_q, q_heads, kv_heads, head_dim, max_context, window,
-                                                   sinks))
+                                  group: int, max_context: int, window: int = 0, sinks: int = 0) -> int:
+    """Bytes that kv4_attention needs for these sizes (max_context: the page table's width in tokens); often 0."""
+    return int(lib().kv4_attention_workspace_bytes(T, seqs, max_q, q_heads, kv_heads, head_dim, group, max_context,
+                                                   window, sinks))
 
 
 def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, context: torch.Tensor,
@@ -886,7 +887,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     if out is not None:
         _out(out, shape, dtype)
     _on(q.get_device(), (page_table,), cache=cache, context=context, cu_q=cu_q, out=out, workspace=workspace)
-    need = kv4_attention_workspace_bytes(T, seqs, most, q_heads, kv_heads, D, width * page, window, sinks)
+    need = kv4_attention_workspace_bytes(T, seqs, most, q_heads, kv_heads, D, group, width * page, window, sinks)
     if workspace is not None:
         _req(workspace, "workspace", (torch.uint8,), ndim=1)
         if workspace.numel() < need:

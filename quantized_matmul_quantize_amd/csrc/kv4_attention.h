@@ -2,7 +2,7 @@
 // the 4-bit paged cache; the format and the masks are stated in
 // include/qmm.h), instantiated for one type of q per source file.
 //
-// One kernel serves decode and chunks.  The rows of one sequence and kv head
+// The rows of one sequence and kv head
 // (its queries times the query heads that share the kv head) stand in the 16
 // columns of the products, the keys are taken 32 at a time (a step), in one
 // pass with a running maximum and sum:
@@ -63,8 +63,8 @@ struct Codes64 {
   }
 };
 
-// Queries as second operands.  The power of two that takes the largest of them
-// to 2^14 .. 2^15 (held to normal numbers), and its inverse.
+// Queries as second operands.  The power of two that takes the largest finite
+// one to 2^14 .. 2^15 (held to normal numbers), and its inverse.
 struct QueryScale {
   float down, up;
 };
@@ -73,8 +73,11 @@ __device__ __forceinline__ float largest_bf16(const u32x4 (&q)[N], float most) {
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-      most = fmaxf(most, fmaxf(fabsf(bf16lo_to_f32(q[j][w])), fabsf(bf16hi_to_f32(q[j][w]))));
+    for (int w = 0; w < 4; ++w) {
+      const float a = fabsf(bf16lo_to_f32(q[j][w])), b = fabsf(bf16hi_to_f32(q[j][w]));
+      most = fmaxf(most, a < INFINITY ? a : 0.0f);    // infinities and NaN are their own row's
+      most = fmaxf(most, b < INFINITY ? b : 0.0f);
+    }
   return most;
 }
 __device__ __forceinline__ QueryScale query_scale(float most) {
@@ -125,14 +128,14 @@ __device__ __forceinline__ float lse_of(float base, float sum) {
   return sum > 0.0f ? (base + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Shape of a kernel: PK as above, NT column tiles a wavefront; WS: the
+// Shape of the kernel for few rows: PK as above, NT column tiles.  The
 // wavefronts of a block share the rows and take every fourth unit of PK steps
-// each, else each has rows of its own and takes them all.
-template <int D, int GROUP, int PK, int NT, bool WS>
+// each.  (Many rows: kv4_attention_chunk.h.)
+template <int D, int GROUP, int PK, int NT>
 struct Shape {
   static constexpr int kG = D / GROUP;
   static constexpr int kCols = 16 / PK;                     // rows in 16 columns
-  static constexpr int kRows = kCols * NT * (WS ? 1 : kWaves);
+  static constexpr int kRows = kCols * NT;
   static constexpr int kMTiles = GROUP / 16;                // channel tiles of a group
   static constexpr int kSteps = D / 32;                     // k-extents of a key
   static constexpr int kChunks = D / 32;                    // 16-byte pieces of a key's codes
@@ -151,16 +154,16 @@ struct Shape {
   static constexpr int kVLoads = PK * 2 * (D == 64 ? 1 : kCodeLoads);
   // the epilogue's sums: 16 columns of D channels a wavefront
   static constexpr int kPad = D + 4;
-  static_assert(kWaveBytes >= (16 * kPad + (WS ? 32 : 0)) * 4, "the epilogue reuses the slots");
+  static_assert(kWaveBytes >= (16 * kPad + 32) * 4, "the epilogue reuses the slots");
   // Rotation of a key's pieces within its row in LDS: the 16 lanes that read
   // one piece of 16 keys then meet every bank once.
   static __device__ __forceinline__ int rot(int r) { return r * kChunks / 16; }
 };
 
-template <int DT, int D, int GROUP, int PK, int NT, bool WS>
+template <int DT, int D, int GROUP, int PK, int NT>
 __device__ __forceinline__ void attention_block(const AttnArgs& a) {
-  static_assert(PK == 1 || (WS && NT == 1), "steps are taken together for few rows only");
-  using L = Shape<D, GROUP, PK, NT, WS>;
+  static_assert(PK == 1 || NT == 1, "steps are taken together for few rows only");
+  using L = Shape<D, GROUP, PK, NT>;
   constexpr int G = L::kG, MT = L::kMTiles, kSteps = L::kSteps;
   constexpr float kOff = Int4Magic<QMM_F16>::offset;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * L::kWaveBytes];
@@ -217,17 +220,16 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
   };
 
   for (int tile = tile0; tile * L::kRows < rows; tile += a.row_tiles) {
-    const int row_lo = tile * L::kRows + (WS ? 0 : wave * 16 * NT);          // this wavefront's rows
+    const int row_lo = tile * L::kRows;
     const int row_hi = min(row_lo + L::kCols * NT, rows) - 1;
     const int pos_lo = sq.first + row_lo / a.ratio;
     const int pos_hi = row_hi < row_lo ? -1 : sq.first + row_hi / a.ratio;
-    // the block's steps: every wavefront splits the same range into chunks
     const Steps st = steps_of(a, sq.first + tile * L::kRows / a.ratio,
                               sq.first + (min((tile + 1) * L::kRows, rows) - 1) / a.ratio);
     const int chunks = max(1, (st.count + a.chunk - 1) / a.chunk);
     if (split >= chunks) continue;
-    const int s_lo = split * a.chunk + (WS ? wave * PK : 0), s_hi = min(split * a.chunk + a.chunk, st.count);
-    constexpr int kStride = PK * (WS ? kWaves : 1);
+    const int s_lo = split * a.chunk + wave * PK, s_hi = min(split * a.chunk + a.chunk, st.count);
+    constexpr int kStride = PK * kWaves;
 
     auto unit_of = [&](int s) {
       Unit x;
@@ -624,7 +626,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       if (L::kSlots == 2) slot ^= 1;
     }
 
-    // ---- results: o - corr, joined over columns and wavefronts (WS), then out or the workspace
+    // ---- results: o - corr, joined over columns and wavefronts, then out or the workspace
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       l[n] = sum_over_quads(l[n]);
@@ -646,7 +648,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       else return g * 32 + 8 * (q & 3) + 4 * ((q >> 2) & 1) + 2 * y + (q >> 3);
     };
     constexpr int kPad = L::kPad;
-    if constexpr (WS) {
+    {
       // 16 columns at a time: maxima and sums of every wavefront, then their scaled sums
       float* all = reinterpret_cast<float*>(lds);
       float* stat = all + kWaves * 16 * kPad;
@@ -698,34 +700,6 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           }
         }
       }
-    } else {
-      // a wavefront's own rows: through its part of LDS, for whole 16-byte stores
-      float* own = reinterpret_cast<float*>(mine);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        asm volatile("" ::: "memory");
-        const float inv = l[n] > 0.0f ? 1.0f / l[n] : 0.0f;
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-          for (int y = 0; y < MT; ++y)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) own[r * kPad + channel(g, y, i)] = o[n][g][y][i] * inv;
-        asm volatile("" ::: "memory");
-        const int row = row_lo + 16 * n + r;
-        const int tok = row / a.ratio;
-        const int64_t rh = static_cast<int64_t>(sq.row0 + tok) * a.q_heads + kvh * a.ratio + row - tok * a.ratio;
-        if (row < rows) {
-          if (a.lse && kb == 0) a.lse[rh] = lse_of(base[n], l[n]);
-#pragma unroll
-          for (int c = 0; c < D / 4; c += 8) {
-            const float* v = own + r * kPad + kb * (D / 4) + c;
-            *reinterpret_cast<u32x4*>(a.out + rh * D + kb * (D / 4) + c) =
-                u32x4{pack_pair<DT>(v[0], v[1]), pack_pair<DT>(v[2], v[3]), pack_pair<DT>(v[4], v[5]), pack_pair<DT>(v[6], v[7])};
-          }
-        }
-        asm volatile("" ::: "memory");
-      }
     }
     __syncthreads();   // LDS is free for the next rows
   }
@@ -735,9 +709,9 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 // accumulator form every round copied the sums out and back for the test of
 // the maximum: 35 instead of 25 us for 7 sequences of 32 heads in groups of
 // 32), where the sums (NT D / 16) and a group's products and scales fit 256.
-template <int DT, int D, int GROUP, int PK, int NT, bool WS>
+template <int DT, int D, int GROUP, int PK, int NT>
 __global__ __launch_bounds__(256, NT * D + 16 * (D / GROUP) * PK * NT <= 320 ? 2 : 1) void attention_kernel(AttnArgs a) {
-  attention_block<DT, D, GROUP, PK, NT, WS>(a);
+  attention_block<DT, D, GROUP, PK, NT>(a);
 }
 
 // Joins the chunks of rows whose keys were split: a block a row and head,

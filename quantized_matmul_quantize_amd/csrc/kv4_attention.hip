@@ -11,14 +11,15 @@ namespace {
 // How the work is cut.  Rows: the fewer, the more steps a wavefront takes at
 // once; from 65 rows on every wavefront has rows of its own.  Keys: split over
 // blocks only where the rows and heads leave compute units idle.
-AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, int64_t D, int64_t max_context,
-                 int64_t window, int64_t sinks) {
+AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, int64_t D, int group,
+                 int64_t max_context, int64_t window, int64_t sinks) {
   AttnPlan p{};
   p.max_q = max_q;
   const int64_t rows = max_q * ratio;
   p.ws = rows <= 64;
-  p.pk = rows <= 8 ? 2 : 1;
-  p.nt = rows <= 16 || D == 256 ? 1 : 2;
+  p.pk = rows <= 8 && attention_pairs(static_cast<int>(D), group) ? 2 : 1;
+  p.nt = !p.ws ? attention_chunk_tiles(static_cast<int>(D), group)
+               : rows <= 16 ? 1 : attention_tiles(static_cast<int>(D), group);
   p.rows = 16 / p.pk * p.nt * (p.ws ? 1 : kWaves);
   p.row_tiles = std::min<int64_t>(ceil_div(rows, p.rows), 65535);
   int64_t steps = ceil_div(max_context, kStep);
@@ -48,15 +49,15 @@ size_t workspace_bytes_of(const AttnPlan& p, int64_t T, int64_t q_heads, int64_t
 }  // namespace qmm
 
 extern "C" size_t kv4_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t q_heads,
-                                                int64_t kv_heads, int64_t head_dim, int64_t max_context,
-                                                int64_t window, int64_t sinks) {
+                                                int64_t kv_heads, int64_t head_dim, int group,
+                                                int64_t max_context, int64_t window, int64_t sinks) {
   using namespace qmm;
   if (T <= 0 || seqs <= 0 || max_q <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 ||
-      max_context <= 0 || max_context >= (int64_t{1} << 31) || window < 0 || sinks < 0 || T >= (int64_t{1} << 31) ||
+      group <= 0 || max_context <= 0 || max_context >= (int64_t{1} << 31) || window < 0 || sinks < 0 || T >= (int64_t{1} << 31) ||
       seqs > 65535 || q_heads > 65535)
     return 0;
-  return workspace_bytes_of(plan_of(seqs, std::min(max_q, T), q_heads / kv_heads, kv_heads, head_dim, max_context,
-                                    window, sinks), T, q_heads, head_dim);
+  return workspace_bytes_of(plan_of(seqs, std::min(max_q, T), q_heads / kv_heads, kv_heads, head_dim, group,
+                                    max_context, window, sinks), T, q_heads, head_dim);
 }
 
 extern "C" int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, int64_t T,
@@ -82,7 +83,8 @@ extern "C" int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_he
       !aligned(cu_q, 4) || !aligned(page_table, 4) || ((q_token_stride | q_head_stride) & 7))
     return QMM_EALIGN;
   const int64_t ratio = q_heads / kv_heads, tokens = table_width * page;
-  const AttnPlan p = plan_of(seqs, cu_q ? std::min(max_q, T) : 1, ratio, kv_heads, head_dim, tokens, window, sinks);
+  const AttnPlan p = plan_of(seqs, cu_q ? std::min(max_q, T) : 1, ratio, kv_heads, head_dim, group, tokens,
+                             window, sinks);
   const size_t need = workspace_bytes_of(p, T, q_heads, head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QMM_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return QMM_EALIGN;

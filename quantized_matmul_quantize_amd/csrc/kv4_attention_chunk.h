@@ -32,8 +32,10 @@ struct Chunk {
   static constexpr int kVScales = kVOps * kVStride;         // binary16 [group][key]
   static constexpr int kVBuffer = kVScales + kG * kKeys * 2;
   static_assert(kKBuffer % 16 == 0 && kVBuffer % 16 == 0, "alignment");
-  // what a producing lane expands: words of a key's codes, and pairs of channels' nibbles of a word of values
-  static constexpr int kWords = kKeys * D / 8 / 256, kNibbles = kKeys * D / 8 / 256;
+  // what a lane expands of a round: kWords words of a key's codes; of a word of two quads of values kNibbles
+  // nibbles of either its low or its high half (kShare lanes a word)
+  static constexpr int kWords = kKeys * D / (512 * kWaves), kKeyWaves = D / (32 * kWords);
+  static constexpr int kShare = 64 * kWaves / (kKeys * D / 64), kNibbles = 8 / kShare;
 };
 
 // Lane (r, kb) finds its 16 bytes of an operand in lane order, and producers
@@ -47,6 +49,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   constexpr int U = KEYS / kStep;                  // steps of a round
   constexpr int kTiles = KEYS / 16;                // 16-key tiles of a round
   constexpr int kWords = L::kWords;
+  constexpr int kAhead = 2;                        // operands read before they are used
+  constexpr int kAluMayCross = 0x6;                // sched_barrier: scalar and vector arithmetic
   __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][L::kKBuffer];
   __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][L::kVBuffer];
 
@@ -71,15 +75,15 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   const table_t table = (table_t)(a.table + b * a.table_stride);
 
   // What a lane expands of a round.  Keys: kWords words of key r of a 16-key
-  // tile (the wavefront's; D 256: two wavefronts a tile).  Values: of one word
-  // of both quads `v_quad` of a step, half of the channels (`part`; D 64: a
-  // quarter).
-  const int k_tile = D == 256 ? wave >> 1 : wave;
-  const int k_piece = D == 256 ? 4 * (wave & 1) + kb : kb;          // of 4 kWords bytes
-  const int v_unit = D == 256 ? 64 * (wave >> 1) + lane : lane;
+  // tile (kKeyWaves wavefronts a tile).  Values: of one word of both quads
+  // `v_quad` of a step half the channels (`part`: even or odd ones) or a
+  // quarter.
+  const int k_tile = wave / L::kKeyWaves;
+  const int k_piece = 4 * (wave % L::kKeyWaves) + kb;               // of 4 kWords bytes
+  const int v_unit = 64 * (wave / L::kShare) + lane;
   const int v_word = v_unit % (D / 8), v_quad = v_unit / (D / 8) % 4;
-  const int v_step = D == 64 ? lane >> 5 : D == 128 ? wave >> 1 : 0;
-  const int part = wave & 1, v_first = D == 64 ? 2 * (wave >> 1) : 0;   // first of its nibbles of a half word
+  const int v_step = D == 64 ? v_unit >> 5 : U == 2 ? wave / L::kShare : 0;
+  const int part = wave % L::kShare & 1, v_first = L::kNibbles * (wave % L::kShare >> 1);   // first of its nibbles
   const int v_group = v_word / (GROUP / 8);
   const int k_at = r * (D / 2) + 4 * kWords * k_piece, kp_at = a.sh.page * D + 4 * r;
   const int v_at = a.sh.page * (D / 2) + 16 * v_word + v_quad * (2 * D);
@@ -120,7 +124,10 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       most = wave_max(most);
       if (lane == 0) stat[wave] = most;
       __syncthreads();
-      const QueryScale qs = query_scale(fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3])));
+      most = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) most = fmaxf(most, stat[w]);
+      const QueryScale qs = query_scale(most);
       __syncthreads();
       unscale = qs.up;
 #pragma unroll
@@ -229,7 +236,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
       for (int w = 0; w < kWords; ++w) {
         const int word = kWords * k_piece + w;     // k-extent j of lane quarter kb is word kSteps kb + j
-        const int j = kWords == 2 ? w : kSteps == 4 ? w : word % kSteps;
+        const int j = kWords == kSteps ? w : word % kSteps;
         uint32_t par = k_par[0];
 #pragma unroll
         for (int g = 1; g < G; ++g) par = j * 32 / GROUP == g ? k_par[g] : par;
@@ -301,25 +308,32 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       limit[n] = -INFINITY;
     }
     auto scores = [&](const uint8_t* buf, f32x4 (&to)[NT][2 * U]) {
+      constexpr int kOps = 2 * U * kSteps;
+      u32x4 k[kAhead];
+      auto read = [&](int i) { return *reinterpret_cast<const u32x4*>(buf + i * 1024 + op_at(r, kb)); };
 #pragma unroll
-      for (int u = 0; u < 2 * U; ++u)
+      for (int i = 0; i < kAhead; ++i) k[i] = read(i);
+      __builtin_amdgcn_sched_barrier(kAluMayCross);
+      f32x4 acc[NT];
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          f32x4 acc[NT];
+      for (int i = 0; i < kOps; ++i) {
+        const int u = i / kSteps, j = i % kSteps, g = j * 32 / GROUP;
+        if (j * 32 % GROUP == 0) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
 #pragma unroll
-          for (int j = g * GROUP / 32; j < (g + 1) * GROUP / 32; ++j) {
-            const u32x4 k = *reinterpret_cast<const u32x4*>(buf + (u * kSteps + j) * 1024 + op_at(r, kb));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n] = mfma(k, qv[n][j], acc[n]);
-          }
+        for (int n = 0; n < NT; ++n) acc[n] = mfma(k[i % kAhead], qv[n][j], acc[n]);
+        if (i + kAhead < kOps) k[i % kAhead] = read(i + kAhead);
+        __builtin_amdgcn_sched_barrier(kAluMayCross);
+        if ((j + 1) * 32 % GROUP == 0) {
           const f32x4 sc = *reinterpret_cast<const f32x4*>(buf + L::kKScales + (g * KEYS + 16 * u + 4 * kb) * 4);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to[n][u][i] = fmaf(acc[n][i], sc[i], g == 0 ? -from[n] : to[n][u][i]);
+            for (int e = 0; e < 4; ++e) to[n][u][e] = fmaf(acc[n][e], sc[e], g == 0 ? -from[n] : to[n][u][e]);
         }
+      }
     };
     float top[NT];
     // masks of a round's scores, their maxima
@@ -390,21 +404,22 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       const uint8_t* vb = &v_lds[round & 1][0];
       const Round fourth = round_of(round + 3);
       const Mine k_fifth = mine_of(round + 4);
-      // ---- scales of the values, pairs of keys
-      f16x2_t sv[G][4 * U];
-      f16x2_t top2{0, 0};
+      // ---- the largest scale of the values, of every second key; the scales
+      // themselves are read again where they are used
+      auto pairs_of = [&](int g, int u) {          // two pairs of keys
+        return *reinterpret_cast<const u32x2*>(vb + L::kVScales + (g * KEYS + 16 * u + 4 * kb) * 2);
+      };
+      f16x2_t most_s[G], top2{0, 0};
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        f16x2_t t{0, 0};
+        most_s[g] = f16x2_t{0, 0};
 #pragma unroll
         for (int u = 0; u < 2 * U; ++u) {
-          const u32x2 v = *reinterpret_cast<const u32x2*>(vb + L::kVScales + (g * KEYS + 16 * u + 4 * kb) * 2);
+          const u32x2 v = pairs_of(g, u);
           const uint32_t v0 = v.x, v1 = v.y;
-          sv[g][2 * u] = __builtin_bit_cast(f16x2_t, v0);
-          sv[g][2 * u + 1] = __builtin_bit_cast(f16x2_t, v1);
-          t = pk_max(t, pk_max(sv[g][2 * u], sv[g][2 * u + 1]));
+          most_s[g] = pk_max(most_s[g], pk_max(__builtin_bit_cast(f16x2_t, v0), __builtin_bit_cast(f16x2_t, v1)));
         }
-        top2 = pk_max(top2, t * pair16(shrink[g]));
+        top2 = pk_max(top2, most_s[g] * pair16(shrink[g]));
       }
       // ---- running maximum and powers of two: one test for both
       bool grow = top2[0] > static_cast<_Float16>(1.0f) || top2[1] > static_cast<_Float16>(1.0f);
@@ -413,11 +428,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       if (__any(grow)) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          f16x2_t t{0, 0};
-#pragma unroll
-          for (int e = 0; e < 4 * U; ++e) t = pk_max(t, sv[g][e]);
-          const float most_s = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
-          const float to = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(most_s) >> 23)) << 23));
+          const float largest = wave_max(fmaxf(static_cast<float>(most_s[g][0]), static_cast<float>(most_s[g][1])));
+          const float to = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(largest) >> 23)) << 23));
           const float f = to / shrink[g];
           shrink[g] = to;
 #pragma unroll
@@ -466,33 +478,40 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       if (k_now.key + 16 > sq.ctx) clean_keys(k_now);
       if (next.key[U - 1] + kStep > sq.ctx) clean_values(next);
       // ---- sums; operands of the next rounds
+      {
+        constexpr int kOps = U * G * MT;
+        u32x4 v[kAhead], pv[NT];
+        auto read = [&](int i) { return *reinterpret_cast<const u32x4*>(vb + i * L::kVStride + op_at(r, kb)); };
 #pragma unroll
-      for (int c = 0; c < U; ++c)
+        for (int i = 0; i < kAhead; ++i) v[i] = read(i);
+        __builtin_amdgcn_sched_barrier(kAluMayCross);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          u32x4 pv[NT];
+        for (int i = 0; i < kOps; ++i) {
+          const int c = i / (G * MT), g = i / MT % G, y = i % MT;
+          if (y == 0) {
+            const u32x2 s01 = pairs_of(g, 2 * c), s23 = pairs_of(g, 2 * c + 1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const f16x2_t s2 = sv[g][4 * c + e] * pair16(shrink[g]);
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t se = e < 2 ? s01[e & 1] : s23[e & 1];
+              const f16x2_t s2 = __builtin_bit_cast(f16x2_t, se) * pair16(shrink[g]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if constexpr (DT == QMM_BF16) {
-                const uint32_t pair = p[n][c][e];
-                pv[n][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, pair) * s2);
-              } else {
-                const f32x4& xs = x[n][2 * c + (e >> 1)];
-                pv[n][e] = weighted(xs[2 * (e & 1)], xs[2 * (e & 1) + 1], s2);
+              for (int n = 0; n < NT; ++n) {
+                if constexpr (DT == QMM_BF16) {
+                  const uint32_t pair = p[n][c][e];
+                  pv[n][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, pair) * s2);
+                } else {
+                  const f32x4& xs = x[n][2 * c + (e >> 1)];
+                  pv[n][e] = weighted(xs[2 * (e & 1)], xs[2 * (e & 1) + 1], s2);
+                }
               }
             }
           }
 #pragma unroll
-          for (int y = 0; y < MT; ++y) {
-            const u32x4 v =
-                *reinterpret_cast<const u32x4*>(vb + (c * (D / 16) + g * MT + y) * L::kVStride + op_at(r, kb));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) o[n][g][y] = mfma(v, pv[n], o[n][g][y]);
-          }
+          for (int n = 0; n < NT; ++n) o[n][g][y] = mfma(v[i % kAhead], pv[n], o[n][g][y]);
+          if (i + kAhead < kOps) v[i % kAhead] = read(i + kAhead);
+          __builtin_amdgcn_sched_barrier(kAluMayCross);
         }
+      }
       expand_keys(&k_lds[round & 1][0]);
       expand_values(&v_lds[(round + 1) & 1][0]);
       fetch_keys(k_next);
@@ -543,10 +562,12 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   }
 }
 
-// Two blocks a compute unit where the registers allow it: one wavefront's
-// products then run under the other's exponentials.
+// Two blocks a compute unit: one wavefront's products then run under the
+// other's exponentials.  (A block of eight wavefronts instead, which expands
+// half as much a wavefront: 804 instead of 829 us for three chunks of prompts,
+// but half as many blocks.)
 template <int DT, int D, int GROUP, int NT>
-__global__ __launch_bounds__(256, NT * D <= 256 ? 2 : 1) void attention_chunk_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D / GROUP < 8 ? 2 : 1) void attention_chunk_kernel(AttnArgs a) {
   attention_chunk_block<DT, D, GROUP, NT>(a);
 }
 

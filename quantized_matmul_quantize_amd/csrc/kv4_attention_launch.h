@@ -8,26 +8,22 @@ namespace qmm {
 namespace {
 
 template <int DT, int D, int GROUP>
-void launch_shape(const AttnArgs& a, AttnPlan& p, hipStream_t s) {
+void launch_shape(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.blocks));
-  constexpr int kMost = D == 256 ? 1 : 2;      // column tiles that fit the registers
-  if (D == 256 && GROUP == 32 && p.pk == 2) {  // eight groups of two steps do not
-    p.pk = 1;
-    p.rows = 16;
-  }
+  constexpr int kTiles = attention_tiles(D, GROUP);
   if (!p.ws) {
-    attention_chunk_kernel<DT, D, GROUP, kMost><<<grid, 256, 0, s>>>(a);
+    attention_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP)><<<grid, 256, 0, s>>>(a);
   } else if (p.pk == 2) {
-    if constexpr (D < 256 || GROUP > 32) attention_kernel<DT, D, GROUP, 2, 1, true><<<grid, 256, 0, s>>>(a);
+    if constexpr (attention_pairs(D, GROUP)) attention_kernel<DT, D, GROUP, 2, 1><<<grid, 256, 0, s>>>(a);
   } else if (p.nt == 1) {
-    attention_kernel<DT, D, GROUP, 1, 1, true><<<grid, 256, 0, s>>>(a);
+    attention_kernel<DT, D, GROUP, 1, 1><<<grid, 256, 0, s>>>(a);
   } else {
-    attention_kernel<DT, D, GROUP, 1, kMost, true><<<grid, 256, 0, s>>>(a);
+    attention_kernel<DT, D, GROUP, 1, kTiles><<<grid, 256, 0, s>>>(a);
   }
 }
 
 template <int DT>
-void launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t s) {
+void launch_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
   const int D = a.sh.D, g = a.sh.group;
   if (D == 64) {
     if (g == 32) launch_shape<DT, 64, 32>(a, p, s);

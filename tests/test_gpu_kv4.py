@@ -210,7 +210,8 @@ class Batch:
         self.starts = np.concatenate([[0], np.cumsum(queries)]).astype(np.int32)
         self.q = half(g.standard_normal((int(self.starts[-1]), hq, D)), dtype)
 
-    def check(self, got, window=0, sinks=0, scale=None, q=None):
+    def check(self, got, window=0, sinks=0, scale=None, q=None, rows=None):
+        """The results (of the tokens and heads where `rows` is true) against fp64."""
         out, lse = got
         q = (self.q if q is None else q).float().numpy()
         T, hq, D = q.shape
@@ -220,12 +221,14 @@ class Batch:
         bound = (2.0 ** -8 + 2 * dx[..., None]) * mass + (count[:, None, None] / 16 + 32) * U * 143 * self.sv
         bound = bound + OUT_HALF_ULP[self.dtype] * np.abs(o) + (2.0 ** -24 if self.dtype == F16 else 0.0)
         err = np.abs(out.float().cpu().numpy() - o)
-        none = count == 0
+        none = np.repeat((count == 0)[:, None], hq, 1)
+        rows = np.ones((T, hq), bool) if rows is None else rows
         assert (out.cpu()[torch.from_numpy(none)] == 0).all()
-        assert (err <= bound)[~none].all(), f"out: worst {np.nanmax(err / bound)} of its bound at {np.argmax(err / bound)}"
+        assert (err <= bound)[~none & rows].all(), f"out: worst {np.nanmax(err / bound)} of its bound at {np.argmax(err / bound)}"
         got_l = lse.cpu().numpy().astype(np.float64)
         assert np.isneginf(got_l[none]).all()
-        worst = np.abs(got_l[~none] - l[~none]) - (dx + 8 * U * (1 + np.abs(l)))[~none]
+        seen = ~none & rows
+        worst = np.abs(got_l[seen] - l[seen]) - (dx + 8 * U * (1 + np.abs(l)))[seen]
         assert (worst <= 0).all(), f"lse: {worst.max()} past its bound"
 
     def run(self, **kw):
@@ -298,7 +301,7 @@ def test_table_rows_apart_strided_queries_and_given_outputs():
     qkv = torch.zeros((3, 16, 128), dtype=F16, device="cuda")
     qkv[:, 4:12] = b.q.cuda()
     out = torch.full((3, 8, 128), 7.0, dtype=F16, device="cuda")
-    need = qmm.kv4_attention_workspace_bytes(3, 3, 1, 8, 4, 128, b.width * 32)
+    need = qmm.kv4_attention_workspace_bytes(3, 3, 1, 8, 4, 128, 32, b.width * 32)
     ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")     # bytes of NaN
     got = b.run(q=qkv[:, 4:12], out=out, workspace=ws)
     assert got[0].data_ptr() == out.data_ptr()
@@ -322,6 +325,59 @@ def test_large_scores_and_a_context_beyond_the_table():
     got = qmm.kv4_attention(b.q[1:].cuda(), b.cache, b.table[1:, :4], torch.tensor([10 ** 6], dtype=torch.int32).cuda())
     same = qmm.kv4_attention(b.q[1:].cuda(), b.cache, b.table[1:, :4], b.context[1:])
     assert torch.equal(got, same)
+
+
+@pytest.mark.parametrize("queries", [[1, 1], [3, 2], [90, 5]])
+def test_a_query_that_is_not_finite_stays_in_its_row(queries):
+    b = Batch(12, BF16, 128, 64, 16, 4, 2, [200, 70], queries)
+    q = b.q.clone()
+    q[0, 0, 5], q[1, 2, 7] = math.inf, math.nan
+    out, lse = (x.cpu() for x in b.run(q=q.cuda()))
+    rest = np.ones(q.shape[:2], bool)
+    rest[0, 0] = rest[1, 2] = False
+    safe = q.clone()
+    safe[0, 0], safe[1, 2] = 0, 0
+    b.check((out, lse), q=safe, rows=rest)
+    assert not out[~torch.from_numpy(rest)].isfinite().all()
+
+
+@pytest.mark.parametrize("queries", [[1, 1], [90, 5]])
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** 40])
+def test_queries_of_any_size(queries, size):
+    """bf16 queries far from the middle of the binary16 range, with a scale to match."""
+    b = Batch(13, BF16, 128, 64, 16, 4, 2, [200, 70], queries)
+    b.q = (b.q.float() * size).to(BF16)
+    b.check(b.run(scale=128 ** -0.5 / size), scale=128 ** -0.5 / size)
+
+
+@pytest.mark.parametrize("queries", [[1, 1], [90, 5]])
+@pytest.mark.parametrize("rise", [True, False])
+def test_values_of_very_different_sizes(queries, rise):
+    """Values that grow (or fall) a hundredfold along the sequence: the power of two that binary16 weights carry moves."""
+    D, group, page, n = 128, 32, 16, 300
+    b = Batch(14, F16, D, group, page, 4, 2, [n, 70], queries)
+    g = rng(15)
+    ramp = np.exp(np.linspace(0, np.log(100.0), n) * (1 if rise else -1))[:, None, None]
+    v = half(g.standard_normal((n, 2, D)) * ramp * np.repeat([1.0, 30.0, 0.05, 1.0], 32), F16)
+    j = np.arange(n)
+    k = half(g.standard_normal((n, 2, D)), F16)
+    slots = b.table[0].cpu().numpy()[j // page].astype(np.int64) * page + j % page
+    qmm.kv4_append(k.cuda(), v.cuda(), torch.from_numpy(slots).cuda(), b.cache)
+    kq, vq = (ref.quantize(x.float().numpy(), group) for x in (k, v))
+    b.k[0], b.v[0], b.sk, b.sv = ref.values(*kq), ref.values(*vq), max(b.sk, float(kq[2].max())), float(vq[2].max())
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+def test_chunks_over_split_keys(dtype, D, group):
+    """Few rows and heads over a long context: blocks share the keys, for chunks and for a few queries alike."""
+    note(f"kv4 split chunks D={D} group={group} {dtype}")
+    b = Batch(16 + D + group, dtype, D, group, 64, 6, 2, [3000, 700], [70, 25])
+    b.check(b.run())
+    b.check(b.run(window=900, sinks=5), window=900, sinks=5)
+    few = Batch(17 + D + group, dtype, D, group, 64, 6, 2, [2600, 90], [9, 3])
+    few.check(few.run())
 
 
 def test_long_context_splits_and_high_pages():
