@@ -505,7 +505,8 @@ int awq_search(const void* W, int w_dtype, const void* X, int x_dtype, int64_t N
  * slot  : page id * page + place in the page (int64).
  * D 64, 128 or 256; page 16, 32, 64, 128 or 256; g 32, 64 or 128, dividing D
  * (QMM_EUNSUPPORTED otherwise).  16-bit types: QMM_BF16, QMM_F16.  A call on
- * no tokens (pages, sequences) is QMM_OK and launches nothing.
+ * no tokens (pages, sequences) is QMM_OK and launches nothing.  At most 4096
+ * heads, and fewer than 2^25 tokens (2^24 page pairs) a call (QMM_ERANGE).
  * Memory of the cache that no token was appended to may hold anything.
  * ------------------------------------------------------------------------- */
 
@@ -557,6 +558,7 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  *           cu_q[b + 1] - 1 of q; NULL when every sequence has one (T == seqs).
  * max_q   : the most queries of a sequence (at least 1).  A hint: it only
  *           shapes the launch.
+ *           Rows of q in no sequence are not written in out and lse.
  * context : int32 [seqs], device; at most table_width * page is used.
  * page_table : int32 [seqs, table_width], rows table_stride elements apart.
  *           The launch is shaped for contexts up to table_width * page, so a
@@ -567,6 +569,8 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  * workspace : device memory of at least kv4_attention_workspace_bytes bytes
  *           with the same arguments (max_context = table_width * page), which
  *           may be 0; 16-byte aligned, no clearing needed.
+ * At most 65535 sequences and query heads, T * q_heads below 2^31 and
+ * table_width * page up to 2^30 (QMM_ERANGE).
  * Arithmetic: fp32 scores, maxima and sums; probabilities times the values'
  * scales are rounded to binary16 once.  Two ranges are shared by the rows of a
  * tile (at most 128 rows of one sequence and kv head): bf16 queries 2^31 below
@@ -599,7 +603,8 @@ int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, 
  * position outside the table gives NaN in the rotated channels.
  * q_weight, k_weight [D] of w_dtype (dtype or QMM_F32), either may be NULL.
  * q_out [T, q_heads, D], k_out [T, k_heads, D] dense; q_out may be q (and
- * k_out k) where that is dense.  All 16-byte aligned (positions 8).
+ * k_out k) where that is dense.  All 16-byte aligned (positions 8).  T below
+ * 2^24 (QMM_ERANGE).
  * ------------------------------------------------------------------------- */
 int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
                  int64_t k_token_stride, int64_t k_head_stride, int64_t k_heads, int dtype, int64_t T,
@@ -612,7 +617,7 @@ int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, i
  * rounded once to fp32.  inv_freq: HOST array of half (1 .. 256) frequencies
  * f_i in radians per position, as scaled for the context; m: the magnitude
  * some scalings ask for (1 otherwise).  table float32 [rows, half, 2], 16-byte
- * aligned; rows < 2^31. */
+ * aligned; rows * half < 2^31 (QMM_ERANGE). */
 int rope_table(const double* inv_freq, int64_t half, int64_t rows, double m, float* table, void* stream);
 
 #ifdef __cplusplus

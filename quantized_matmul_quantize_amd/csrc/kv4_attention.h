@@ -2,10 +2,9 @@
 // the 4-bit paged cache; the format and the masks are stated in
 // include/qmm.h), instantiated for one type of q per source file.
 //
-// The rows of one sequence and kv head
-// (its queries times the query heads that share the kv head) stand in the 16
-// columns of the products, the keys are taken 32 at a time (a step), in one
-// pass with a running maximum and sum:
+// The rows of one sequence and kv head (its queries times the query heads that
+// share the kv head) stand in the 16 columns of the products, the keys are
+// taken 32 at a time (a step), in one pass with a running maximum and sum:
 //
 //   S^T = K Q^T   codes of 16 keys x 32 channels as the first operand, q as the
 //                 second, so a lane ends with 4 keys of one column;
@@ -24,7 +23,7 @@
 // offset of 64 takes one shift a word less than 16, but its rounding is the
 // scores' largest error; bf16 operands would need 128.)  bf16 queries are first
 // scaled by a power of two, their largest to 2^14 .. 2^15: exact but for what
-// lies 2^38 below it.  p' is rounded to binary16 (2^-12) for either type of q:
+// lies 2^31 below it.  p' is rounded to binary16 (2^-12) for either type of q:
 // bf16 would cost 2^-9.  Its range is kept by the two powers of two that are
 // moved only when they must be: p lies below 2^15 (and reaches 2^7 where the
 // maximum was last moved, so that what is lost below 2^-25 is 2^-32 of the
@@ -32,12 +31,15 @@
 //
 // What bounds decode is the vector unit, not the matrix cores: two operations
 // a pair of codes to make operands of them, and then the arithmetic on the
-// scores, of which few rows leave most columns idle.  So with 8 rows or fewer
-// a wavefront takes two steps at once (PK = 2): both halves of the columns
+// scores, of which few rows leave most columns idle.  So with few rows a
+// wavefront takes two steps at once (PK = 2): both halves of the columns
 // hold the same rows but keep the scores, maxima, sums and results of a step
 // of their own, and are joined at the end, as the wavefronts are.  (Four steps
 // at once for 4 rows: 220 instead of 250 vector operations a step, but 70 KiB
 // of LDS a block and 58 instead of 54 us for 64 sequences of 4096 tokens.)
+// Of those 54 us (8 kv heads of 128 in one group, 243 MB: 4.5 TB/s) the loads
+// alone take 45, the arithmetic alone 44; with 2 sequences of 131072 tokens in
+// groups of 64 (293 MB) 52 and 51 of 66.
 #pragma once
 
 #include "kv4_attention_args.h"

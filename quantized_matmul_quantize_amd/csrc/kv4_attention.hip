@@ -8,20 +8,31 @@
 namespace qmm {
 namespace {
 
-// How the work is cut.  Rows: the fewer, the more steps a wavefront takes at
-// once; from 65 rows on every wavefront has rows of its own.  Keys: split over
-// blocks only where the rows and heads leave compute units idle.
+// How the work is cut.  Up to 96 rows the wavefronts of a block share the rows
+// and split the keys; beyond, each has rows of its own, of shared operands
+// (32 sequences of 4000 tokens, 8 kv heads, D 128 in one group, us: 64 rows
+// 71 shared, 124 own; 96 rows 107, 136; 128 rows 133, 149; 256 rows 252, 182;
+// in groups of 64: 96 rows 133, 156; 128 rows 165, 157; 256 rows 314, 305).
+// The fewer the rows, the more steps a wavefront takes at once; where a tile
+// for every 8 (16) rows leaves most of the chip empty, blocks of fewer rows are
+// the better ones (groups of 64, 16 rows: 8 sequences of 2000 tokens 19.6 us
+// in pairs of steps, 22.2 in single ones, 32 of 4000 54 and 49; 20 rows: 8
+// sequences 22.7 us in tiles of 16, 28.1 of 32, 32 of them 69 and 61).
+// Keys are split over blocks only where rows and heads leave compute units idle.
 AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, int64_t D, int group,
                  int64_t max_context, int64_t window, int64_t sinks) {
   AttnPlan p{};
   p.max_q = max_q;
-  const int64_t rows = max_q * ratio;
-  p.ws = rows <= 64;
-  p.pk = rows <= 8 && attention_pairs(static_cast<int>(D), group) ? 2 : 1;
+  const int64_t rows = max_q * ratio, fill = 2 * device_cus();
+  p.ws = rows <= 96;
+  const bool eights = rows <= 8 || (rows <= 16 && 4 * seqs * kv_heads * ceil_div(rows, 8) <= fill);
+  const bool sixteens = rows <= 16 || seqs * kv_heads * ceil_div(rows, 16) < fill;
+  p.pk = eights && attention_pairs(static_cast<int>(D), group) ? 2 : 1;
   p.nt = !p.ws ? attention_chunk_tiles(static_cast<int>(D), group)
-               : rows <= 16 ? 1 : attention_tiles(static_cast<int>(D), group);
+               : sixteens ? 1 : attention_tiles(static_cast<int>(D), group);
   p.rows = 16 / p.pk * p.nt * (p.ws ? 1 : kWaves);
-  p.row_tiles = std::min<int64_t>(ceil_div(rows, p.rows), 65535);
+  // (blocks loop over row tiles past these: a launch holds 2^24 blocks of 256 threads)
+  p.row_tiles = std::min(ceil_div(rows, p.rows), std::max<int64_t>(1, (int64_t{1} << 22) / (seqs * kv_heads)));
   int64_t steps = ceil_div(max_context, kStep);
   if (window > 0)
     steps = std::min(steps, ceil_div(std::min(window, max_context) + p.rows / ratio + 1, kStep) + 1 +
@@ -31,7 +42,7 @@ AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, i
   // 17 in three), and ragged contexts even out less in larger ones (7 sequences
   // of up to 2301: 29 us in two chunks, 25 in four; two of 131072: 76 us in
   // 16, 65 in 32, 73 in 64).
-  const int64_t blocks = seqs * kv_heads * p.row_tiles, fill = 2 * device_cus();
+  const int64_t blocks = seqs * kv_heads * p.row_tiles;
   const int64_t want = 4 * blocks >= 3 * fill ? 1 : std::max<int64_t>(1, std::min(ceil_div(fill, blocks), steps / 24));
   const int64_t round = p.ws ? kWaves * p.pk : 8;         // steps of a round of the wavefronts, or two of a block
   p.chunk = want == 1 ? std::max<int64_t>(steps, 1)
@@ -88,7 +99,7 @@ extern "C" int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_he
   const size_t need = workspace_bytes_of(p, T, q_heads, head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QMM_EWORKSPACE;
   if (need > 0 && !aligned(workspace, 16)) return QMM_EALIGN;
-  if (p.blocks >= (int64_t{1} << 31)) return QMM_ERANGE;
+  if (p.blocks >= (int64_t{1} << 24)) return QMM_ERANGE;
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_ts = q_token_stride;

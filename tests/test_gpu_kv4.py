@@ -370,6 +370,17 @@ def test_values_of_very_different_sizes(queries, rise):
 
 @pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("D,group", FORMATS)
+def test_a_few_queries_of_many_sequences(dtype, D, group):
+    """Enough sequences to fill the chip with blocks of 32 rows each."""
+    note(f"kv4 many sequences D={D} group={group} {dtype}")
+    queries = [5, 1, 4, 0, 5, 3, 2, 5] * 10
+    b = Batch(18 + D + group, dtype, D, group, 16, 16, 4, [(7 * i) % 61 + 5 * (i % 3 == 0) for i in range(80)], queries)
+    b.check(b.run())
+    b.check(b.run(window=9, sinks=2), window=9, sinks=2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
 def test_chunks_over_split_keys(dtype, D, group):
     """Few rows and heads over a long context: blocks share the keys, for chunks and for a few queries alike."""
     note(f"kv4 split chunks D={D} group={group} {dtype}")

@@ -54,7 +54,7 @@ def test_append_and_read_errors():
         assert f(*a(**kw)) == EINVAL, kw
     for kw in [dict(dt=F32), dict(dt=I32), dict(D=96), dict(page=24), dict(group=48), dict(D=64, group=128)]:
         assert f(*a(**kw)) == EUNSUP, kw
-    for kw in [dict(T=1 << 31), dict(pages=1 << 31), dict(heads=5000), dict(kts=1 << 26), dict(vts=-(1 << 26))]:
+    for kw in [dict(T=1 << 25), dict(T=1 << 31), dict(pages=1 << 31), dict(heads=5000), dict(kts=1 << 26), dict(vts=-(1 << 26))]:
         assert f(*a(**kw)) == ERANGE, kw
     for kw in [dict(k=MIS), dict(v=MIS), dict(cache=MIS), dict(slots=P + 4), dict(kts=1020), dict(vhs=4)]:
         assert f(*a(**kw)) == EALIGN, kw
@@ -73,7 +73,7 @@ def test_copy_errors():
     assert f(P, 1, 4, 0, P, P, 1, None) == EINVAL and f(P, 1, 4, 64, P, P, -1, None) == EINVAL
     assert f(P, 1, 4, 72, P, P, 1, None) == EALIGN and f(MIS, 1, 4, 64, P, P, 1, None) == EALIGN
     assert f(P, 1, 4, 64, P + 4, P, 1, None) == EALIGN
-    assert f(P, 70000, 4, 64, P, P, 1, None) == ERANGE and f(P, 1, 4, 64, P, P, 1 << 31, None) == ERANGE
+    assert f(P, 70000, 4, 64, P, P, 1, None) == ERANGE and f(P, 1, 4, 64, P, P, 1 << 24, None) == ERANGE
 
 
 def attention_args(**k):
@@ -134,14 +134,14 @@ def test_rope_errors():
         assert f(*a(**kw)) == EINVAL, kw
     for kw in [dict(dt=F32), dict(wdt=F16), dict(D=132), dict(D=520, rot=16), dict(rot=24), dict(rot=144)]:
         assert f(*a(**kw)) == EUNSUP, kw
-    assert f(*a(T=1 << 31)) == ERANGE and f(*a(hq=70000)) == ERANGE
+    assert f(*a(T=1 << 24)) == ERANGE and f(*a(hq=70000)) == ERANGE
     for kw in [dict(q=MIS), dict(ko=MIS), dict(qw=MIS), dict(table=P + 8), dict(pos=P + 4), dict(qts=4100), dict(kts=1028)]:
         assert f(*a(**kw)) == EALIGN, kw
     g = qmm.lib().rope_table
     host = ctypes.cast((ctypes.c_double * 2)(1.0, 0.1), ctypes.c_void_p)
     d = ctypes.c_double(1.0)
     assert g(None, 2, 4, d, P, None) == EINVAL and g(host, 0, 4, d, P, None) == EINVAL and g(host, 2, 0, d, P, None) == EINVAL
-    assert g(host, 257, 4, d, P, None) == EUNSUP and g(host, 2, 1 << 31, d, P, None) == ERANGE
+    assert g(host, 257, 4, d, P, None) == EUNSUP and g(host, 2, 1 << 30, d, P, None) == ERANGE
     assert g(host, 2, 4, d, MIS, None) == EALIGN
 
 
