@@ -19,6 +19,8 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
+from .kv_pages import KvPages
+
 __all__ = [
     "QmmError", "lib", "library_path", "F32", "F16", "BF16", "I32", "GROUP", "SQ_STATIC_SCRATCH_BYTES",
     "w4_sizes", "wq_sizes", "quantize_groupwise", "quantize_groupwise_symmetric", "quantize_groupwise_ex",
@@ -29,7 +31,7 @@ __all__ = [
     "fp8_quantize", "fp8_gemm", "fp8_w8a8_gemm",
     "llm_int8_outliers", "llm_int8_workspace_bytes", "llm_int8_gemm", "awq_workspace_bytes", "awq_search", "stream_read",
     "kv4_cache", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention_workspace_bytes",
-    "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope",
+    "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope", "KvPages",
 ]
 
 F32, F16, BF16, I32 = 0, 1, 2, 3
