@@ -15,6 +15,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -103,6 +104,11 @@ _SIGS = {
                       _F, _P, _P, _P], _I),
     "rope_table": ([_P, _I64, _I64, ctypes.c_double, _P, _P], _I),
 }
+# The calls of a decode step with their arguments as one block of 8-byte words (include/qmm_blocks.h): ctypes converts
+# one argument and not up to 27 (kv4_attention: 3.8 us a call by arguments, 0.7 by a block).
+_BLOCKS = {name: struct.Struct("=" + "".join("d" if t is _F else "q" for t in _SIGS[name][0]))
+           for name in ("kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention", "qk_norm_rope")}
+_SIGS.update({name + "_block": ([ctypes.c_char_p], _I) for name in _BLOCKS})
 
 
 def lib() -> ctypes.CDLL:
@@ -125,6 +131,16 @@ def _call(name: str, *args) -> None:
     st = getattr(lib(), name)(*args)
     if st != 0:
         raise QmmError(name, st)
+
+
+def _call_block(name: str, *args) -> None:
+    st = getattr(lib(), name + "_block")(_BLOCKS[name].pack(*args))
+    if st != 0:
+        raise QmmError(name, st)
+
+
+def _ptr0(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -778,6 +794,11 @@ def _strides(t, name: str):
     return ts, hs
 
 
+def _fresh(t: torch.Tensor, shape) -> torch.Tensor:
+    """A dense tensor of t's shape and type (empty_like is half of new_empty's time, but keeps strides)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape)
+
+
 def _vector(t, name: str, dtype, n: int) -> None:
     if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != (n,):
         _req(t, name, (dtype,), shape=(n,))
@@ -811,8 +832,8 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: tor
     vt, vh = _strides(v, "v")
     _vector(slots, "slots", torch.int64, T)
     _on(cache.get_device(), (k, v), cache=cache, slots=slots)
-    _call("kv4_append", k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DT[dtype], T, slots.data_ptr(), cache.data_ptr(),
-          pages, heads, D, page, group, _stream(cache))
+    _call_block("kv4_append", k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DT[dtype], T, slots.data_ptr(),
+                cache.data_ptr(), pages, heads, D, page, group, _stream(cache))
 
 
 def kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16):
@@ -825,8 +846,8 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: tor
     T = slots.shape[0]
     _on(cache.get_device(), (), cache=cache, slots=slots)
     k, v = cache.new_empty((2, T, heads, head_dim), dtype=dtype).unbind()
-    _call("kv4_read", cache.data_ptr(), pages, heads, head_dim, page, group, slots.data_ptr(), T, k.data_ptr(),
-          v.data_ptr(), _DT[dtype], _stream(cache))
+    _call_block("kv4_read", cache.data_ptr(), pages, heads, head_dim, page, group, slots.data_ptr(), T, k.data_ptr(),
+                v.data_ptr(), _DT[dtype], _stream(cache))
     return k, v
 
 
@@ -841,8 +862,8 @@ def kv4_copy_pages(cache: torch.Tensor, src: torch.Tensor, dst: torch.Tensor) ->
     _vector(dst, "dst", torch.int64, n)
     _on(cache.get_device(), (), cache=cache, src=src, dst=dst)
     *layers, pages, heads, page, token = cache.shape
-    _call("kv4_copy_pages", cache.data_ptr(), layers[0] if layers else 1, pages, heads * page * token, src.data_ptr(),
-          dst.data_ptr(), n, _stream(cache))
+    _call_block("kv4_copy_pages", cache.data_ptr(), layers[0] if layers else 1, pages, heads * page * token,
+                src.data_ptr(), dst.data_ptr(), n, _stream(cache))
 
 
 @functools.lru_cache(maxsize=4096)      # of sizes alone
@@ -897,12 +918,12 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
     elif need:
         workspace = cache.new_empty(need)
     if out is None:
-        out = q.new_empty(shape)
+        out = _fresh(q, shape)
     lse = q.new_empty((T, q_heads), dtype=torch.float32) if return_lse else None
-    _call("kv4_attention", q.data_ptr(), qt, qh, _DT[dtype], T, q_heads, _ptr(cu_q), seqs, most, context.data_ptr(),
-          page_table.data_ptr(), width, stride, cache.data_ptr(), pages, kv_heads, D, page, group,
-          D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(lse), _ptr(workspace),
-          need if workspace is not None else 0, _stream(q))
+    _call_block("kv4_attention", q.data_ptr(), qt, qh, _DT[dtype], T, q_heads, _ptr0(cu_q), seqs, most,
+                context.data_ptr(), page_table.data_ptr(), width, stride, cache.data_ptr(), pages, kv_heads, D, page,
+                group, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr0(lse), _ptr0(workspace),
+                need if workspace is not None else 0, _stream(q))
     return (out, lse) if return_lse else out
 
 
@@ -1008,10 +1029,10 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     _on(q.get_device(), (k,), q_weight=q_weight, k_weight=k_weight, positions=positions, table=table, q_out=q_out,
         k_out=k_out)
     if q_out is None:
-        q_out = q.new_empty(shape)
+        q_out = _fresh(q, shape)
     if k is not None and k_out is None:
-        k_out = k.new_empty(k_shape)
-    _call("qk_norm_rope", q.data_ptr(), qt, qh, q_heads, _ptr(k), kt, kh, k_heads, _DT[dtype], T, D, _ptr(positions),
-          _ptr(table), rows, rot, interleaved, _ptr(q_weight), _ptr(k_weight), _DT[w_dtype], eps, q_out.data_ptr(),
-          _ptr(k_out), _stream(q))
+        k_out = _fresh(k, k_shape)
+    _call_block("qk_norm_rope", q.data_ptr(), qt, qh, q_heads, _ptr0(k), kt, kh, k_heads, _DT[dtype], T, D,
+                _ptr0(positions), _ptr0(table), rows, rot, interleaved, _ptr0(q_weight), _ptr0(k_weight), _DT[w_dtype],
+                eps, q_out.data_ptr(), _ptr0(k_out), _stream(q))
     return q_out, k_out

@@ -26,7 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["abi.hip", "quantize.hip", "w4a16.hip", "w8a8.hip", "w8a16.hip", "formats.hip", "awq.hip",
            "kv4.hip", "kv4_attention.hip", "kv4_attention_bf16.hip", "kv4_attention_f16.hip",
-           "rope.hip"]
+           "rope.hip", "blocks.hip"]
 
 # Per-source extra flags.  The MFMA kernels keep their accumulators in
 # ordinary VGPRs: with the default accumulator-register form the register

@@ -304,3 +304,26 @@ def test_reference_attention_against_sums_of_one_key():
     assert n.tolist() == [2, 2, 2] and np.allclose(out[2, 0], (v[0, 0] + v[3, 0]) / 2)
     out, lse, _, n = ref.attention(q, [k], [v], [4], [3], 1.0, here=[np.array([False] * 4)])
     assert n.tolist() == [0, 0, 0] and (out == 0).all() and np.isneginf(lse).all()
+
+
+def test_blocks_are_the_calls():
+    """<name>_block: the same statuses for the same arguments, a word each; floating-point ones as double."""
+    lib = qmm.lib()
+    value = lambda x: 0 if x is None else getattr(x, "value", x)
+    calls = {"kv4_append": [append_args(), append_args(T=0, k=None), append_args(D=96), append_args(k=MIS), append_args(T=-1)],
+             "kv4_attention": [attention_args(T=0), attention_args(D=96), attention_args(q=MIS), attention_args(hq=33),
+                               attention_args(scale=float("nan")), attention_args(width=2000, stride=2000, ws=None)],
+             "kv4_read": [[P, 10, 8, 96, 64, 64, P, 4, P, P, BF16, None], [P, 10, 8, 128, 64, 64, P, 4, MIS, P, BF16, None]],
+             "kv4_copy_pages": [[P, 1, 4, 72, P, P, 1, None], [P, 0, 4, 64, P, P, 1, None], [P, 1, 4, 64, P, P, 0, None]],
+             "qk_norm_rope": [[P, 4096, 128, 32, P, 1024, 128, 8, BF16, 4, 128, P, P, 100, 24, 0, P, P, BF16,
+                               ctypes.c_float(1e-6), P, P, None],
+                              [P, 4096, 128, 32, P, 1024, 128, 8, BF16, 4, 128, P, P, 100, 128, 0, P, P, BF16,
+                               ctypes.c_float(-1.0), P, P, None]]}
+    launched = {("kv4_append", 0)}                   # valid, so it would launch: nothing to compare without a GPU
+    for name, lists in calls.items():
+        block = getattr(lib, name + "_block")
+        assert block(None) == EINVAL
+        for i, args in enumerate(lists):
+            if (name, i) not in launched:
+                want = getattr(lib, name)(*args)
+                assert block(qmm._BLOCKS[name].pack(*map(value, args))) == want, (name, i)
