@@ -8,16 +8,22 @@
 namespace qmm {
 namespace {
 
+constexpr int64_t kLeastSteps = 24;     // of a block whose sequence is split
+
 // How the work is cut.  Up to 96 rows the wavefronts of a block share the rows
 // and split the keys; beyond, each has rows of its own, of shared operands
 // (32 sequences of 4000 tokens, 8 kv heads, D 128 in one group, us: 64 rows
 // 71 shared, 124 own; 96 rows 107, 136; 128 rows 133, 149; 256 rows 252, 182;
 // in groups of 64: 96 rows 133, 156; 128 rows 165, 157; 256 rows 314, 305).
 // The fewer the rows, the more steps a wavefront takes at once; where a tile
-// for every 8 (16) rows leaves most of the chip empty, blocks of fewer rows are
-// the better ones (groups of 64, 16 rows: 8 sequences of 2000 tokens 19.6 us
-// in pairs of steps, 22.2 in single ones, 32 of 4000 54 and 49; 20 rows: 8
-// sequences 22.7 us in tiles of 16, 28.1 of 32, 32 of them 69 and 61).
+// for every 8 rows leaves the chip three quarters empty (half, where the keys
+// are too few to be split over blocks), blocks of 8 rows in pairs of steps are
+// the better ones, where one for every 16 leaves it not full, those of 16 are
+// (us, D 128 in groups of 64, 8 kv heads, 16 rows: 8 sequences of 2000 tokens
+// 20.0 in tiles of 8, 22.5 of 16, 16 of 1000 16.3 and 18.5, 16 of 2000 27.6
+// and 25.4, 32 of 4000 54 and 49; 20 rows: 4 of 2000 19.9 and 22.2, 8 of 2000
+// 25.3 and 22.9, there in tiles of 32 28.1; 32 of 4000 69 in tiles of 16, 61
+// of 32).
 // Keys are split over blocks only where rows and heads leave compute units idle.
 AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, int64_t D, int group,
                  int64_t max_context, int64_t window, int64_t sinks) {
@@ -25,8 +31,11 @@ AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, i
   p.max_q = max_q;
   const int64_t rows = max_q * ratio, fill = 2 * device_cus();
   p.ws = rows <= 96;
-  const bool eights = rows <= 8 || (rows <= 16 && 4 * seqs * kv_heads * ceil_div(rows, 8) <= fill);
-  const bool sixteens = rows <= 16 || seqs * kv_heads * ceil_div(rows, 16) < fill;
+  const int64_t kept = std::min(window, max_context) + std::min(sinks, max_context);
+  const int64_t keys = window > 0 ? std::min(max_context, kept) : max_context;
+  const bool whole = keys < 2 * kLeastSteps * kStep;
+  const bool eights = rows <= 8 || (p.ws && (whole ? 2 : 4) * seqs * kv_heads * ceil_div(rows, 8) <= fill);
+  const bool sixteens = eights || rows <= 16 || seqs * kv_heads * ceil_div(rows, 16) < fill;
   p.pk = eights && attention_pairs(static_cast<int>(D), group) ? 2 : 1;
   p.nt = !p.ws ? attention_chunk_tiles(static_cast<int>(D), group)
                : sixteens ? 1 : attention_tiles(static_cast<int>(D), group);
@@ -37,13 +46,14 @@ AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, i
   if (window > 0)
     steps = std::min(steps, ceil_div(std::min(window, max_context) + p.rows / ratio + 1, kStep) + 1 +
                                 ceil_div(std::min(sinks, max_context), kStep));
-  // Two blocks a compute unit, and no fewer than 24 steps each: the join of
+  // Two blocks a compute unit, and no fewer than kLeastSteps each: the join of
   // the chunks is a launch of its own (one sequence of 700 tokens: 13 us whole,
   // 17 in three), and ragged contexts even out less in larger ones (7 sequences
   // of up to 2301: 29 us in two chunks, 25 in four; two of 131072: 76 us in
   // 16, 65 in 32, 73 in 64).
   const int64_t blocks = seqs * kv_heads * p.row_tiles;
-  const int64_t want = 4 * blocks >= 3 * fill ? 1 : std::max<int64_t>(1, std::min(ceil_div(fill, blocks), steps / 24));
+  const int64_t want =
+      4 * blocks >= 3 * fill ? 1 : std::max<int64_t>(1, std::min(ceil_div(fill, blocks), steps / kLeastSteps));
   const int64_t round = p.ws ? kWaves * p.pk : 8;         // steps of a round of the wavefronts, or two of a block
   p.chunk = want == 1 ? std::max<int64_t>(steps, 1)
                       : std::max<int64_t>(1, (ceil_div(steps, want) + round / 2) / round) * round;
