@@ -845,7 +845,8 @@ def kv4_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: tor
     _req(slots, "slots", (torch.int64,), ndim=1)
     T = slots.shape[0]
     _on(cache.get_device(), (), cache=cache, slots=slots)
-    k, v = cache.new_empty((2, T, heads, head_dim), dtype=dtype).unbind()
+    k = cache.new_empty((T, heads, head_dim), dtype=dtype)
+    v = torch.empty_like(k)
     _call_block("kv4_read", cache.data_ptr(), pages, heads, head_dim, page, group, slots.data_ptr(), T, k.data_ptr(),
                 v.data_ptr(), _DT[dtype], _stream(cache))
     return k, v

@@ -9,7 +9,8 @@
 // one barrier a round.  What is left per score is one multiplication by the
 // key's scale (with the running base in the same operation where a head is one
 // group), the exponential, a conversion and half a packed product with the
-// value's scale; the sums of the probabilities come from the matrix cores too.
+// value's scale, and the sum of the probabilities (on the matrix cores it would
+// be the sum of their roundings, 10^-4 off where a row sees few keys).
 // (The power of two of bf16 queries is the block's.)  Three chunks of 2048
 // queries on 8192 keys, 32 and 8 heads of 128 in one group: 605 GFLOP in 845
 // us, 716 TFLOP/s, 61% of what a large bf16 product of the library reaches; two
@@ -284,7 +285,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       }
     };
 
-    f32x4 o[NT][G][MT], l[NT];
+    f32x4 o[NT][G][MT];
+    float l[NT];           // of this lane's keys
     float base[NT];
     float shrink[G];
 #pragma unroll
@@ -292,14 +294,12 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       base[n] = -INFINITY;
-      l[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      l[n] = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int y = 0; y < MT; ++y) o[n][g][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const uint32_t one2 = 0x3C003C00u;
-    const u32x4 ones{one2, one2, one2, one2};
 
     // Scores of a round, less the base they were taken at (0 before the first
     // key): products of c - z, then the keys' scales, the base in the same
@@ -467,16 +467,14 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int c = 0; c < U; ++c) {
-          u32x4 pw;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             f32x4& xs = x[n][2 * c + (e >> 1)];
             xs[2 * (e & 1)] = exp2_fast(xs[2 * (e & 1)]);
             xs[2 * (e & 1) + 1] = exp2_fast(xs[2 * (e & 1) + 1]);
-            pw[e] = pack_pair<QMM_F16>(xs[2 * (e & 1)], xs[2 * (e & 1) + 1]);
+            l[n] += xs[2 * (e & 1)] + xs[2 * (e & 1) + 1];
+            if constexpr (DT == QMM_BF16) p[n][c][e] = pack_pair<QMM_F16>(xs[2 * (e & 1)], xs[2 * (e & 1) + 1]);
           }
-          if constexpr (DT == QMM_BF16) p[n][c] = pw;
-          l[n] = mfma(ones, pw, l[n]);
         }
       }
       if (k_now.key + 16 > sq.ctx) clean_keys(k_now);
@@ -540,10 +538,10 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = row_lo + 16 * n + r;
+      const float sum = sum_over_quads(l[n]);
       if (row >= rows) continue;
       const int tok = row / a.ratio;
       const int64_t rh = static_cast<int64_t>(sq.row0 + tok) * a.q_heads + kvh * a.ratio + row - tok * a.ratio;
-      const float sum = l[n][0];
       const float inv = chunks > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
