@@ -416,12 +416,6 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       const bool whole = holes == 0 && end - first == PK * kStep && end - 1 <= pos_lo &&
                          (a.window == 0 || first > pos_hi - a.window || end <= a.sinks);
       const int mine_missing = holes >> (2 * bank);
-      // memory past the context may hold anything: scales and zero-points of 0
-      auto clean = [&](u32x4& par, int u) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          par[i] = t0 + 16 * u + 4 * kb + i < sq.ctx && !((mine_missing >> u) & 1) ? par[i] : 0u;
-      };
       // ---- scores
       const uint8_t* params = slot + 2 * bank * L::kKTile + 8 * D + 16 * kb;
       f32x4 x[NT][2];
@@ -429,8 +423,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          u32x4 par = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + g * 64);
-          if (!whole) clean(par, u);
+          const u32x4 par = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + g * 64);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float sc = kv4_scale(par[i]) * key_scale, z = kv4_zero(par[i]);
@@ -441,7 +434,14 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
             }
           }
         }
+      // The memory of a hidden key may hold anything: its scores are replaced
+      // whatever they are, and its values' scale is taken as 0 where no row of
+      // the lane sees it (0 times a NaN would be one).  Codes and zero-points
+      // are finite whatever their bits.
+      uint32_t keep[4];              // bits of the pairs of scales that remain
       if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) keep[e] = 0u;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -452,6 +452,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
               const bool seen = !((mine_missing >> u) & 1) && t <= pos[n] &&
                                 (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
               x[n][u][i] = seen ? x[n][u][i] : -INFINITY;
+              keep[2 * u + i / 2] |= seen ? 0xFFFFu << (16 * (i & 1)) : 0u;
             }
           }
       }
@@ -463,16 +464,13 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           par[u] = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + G * 64 + g * 64);
-        if (!whole) {
-          clean(par[0], 0);
-          clean(par[1], 1);
-        }
         f16x2_t top{0, 0};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t p0 = par[e >> 1][2 * (e & 1)], p1 = par[e >> 1][2 * (e & 1) + 1];
           zv[g][e] = (__builtin_amdgcn_perm(p1, p0, 0x0c060c02u) << 4) | magic_v;
           sv[g][e] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
+          if (!whole) sv[g][e] &= keep[e];
           top = pk_max(top, __builtin_bit_cast(f16x2_t, sv[g][e]));
         }
         most = pk_max(most, top * pair16(shrink[g]));

@@ -97,11 +97,16 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   // the last tiles see the most keys and go first
   for (int tile = tiles - 1 - order; tile >= 0; tile -= a.row_tiles) {
     const int blk_last = min((tile + 1) * L::kRows, rows) - 1;
-    const Steps st = steps_of(a, sq.first + tile * L::kRows / a.ratio, sq.first + blk_last / a.ratio);
+    const int blk_lo = sq.first + tile * L::kRows / a.ratio, blk_hi = sq.first + blk_last / a.ratio;
+    const Steps st = steps_of(a, blk_lo, blk_hi);
     const int chunks = max(1, (st.count + a.chunk - 1) / a.chunk);
     if (split >= chunks) continue;
     const int s_lo = split * a.chunk, s_hi = min(s_lo + a.chunk, st.count);
     const int rounds = (s_hi - s_lo + U - 1) / U;
+    // Keys that no row of the block sees: past blk_hi, in the last step, or up to
+    // `hide` and no sinks, in the step where the window begins and the one before.
+    const int hide = a.window > 0 ? blk_lo - a.window : -1;
+    const int clean_to = (st.sink_steps - s_lo) / U, clean_from = (st.count - 1 - s_lo) / U;   // rounds
     const int row_lo = tile * L::kRows + wave * 16 * NT;
     const int row_hi = min(row_lo + 16 * NT, rows) - 1;
     const int pos_lo = sq.first + row_lo / a.ratio;
@@ -205,7 +210,11 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       for (int g = 0; g < G; ++g)
         k_par[g] = __builtin_amdgcn_raw_buffer_load_b32(rs, kp_at + g * a.sh.page * 4, place * 4, 0);
     };
-    // Memory past the context may hold anything: its scales and zero-points are taken as 0.
+    // The memory of hidden keys may hold anything.  Scores are replaced whatever
+    // they are (past the context, where rows that are none may not be masked,
+    // the keys' scales are taken as 0); but 0 times a scale that is a NaN would
+    // be one, so of a key that no row of the block sees the values' scale is
+    // taken as 0.
     auto clean_keys = [&](Mine x) {
 #pragma unroll
       for (int g = 0; g < G; ++g) k_par[g] = x.key + r < sq.ctx ? k_par[g] : 0u;
@@ -231,7 +240,10 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v_par[i][e] = t0 + 16 * i + 4 * v_quad + e < sq.ctx ? v_par[i][e] : 0u;
+        for (int e = 0; e < 4; ++e) {
+          const int t = t0 + 16 * i + 4 * v_quad + e;
+          v_par[i][e] = t <= blk_hi && (t > hide || t < a.sinks) ? v_par[i][e] : 0u;
+        }
     };
     const uint32_t magic = vgpr_const(Codes64::magic);
     auto less = [](uint32_t p, uint32_t z) {       // pairs: (64 + c) + -(64 + z)
@@ -487,7 +499,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         }
       }
       if (k_now.key + 16 > sq.ctx) clean_keys(k_now);
-      if (next.key[U - 1] + kStep > sq.ctx) clean_values(next);
+      if (round < clean_to || round + 1 >= clean_from) clean_values(next);
       // ---- sums; operands of the next rounds
       {
         constexpr int kOps = U * G * MT;
