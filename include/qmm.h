@@ -572,11 +572,11 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  * At most 65535 sequences and query heads, T * q_heads below 2^31 and
  * table_width * page up to 2^30 (QMM_ERANGE).
  * Arithmetic: fp32 scores, maxima and sums; probabilities times the values'
- * scales are rounded to binary16 once.  Two ranges are shared by the rows of a
- * tile (at most 128 rows of one sequence and kv head): bf16 queries 2^31 below
- * the largest of the tile, and values whose scale lies 2^11 below the largest
- * of their channel group, lose bits of their own size.  Infinities and NaN of
- * a query stay in its row.  Results do not depend on timing (no atomics).
+ * scales are rounded to binary16 once.  Values whose scale lies 2^11 below the
+ * largest that the row sees of their channel group lose bits of their own
+ * size, and so do bf16 queries 2^31 below the largest of their tile (at most
+ * 128 rows of one sequence and kv head).  Infinities and NaN of a query stay
+ * in its row.  Results do not depend on timing (no atomics).
  * ------------------------------------------------------------------------- */
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                                      int64_t head_dim, int group, int64_t max_context, int64_t window,

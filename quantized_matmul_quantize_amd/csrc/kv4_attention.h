@@ -24,8 +24,8 @@
 // scores' largest error; bf16 operands would need 128.)  bf16 queries are first
 // scaled by a power of two, their largest to 2^14 .. 2^15: exact but for what
 // lies 2^31 below it.  p' is rounded to binary16 (2^-12) for either type of q:
-// bf16 would cost 2^-9.  Its range is kept by the two powers of two that are
-// moved only when they must be: p lies below 2^15 (and reaches 2^7 where the
+// bf16 would cost 2^-9.  Its range is kept by two powers of two of each row, of
+// the keys that it sees, that are moved only when they must be: p lies below 2^15 (and reaches 2^7 where the
 // maximum was last moved, so that what is lost below 2^-25 is 2^-32 of the
 // largest), s 2^-e below 1.  The scores, maxima and sums of p stay in fp32.
 //
@@ -123,6 +123,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ f16x2_t pk_max(f16x2_t a, f16x2_t b) { return __builtin_elementwise_max(a, b); }
 __device__ __forceinline__ f16x2_t pair16(float v) {
   return f16x2_t{static_cast<_Float16>(v), static_cast<_Float16>(v)};
+}
+// Powers of two for values of the scales that a row sees and of those it does
+// not: the row's own largest goes to 2^-3 .. 2^-2, and no other may pass 2^14,
+// as its probability of 0 would meet an infinity.  (A scale is below 2^16.)
+__device__ __forceinline__ float shrink_for(float largest) {
+  return __uint_as_float((251u - (__float_as_uint(largest) >> 23)) << 23);
+}
+__device__ __forceinline__ float shrink_for_hidden(float largest) {
+  return __uint_as_float(min(267u - (__float_as_uint(largest) >> 23), 254u) << 23);
+}
+__device__ __forceinline__ float larger(f16x2_t v) { return fmaxf(static_cast<float>(v[0]), static_cast<float>(v[1])); }
+__device__ __forceinline__ bool past_one(f16x2_t v) {
+  return v[0] > static_cast<_Float16>(1.0f) || v[1] > static_cast<_Float16>(1.0f);
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // log sum exp from the base-2 maximum and the sum
@@ -339,15 +352,14 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
     // p = 2^(x - base); base is -inf until a key is seen, then at least 2^-15
     // below and at most 2^7 above the largest x
     float base[NT], l[NT];
-    float shrink[G];        // 2^-e[g], the same in every lane
-#pragma unroll
-    for (int g = 0; g < G; ++g) shrink[g] = 32768.0f;
+    f16x2_t shrink[NT][G];  // 2^-e[g], the column's, twice
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       base[n] = -INFINITY;
       l[n] = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
+        shrink[n][g] = pair16(32768.0f);
         corr[n][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int x = 0; x < MT; ++x) o[n][g][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -438,10 +450,12 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       // whatever they are, and its values' scale is taken as 0 where no row of
       // the lane sees it (0 times a NaN would be one).  Codes and zero-points
       // are finite whatever their bits.
-      uint32_t keep[4];              // bits of the pairs of scales that remain
+      uint32_t keep[NT][4];          // bits of the pairs of scales that a row sees
       if (!whole) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) keep[e] = 0u;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) keep[n][e] = 0u;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -452,31 +466,34 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
               const bool seen = !((mine_missing >> u) & 1) && t <= pos[n] &&
                                 (a.window == 0 || t > pos[n] - a.window || t < a.sinks);
               x[n][u][i] = seen ? x[n][u][i] : -INFINITY;
-              keep[2 * u + i / 2] |= seen ? 0xFFFFu << (16 * (i & 1)) : 0u;
+              keep[n][2 * u + i / 2] |= seen ? 0xFFFFu << (16 * (i & 1)) : 0u;
             }
           }
       }
-      // ---- scales of the values, pairs of keys; the running powers of two
-      f16x2_t most{0, 0};
+      // ---- scales of the values, pairs of keys; the running powers of two, by
+      // the scales that a row sees: a key that is hidden from it, such as a later
+      // token, must not cost it bits
+      f16x2_t most[G];
+      bool grow = false;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         u32x4 par[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           par[u] = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + G * 64 + g * 64);
-        f16x2_t top{0, 0};
+        most[g] = f16x2_t{0, 0};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t p0 = par[e >> 1][2 * (e & 1)], p1 = par[e >> 1][2 * (e & 1) + 1];
           zv[g][e] = (__builtin_amdgcn_perm(p1, p0, 0x0c060c02u) << 4) | magic_v;
           sv[g][e] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
-          if (!whole) sv[g][e] &= keep[e];
-          top = pk_max(top, __builtin_bit_cast(f16x2_t, sv[g][e]));
+          if (!whole) sv[g][e] &= NT == 1 ? keep[0][e] : keep[0][e] | keep[NT - 1][e];
+          most[g] = pk_max(most[g], __builtin_bit_cast(f16x2_t, sv[g][e]));
         }
-        most = pk_max(most, top * pair16(shrink[g]));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) grow |= past_one(most[g] * shrink[n][g]);
       }
       // ---- running maximum and powers of two: one test for both
-      bool grow = most[0] > static_cast<_Float16>(1.0f) || most[1] > static_cast<_Float16>(1.0f);
       float top[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -489,23 +506,6 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       }
       if (__any(grow)) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          f16x2_t t{0, 0};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) t = pk_max(t, __builtin_bit_cast(f16x2_t, sv[g][e]));
-          const float top = wave_max(fmaxf(static_cast<float>(t[0]), static_cast<float>(t[1])));
-          // the largest scale to 2^-3 .. 2^-2; it only shrinks (a scale is below 2^16)
-          const float next_shrink = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(top) >> 23)) << 23));
-          const float f = next_shrink / shrink[g];
-          shrink[g] = next_shrink;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            corr[n][g] *= f;
-#pragma unroll
-            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
-          }
-        }
-#pragma unroll
         for (int n = 0; n < NT; ++n) {
           // 2^7 at the new maximum; columns that have seen no key stay at -inf
           const float to = fmaxf(base[n], max_over_quads(top[n]) - 7.0f);
@@ -514,17 +514,26 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           l[n] *= fade;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            corr[n][g] *= fade;
+            f16x2_t own = most[g];
+            if (NT > 1 && !whole) {
+              own = f16x2_t{0, 0};
 #pragma unroll
-            for (int y = 0; y < MT; ++y) o[n][g][y] *= fade;
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t seen = sv[g][e] & keep[n][e];
+                own = pk_max(own, __builtin_bit_cast(f16x2_t, seen));
+              }
+            }
+            const float now_shrink = static_cast<float>(shrink[n][g][0]);
+            float next_shrink = fminf(now_shrink, shrink_for(max_over_quads(larger(own))));
+            if (NT > 1) next_shrink = fminf(next_shrink, shrink_for_hidden(max_over_quads(larger(most[g]))));
+            const float f = fade * (next_shrink / now_shrink);
+            shrink[n][g] = pair16(next_shrink);
+            corr[n][g] *= f;
+#pragma unroll
+            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
           }
         }
       }
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sv[g][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, sv[g][e]) * pair16(shrink[g]));
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const float from = base[n] == -INFINITY ? 0.0f : base[n];
@@ -546,7 +555,8 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            pv[n][e] = weighted(p[n][2 * e], p[n][2 * e + 1], __builtin_bit_cast(f16x2_t, sv[g][e]));
+            pv[n][e] = weighted(p[n][2 * e], p[n][2 * e + 1],
+                                __builtin_bit_cast(f16x2_t, sv[g][e]) * shrink[n][g]);
           // row m of the first operand holds the zero-points of m's own step,
           // so column r finds its sum where 4 kb + i belongs to r's step
           corr[n][g] = mfma(u32x4{zv[g][0], zv[g][1], zv[g][2], zv[g][3]}, pv[n], corr[n][g]);
@@ -633,7 +643,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float own = PK == 1 ? corr[n][g][0] : __shfl(corr[n][g][0], r + 16 * (4 / PK) * bank, kWave);
-        const float grown = 1.0f / shrink[g];
+        const float grown = 1.0f / static_cast<float>(shrink[n][g][0]);
 #pragma unroll
         for (int y = 0; y < MT; ++y)
 #pragma unroll

@@ -103,10 +103,10 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     if (split >= chunks) continue;
     const int s_lo = split * a.chunk, s_hi = min(s_lo + a.chunk, st.count);
     const int rounds = (s_hi - s_lo + U - 1) / U;
-    // Keys that no row of the block sees: past blk_hi, in the last step, or up to
-    // `hide` and no sinks, in the step where the window begins and the one before.
+    // Keys that no row of the block sees: past blk_hi, in the last round, or up to
+    // `hide` and no sinks, in the step where the window begins and the one before
+    // (rounds that hold them are cleaned, and the sinks' with them).
     const int hide = a.window > 0 ? blk_lo - a.window : -1;
-    const int clean_to = (st.sink_steps - s_lo) / U, clean_from = (st.count - 1 - s_lo) / U;   // rounds
     const int row_lo = tile * L::kRows + wave * 16 * NT;
     const int row_hi = min(row_lo + 16 * NT, rows) - 1;
     const int pos_lo = sq.first + row_lo / a.ratio;
@@ -300,17 +300,17 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     f32x4 o[NT][G][MT];
     float l[NT];           // of this lane's keys
     float base[NT];
-    float shrink[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) shrink[g] = 32768.0f;
+    f16x2_t shrink[NT][G]; // the column's, twice
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       base[n] = -INFINITY;
       l[n] = 0.0f;
 #pragma unroll
-      for (int g = 0; g < G; ++g)
+      for (int g = 0; g < G; ++g) {
+        shrink[n][g] = pair16(32768.0f);
 #pragma unroll
         for (int y = 0; y < MT; ++y) o[n][g][y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
     }
 
     // Scores of a round, less the base they were taken at (0 before the first
@@ -352,11 +352,13 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       }
     };
     float top[NT];
+    bool hides;            // some key from some row
     // masks of a round's scores, their maxima
     auto mask = [&](const Round& now) {
       const int first = now.key[0], end = now.key[U - 1] + kStep, holes = holes_of(now);
       const bool whole = holes == 0 && end - first == U * kStep && end - 1 <= pos_lo &&
                          (a.window == 0 || first > pos_hi - a.window || end <= a.sinks);
+      hides = !whole;
       if (!whole) {
 #pragma unroll
         for (int u = 0; u < 2 * U; ++u) {
@@ -425,7 +427,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       auto pairs_of = [&](int g, int u) {          // two pairs of keys
         return *reinterpret_cast<const u32x2*>(vb + L::kVScales + (g * KEYS + 16 * u + 4 * kb) * 2);
       };
-      f16x2_t most_s[G], top2{0, 0};
+      f16x2_t most_s[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         most_s[g] = f16x2_t{0, 0};
@@ -435,39 +437,62 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           const uint32_t v0 = v.x, v1 = v.y;
           most_s[g] = pk_max(most_s[g], pk_max(__builtin_bit_cast(f16x2_t, v0), __builtin_bit_cast(f16x2_t, v1)));
         }
-        top2 = pk_max(top2, most_s[g] * pair16(shrink[g]));
       }
-      // ---- running maximum and powers of two: one test for both
-      bool grow = top2[0] > static_cast<_Float16>(1.0f) || top2[1] > static_cast<_Float16>(1.0f);
+      // ---- running maximum and powers of two: one test for both.  What is hidden
+      // from a row, such as a later token, must not cost it bits.
+      bool grow = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) grow |= top[n] > limit[n];
+      for (int n = 0; n < NT; ++n) {
+        grow |= top[n] > limit[n];
+#pragma unroll
+        for (int g = 0; g < G; ++g) grow |= past_one(most_s[g] * shrink[n][g]);
+      }
       if (__any(grow)) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float largest = wave_max(fmaxf(static_cast<float>(most_s[g][0]), static_cast<float>(most_s[g][1])));
-          const float to = fminf(shrink[g], __uint_as_float((251u - (__float_as_uint(largest) >> 23)) << 23));
-          const float f = to / shrink[g];
-          shrink[g] = to;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float to = fmaxf(base[n], max_over_quads(top[n]) + from[n] - 7.0f);
           const float fade = to == -INFINITY ? 1.0f : exp2_fast(base[n] - to);
           const float now_from = to == -INFINITY ? 0.0f : to;
+          f16x2_t own[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) own[g] = most_s[g];
+          if (hides) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) own[g] = f16x2_t{0, 0};
+#pragma unroll
+            for (int u = 0; u < 2 * U; ++u) {
+              uint32_t keep[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                keep[i] = (x[n][u][2 * i] == -INFINITY ? 0u : 0xFFFFu) |
+                          (x[n][u][2 * i + 1] == -INFINITY ? 0u : 0xFFFF0000u);
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                const u32x2 v = pairs_of(g, u);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t seen = v[i] & keep[i];
+                  own[g] = pk_max(own[g], __builtin_bit_cast(f16x2_t, seen));
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float now_shrink = static_cast<float>(shrink[n][g][0]);
+            const float next_shrink = fminf(fminf(now_shrink, shrink_for(max_over_quads(larger(own[g])))),
+                                            shrink_for_hidden(max_over_quads(larger(most_s[g]))));
+            const float f = fade * (next_shrink / now_shrink);
+            shrink[n][g] = pair16(next_shrink);
+#pragma unroll
+            for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
+          }
 #pragma unroll
           for (int u = 0; u < 2 * U; ++u) x[n][u] += from[n] - now_from;
           from[n] = now_from;
           limit[n] = to == -INFINITY ? -INFINITY : 15.0f;
           base[n] = to;
           l[n] *= fade;
-#pragma unroll
-          for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int y = 0; y < MT; ++y) o[n][g][y] *= fade;
         }
       }
       // ---- the next round's scores, this one's probabilities (where the
@@ -499,7 +524,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         }
       }
       if (k_now.key + 16 > sq.ctx) clean_keys(k_now);
-      if (round < clean_to || round + 1 >= clean_from) clean_values(next);
+      if (s_lo + (round + 1) * U <= st.sink_steps || round + 2 >= rounds) clean_values(next);
       // ---- sums; operands of the next rounds
       {
         constexpr int kOps = U * G * MT;
@@ -516,9 +541,9 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t se = e < 2 ? s01[e & 1] : s23[e & 1];
-              const f16x2_t s2 = __builtin_bit_cast(f16x2_t, se) * pair16(shrink[g]);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
+                const f16x2_t s2 = __builtin_bit_cast(f16x2_t, se) * shrink[n][g];
                 if constexpr (DT == QMM_BF16) {
                   const uint32_t pair = p[n][c][e];
                   pv[n][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, pair) * s2);
@@ -566,7 +591,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       const float inv = chunks > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float f = inv / shrink[g];
+        const float f = inv / static_cast<float>(shrink[n][g][0]);
 #pragma unroll
         for (int y = 0; y < MT; ++y) {
           const f32x4 v = o[n][g][y] * f;

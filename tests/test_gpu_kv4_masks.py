@@ -107,7 +107,6 @@ SHAPES = {"one": (4, 2, [3, 40, 333, 150, 0], [1] * 5), "few": (4, 2, [290, 150]
           "many": several(80), "chunk": (4, 2, [500, 170], [90, 61])}
 
 
-
 @pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("D,group", FORMATS)
 @pytest.mark.parametrize("shape", list(SHAPES))
@@ -122,3 +121,19 @@ def test_what_hidden_keys_hold_changes_nothing(dtype, D, group, shape):
             assert c.fill_hidden(window, sinks, word) > 0
             got = c.run(window=window, sinks=sinks)
             c.check(got, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+@pytest.mark.parametrize("shape", ["few", "some", "many", "chunk"])
+def test_later_tokens_change_nothing(dtype, D, group, shape):
+    """The last token's values are infinite (stored with the largest scale): the rows before it do not see it."""
+    note(f"kv4 later tokens D={D} group={group} {shape} {dtype}")
+    hq, hkv, lens, queries = SHAPES[shape]
+
+    def edit(b, k, v):
+        v[-1, :, ::group] = math.inf
+    c = Case(2 + D + group, dtype, D, group, 16, hq, hkv, lens, queries, edit)
+    rows = np.ones(int(c.starts[-1]), bool)
+    rows[c.starts[1:][np.array(queries) > 0] - 1] = False
+    c.check(c.run(), rows=rows)
