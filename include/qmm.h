@@ -576,7 +576,8 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  * largest that the row sees of their channel group lose bits of their own
  * size, and so do bf16 queries 2^31 below the largest of their tile (at most
  * 128 rows of one sequence and kv head).  Infinities and NaN of a query stay
- * in its row.  Results do not depend on timing (no atomics).
+ * in its row, whose out and lse are then NaN (0 and -inf where every score is
+ * -inf).  Results do not depend on timing (no atomics).
  * ------------------------------------------------------------------------- */
 size_t kv4_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t q_heads, int64_t kv_heads,
                                      int64_t head_dim, int group, int64_t max_context, int64_t window,

@@ -138,9 +138,16 @@ __device__ __forceinline__ bool past_one(f16x2_t v) {
   return v[0] > static_cast<_Float16>(1.0f) || v[1] > static_cast<_Float16>(1.0f);
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-// log sum exp from the base-2 maximum and the sum
+// log sum exp from the base-2 maximum and the sum, and what results are divided
+// by.  A sum of 0 is that of no key; one that is not a number is its row's.
 __device__ __forceinline__ float lse_of(float base, float sum) {
-  return sum > 0.0f ? (base + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+  return sum == 0.0f ? -INFINITY : (base + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+}
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+// A part's sum at the maximum of all parts: one without a maximum saw no key or
+// none that is a number, and adds what it has.
+__device__ __forceinline__ float sum_at(float sum, float m, float most) {
+  return m == -INFINITY ? sum : sum * exp2_fast(m - most);
 }
 
 // Shape of the kernel for few rows: PK as above, NT column tiles.  The
@@ -695,7 +702,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           for (int w = 0; w < kWaves * PK; ++w) {
             const int col = (w % PK) * L::kCols + rr;
             const float m = stat[(w / PK) * 32 + col];
-            sum += m == -INFINITY ? 0.0f : stat[(w / PK) * 32 + 16 + col] * exp2_fast(m - M);
+            sum += sum_at(stat[(w / PK) * 32 + 16 + col], m, M);
             v += *reinterpret_cast<const f32x4*>(all + ((w / PK) * 16 + col) * kPad + c0);
           }
           const int tok = row / a.ratio;
@@ -704,7 +711,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
             *reinterpret_cast<f32x4*>(a.part_o + (rh * a.splits + split) * D + c0) = v;
             if (c0 == 0) a.part_ml[rh * a.splits + split] = make_float2(M, sum);
           } else {
-            v *= sum > 0.0f ? 1.0f / sum : 0.0f;
+            v *= inverse_of(sum);
             *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack_pair<DT>(v.x, v.y), pack_pair<DT>(v.z, v.w)};
             if (a.lse && c0 == 0) a.lse[rh] = lse_of(M, sum);
           }
@@ -745,7 +752,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int row
     float m = -INFINITY, l = 0.0f;
     for (int c = lane; c < chunks; c += kWave) m = fmaxf(m, ml[c].x);
     m = wave_max(m);
-    for (int c = lane; c < chunks; c += kWave) l += ml[c].x == -INFINITY ? 0.0f : ml[c].y * exp2_fast(ml[c].x - m);
+    for (int c = lane; c < chunks; c += kWave) l += sum_at(ml[c].y, ml[c].x, m);
     l = wave_sum(l);
     f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -760,7 +767,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int row
     if (part == 0) {
 #pragma unroll
       for (int g = 1; g < kGroups; ++g) o += sums[g * kWide + c4];
-      o *= l > 0.0f ? 1.0f / l : 0.0f;
+      o *= inverse_of(l);
       *reinterpret_cast<u32x2*>(a.out + rh * D + 4 * c4) = u32x2{pack_pair<DT>(o.x, o.y), pack_pair<DT>(o.z, o.w)};
       if (a.lse && c4 == 0) a.lse[rh] = lse_of(m, l);
     }

@@ -588,7 +588,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       if (row >= rows) continue;
       const int tok = row / a.ratio;
       const int64_t rh = static_cast<int64_t>(sq.row0 + tok) * a.q_heads + kvh * a.ratio + row - tok * a.ratio;
-      const float inv = chunks > 1 ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = chunks > 1 ? 1.0f : inverse_of(sum);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float f = inv / static_cast<float>(shrink[n][g][0]);

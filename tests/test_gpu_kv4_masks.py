@@ -137,3 +137,20 @@ def test_later_tokens_change_nothing(dtype, D, group, shape):
     rows = np.ones(int(c.starts[-1]), bool)
     rows[c.starts[1:][np.array(queries) > 0] - 1] = False
     c.check(c.run(), rows=rows)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("hq,hkv,lens,queries", [(4, 2, [200, 70], [1, 1]), (4, 2, [200, 70], [3, 2]), (4, 2, [200, 70], [90, 5]),
+                                                 (4, 2, [3000, 700], [1, 1]), (6, 2, [3000, 700], [9, 3]),
+                                                 (6, 2, [3000, 700], [70, 25])])
+def test_a_query_that_is_not_finite_has_no_log_sum(dtype, hq, hkv, lens, queries):
+    """NaN, not the -inf of a row that sees no key: a merge by log-sum-exp would drop it without a word."""
+    note(f"kv4 not finite {lens} {queries} {dtype}")
+    c = Case(3, dtype, 128, 64, 16, hq, hkv, lens, queries)
+    q = c.q.clone()
+    q[0, 0, 5], q[1, 1, 7], q[1, 3, 100] = math.inf, math.nan, -math.inf
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool)
+    bad[0, 0] = bad[1, 1] = bad[1, 3] = True
+    out, lse = c.run(q=q)
+    assert lse[bad].isnan().all() and out[bad].isnan().all()
+    assert lse[~bad].isfinite().all() and out[~bad].isfinite().all()
