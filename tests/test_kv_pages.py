@@ -135,3 +135,108 @@ def test_errors_change_nothing():
     k.shrink(a, 1)
     assert k.table([a])[0].tolist() == [[-1, -1]] and k.length(a) == 8
     assert k.table([])[0].shape == (0, 1)
+
+
+def test_drafts_dropped_after_a_window_was_forgotten():
+    """A shorter sequence's next query sees further back: what it would see must not have been given back."""
+    for tokens, drafts, window, drop in [(106, 5, 64, 5), (200, 0, 64, 20)]:
+        k = KvPages(40, 16)
+        s = k.add()
+        k.extend([s], [tokens + drafts])
+        k.forget(s, window)
+        before = k.table([s])[0]
+        with pytest.raises(ValueError, match="forgotten"):
+            k.shrink(s, drop)
+        assert k.length(s) == tokens + drafts and torch.equal(k.table([s])[0], before)
+        k.extend([s], [1])                                            # as long as it is not shortened it goes on
+    # with room for the drafts they may be dropped, and every key that the next query sees is held
+    k = KvPages(40, 16)
+    s = k.add()
+    k.extend([s], [111])
+    k.forget(s, 64, drafts=5)
+    k.shrink(s, 5)
+    assert k.table([s])[0][0, 43 // 16:].min() >= 0 and k.table([s])[0][0, 1] == -1
+    k.extend([s], [1])
+    t = k.fork(s)
+    with pytest.raises(ValueError, match="forgotten"):                # a fork has forgotten the same
+        k.shrink(t, 20)
+    with pytest.raises(ValueError):
+        k.forget(s, 64, drafts=-1)
+    # back to before anything forgotten, among the first tokens kept
+    k = KvPages(40, 16)
+    s = k.add()
+    k.extend([s], [200])
+    k.forget(s, 32, 20)
+    k.shrink(s, 200 - 32)
+    k.extend([s], [100])
+    assert k.table([s])[0].min() >= 0
+    # a sequence that holds no page any more has nothing to go on from
+    k = KvPages(4, 4)
+    s = k.add()
+    k.extend([s], [9])
+    k.forget(s, 2)
+    k.shrink(s, 1)
+    with pytest.raises(ValueError, match="forgotten"):
+        k.extend([s], [1])
+    assert k.length(s) == 8 and k.free_pages == 4
+    k.shrink(s, 8)
+    assert k.extend([s], [1])[0].tolist() == [2 * 4]
+
+
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("page", [1, 4, 16])
+def test_a_window_never_loses_a_key(seed, page):
+    """Each sequence with a window of its own, shortened at random: a shrink is refused exactly where the next query
+    would see a forgotten token, and every new query's keys are in the table with what was written."""
+    g = np.random.Generator(np.random.PCG64(100 + seed))
+    m, sees = Model(120, page), {}
+    shrunk = 0
+
+    def missing(s, length):
+        row = m.k.table([s])[0][0].tolist()
+        window, sinks = sees[s]
+        return [j for j in range(length) if (j > length - window or j < sinks) and row[j // page] < 0]
+    for step in range(300):
+        seqs = list(m.want)
+        what = g.integers(0, 8)
+        if not seqs or (what == 0 and len(seqs) < 6):
+            s = m.k.add()
+            m.want[s], sees[s] = [], (int(g.integers(1, 4 * page + 2)), int(g.integers(0, page + 2)))
+            continue
+        s = seqs[g.integers(len(seqs))]
+        if what <= 2:
+            n = int(g.integers(1, 2 * page + 3))
+            try:
+                lost = missing(s, len(m.want[s]))
+                m.extend([s], [n], g)
+                assert not lost
+            except RuntimeError:
+                m.k.free(s)
+                del m.want[s], sees[s]
+            except ValueError:
+                assert lost and all(p < 0 for p in m.k.table([s])[0][0].tolist())
+                m.k.free(s)
+                del m.want[s], sees[s]
+        elif what == 3:
+            t = m.k.fork(s)
+            m.want[t], sees[t] = list(m.want[s]), sees[s]
+        elif what <= 5:
+            window, sinks = sees[s]
+            drafts = int(g.integers(0, page + 1))
+            m.k.forget(s, window, sinks, drafts)
+            n = len(m.want[s]) - drafts
+            m.want[s] = [w if j < sinks or j > n - window else None for j, w in enumerate(m.want[s])]
+        else:
+            n = int(g.integers(0, min(len(m.want[s]), 2 * page) + 1))
+            length = len(m.want[s]) - n
+            lost, row = missing(s, length), m.k.table([s])[0][0].tolist()
+            into = length % page and row[length // page] < 0
+            try:
+                m.k.shrink(s, n)
+                shrunk += 1
+                assert not into and (not lost or all(p < 0 for p in row[:-(-length // page)]))
+                m.want[s] = m.want[s][:length]
+            except ValueError:
+                assert into or lost
+        m.check()
+    assert shrunk > 5
