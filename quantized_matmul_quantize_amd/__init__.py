@@ -939,8 +939,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = N
       "ntk"         the base raised by factor^(rot / (rot - 2)), so the slowest pair is interpolated, the fastest kept;
       "wavelength"  a pair that turns more than `high` (default 4) times in the original context keeps its frequency,
                     one that turns less than `low` times is divided by factor, linear in the turns between;
-      "yarn"        the same two ends (high default 32), linear in the pair's index between, and the rotated channels
-                    grow by 0.1 ln(factor) + 1."""
+      "yarn"        the same two ends (high default 32), linear in the pair's index between (where every pair turns
+                    more than `low` times, the ramp goes on past the last one), and the rotated channels grow by
+                    0.1 ln(factor) + 1."""
     if rot < 2 or rot % 2:
         raise ValueError(f"rot must be even and positive, not {rot}")
     if base <= 0 or factor <= 0:
@@ -965,7 +966,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: Optional[str] = N
         keep = [min(1.0, max(0.0, (original * v / (2 * math.pi) - low) / (high - low))) for v in f]
         return [k * v + (1.0 - k) * v / factor for k, v in zip(keep, f)], 1.0
     index = lambda turns: half * math.log(original / (2 * math.pi * turns)) / math.log(base)
-    first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), half - 1)
+    first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), rot - 1)
     keep = [1.0 - min(1.0, max(0.0, (i - first) / max(last - first, 0.001))) for i in range(half)]
     return [k * v + (1.0 - k) * v / factor for k, v in zip(keep, f)], \
         0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0

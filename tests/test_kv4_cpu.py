@@ -327,3 +327,19 @@ def test_blocks_are_the_calls():
             if (name, i) not in launched:
                 want = getattr(lib, name)(*args)
                 assert block(qmm._BLOCKS[name].pack(*map(value, args))) == want, (name, i)
+
+
+@pytest.mark.parametrize("kw", [dict(base=10000.0, original=131072), dict(base=500000.0, original=4 * 10 ** 6),
+                                dict(base=10000.0, original=4096), dict(base=500000.0, original=8192)])
+def test_yarn_ramp_is_linear_between_its_ends(kw):
+    """Also where every pair turns more than `low` times in the original context, so that the ramp's end lies past the
+    last pair (a ramp held to the last pair would divide it fully)."""
+    rot, factor, low, high = 128, 8.0, 1.0, 32.0
+    y, _ = qmm.rope_frequencies(rot, scaling="yarn", factor=factor, low=low, high=high, **kw)
+    f = np.array(qmm.rope_frequencies(rot, base=kw["base"])[0])
+    # f_i turns original f_i / 2 pi times: i of a given number of turns, to whole pairs outwards
+    at = lambda turns: rot / 2 * math.log(kw["original"] / (2 * math.pi * turns)) / math.log(kw["base"])
+    first, last = max(math.floor(at(high)), 0), math.ceil(at(low))
+    keep = 1 - np.clip((np.arange(rot // 2) - first) / (last - first), 0, 1)
+    assert np.allclose(y, f * (keep + (1 - keep) / factor), rtol=1e-13)
+    assert last < 64 or (y[-1] > 1.01 * f[-1] / factor)
