@@ -556,8 +556,8 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  *           consecutive, strides in elements, multiples of 8; 16-byte aligned.
  * cu_q    : int32 [seqs + 1], device: sequence b's queries are rows cu_q[b] ..
  *           cu_q[b + 1] - 1 of q; NULL when every sequence has one (T == seqs).
- * max_q   : the most queries of a sequence (at least 1).  A hint: it only
- *           shapes the launch.
+ * max_q   : the most queries of a sequence (at least 1; 1 without cu_q).  A
+ *           hint: it only shapes the launch and the workspace.
  *           Rows of q in no sequence are not written in out and lse.
  * context : int32 [seqs], device; at most table_width * page is used.
  * page_table : int32 [seqs, table_width], rows table_stride elements apart.
@@ -569,8 +569,8 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  * workspace : device memory of at least kv4_attention_workspace_bytes bytes
  *           with the same arguments (max_context = table_width * page), which
  *           may be 0; 16-byte aligned, no clearing needed.
- * At most 65535 sequences and query heads, T * q_heads below 2^31 and
- * table_width * page up to 2^30 (QMM_ERANGE).
+ * At most 65535 sequences and query heads, T * q_heads below 2^31,
+ * seqs * kv_heads below 2^24 and table_width * page up to 2^30 (QMM_ERANGE).
  * Arithmetic: fp32 scores, maxima and sums; probabilities times the values'
  * scales are rounded to binary16 once.  Values whose scale lies 2^11 below the
  * largest that the row sees of their channel group lose bits of their own

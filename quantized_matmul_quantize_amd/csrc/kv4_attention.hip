@@ -104,7 +104,7 @@ extern "C" int kv4_attention(const void* q, int64_t q_token_stride, int64_t q_he
       !aligned(cu_q, 4) || !aligned(page_table, 4) || ((q_token_stride | q_head_stride) & 7))
     return QMM_EALIGN;
   const int64_t ratio = q_heads / kv_heads, tokens = table_width * page;
-  const AttnPlan p = plan_of(seqs, cu_q ? std::min(max_q, T) : 1, ratio, kv_heads, head_dim, group, tokens,
+  const AttnPlan p = plan_of(seqs, std::min(max_q, T), ratio, kv_heads, head_dim, group, tokens,
                              window, sinks);
   const size_t need = workspace_bytes_of(p, T, q_heads, head_dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QMM_EWORKSPACE;

@@ -343,3 +343,18 @@ def test_yarn_ramp_is_linear_between_its_ends(kw):
     keep = 1 - np.clip((np.arange(rot // 2) - first) / (last - first), 0, 1)
     assert np.allclose(y, f * (keep + (1 - keep) / factor), rtol=1e-13)
     assert last < 64 or (y[-1] > 1.01 * f[-1] / factor)
+
+
+def test_workspace_of_one_query_each_whatever_the_hint():
+    """Without cu_q a call needs what the size query says for the same arguments, the hint included."""
+    f, w = qmm.lib().kv4_attention, qmm.lib().kv4_attention_workspace_bytes
+    differ = 0
+    for seqs, width in [(4, 2000), (16, 500), (64, 2000), (8, 100)]:
+        for max_q in (1, 3, 16, 64):
+            need = w(seqs, seqs, max_q, 32, 8, 128, 64, width * 64, 0, 0)
+            differ += need != w(seqs, seqs, 1, 32, 8, 128, 64, width * 64, 0, 0)
+            args = dict(T=seqs, seqs=seqs, max_q=max_q, width=width, stride=width, ws=MIS)
+            if need:
+                assert f(*attention_args(wsb=need, **args)) == EALIGN      # enough, were it aligned
+                assert f(*attention_args(wsb=need - 1, **args)) == EWS
+    assert differ > 0
