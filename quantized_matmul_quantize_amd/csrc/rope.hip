@@ -143,7 +143,10 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(HeadRows q, HeadRows 
         if (lanes >= 32) sum += __shfl_xor(sum, 16, kWave);
         if (lanes >= 64) sum += __shfl_xor(sum, 32, kWave);
         if (is_q ? q.weight != nullptr : k.weight != nullptr) {
-          const float inv = __builtin_amdgcn_rsqf(fmaf(sum, inv_d, eps));
+          // the instruction takes subnormal numbers for 0
+          const float mean = fmaf(sum, inv_d, eps);
+          const bool tiny = mean < 0x1p-126f;
+          const float inv = __builtin_amdgcn_rsqf(tiny ? mean * 0x1p64f : mean) * (tiny ? 0x1p32f : 1.0f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (is_q ? qw[i] : kw[i]);
         }

@@ -122,3 +122,12 @@ def test_table_in_64_bits(kw):
     for p in (0, 1, 77, 65535, rows - 1):
         want = np.stack([m * np.cos(p * np.array(f)), m * np.sin(p * np.array(f))], -1)
         assert np.abs(got[p] - want).max() <= m * (U + 1e-9)
+
+
+@pytest.mark.parametrize("dtype,eps", [(BF16, 0.0), (BF16, 1e-40)])
+def test_heads_whose_squares_are_subnormal(dtype, eps):
+    """Channels of 5e-20: a mean square of 2.5e-39, below fp32's normal numbers, still has a square root."""
+    q = half(rng(2).standard_normal((9, 3, 64)) * 5e-20, dtype)
+    w = half(1 + 0.3 * rng(3).standard_normal(64), dtype)
+    out, _ = qmm.qk_norm_rope(q.cuda(), None, q_weight=w.cuda(), eps=eps)
+    check(out, q, w, None, None, eps, False)
