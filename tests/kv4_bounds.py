@@ -18,8 +18,8 @@ scale of the visible keys and, of a channel's group, values):
           with 64 added, at most 79 each: (n / 16 + 32) u 158 sv;
           the output's own rounding.
 
-A probability rounded to bf16 would cost 2^-8 mass, and a key of more than
-about 2^-11 of a row's weight is missed: both are over the bound.
+Over the bound are probabilities rounded to bf16 (2^-8 each) where a row sees
+some tens of keys, and a missing value of more than about 2^-10 of the weight.
 """
 from __future__ import annotations
 

@@ -110,6 +110,16 @@ SHAPES = {"one": (4, 2, [3, 40, 333, 150, 0], [1] * 5), "few": (4, 2, [290, 150]
 @pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("D,group", FORMATS)
 @pytest.mark.parametrize("shape", list(SHAPES))
+def test_against_the_arithmetic(dtype, D, group, shape):
+    note(f"kv4 bounds D={D} group={group} {shape} {dtype}")
+    hq, hkv, lens, queries = SHAPES[shape]
+    c = Case(D + group, dtype, D, group, 16, hq, hkv, lens, queries)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+@pytest.mark.parametrize("shape", list(SHAPES))
 def test_what_hidden_keys_hold_changes_nothing(dtype, D, group, shape):
     """Only the sinks and the window are written: the other tokens of their pages hold NaN, infinities or the largest
     scale, and the table still names their pages."""

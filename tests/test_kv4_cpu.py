@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv4_bounds as bounds
 import kv4_reference as ref
 import quantized_matmul_quantize_amd as qmm
 
@@ -358,3 +359,38 @@ def test_workspace_of_one_query_each_whatever_the_hint():
                 assert f(*attention_args(wsb=need, **args)) == EALIGN      # enough, were it aligned
                 assert f(*attention_args(wsb=need - 1, **args)) == EWS
     assert differ > 0
+
+
+def test_bounds_notice_coarser_probabilities_and_missing_values():
+    """The bounds that the kernels are held to: binary16 probabilities are within them, bf16 ones are not where a row
+    sees some tens of keys, and the value of no key of a context of 200 with more than 2^-9 of the weight goes missing."""
+    g = np.random.Generator(np.random.PCG64(4))
+    D, lens = 128, [5, 33, 200]
+    q = g.standard_normal((3, 4, D)).astype(np.float16).astype(np.float32)
+    parts = [[], [], [], []]
+    for n in lens:
+        for i, x in enumerate((g.standard_normal((n, 2, D)), g.standard_normal((n, 2, D)))):
+            c, z, s = ref.quantize(x.astype(np.float16).astype(np.float32), 64)
+            parts[i].append(ref.values(c, z, s))
+            parts[2 + i].append(s.astype(np.float64))
+    run = lambda rounded=lambda p: p: bounds.attention(q, *parts, lens, [1, 1, 1], D ** -0.5, rounded=rounded)
+    out, lse, b_out, b_lse, count = run()
+    want = ref.attention(q, parts[0], parts[1], lens, [1, 1, 1], D ** -0.5)
+    assert np.allclose(out, want[0], rtol=1e-12) and np.allclose(lse, want[1], rtol=1e-12) and (count == want[3]).all()
+    bound = b_out + 2.0 ** -11 * np.abs(out)
+    err = lambda rounded: np.abs(run(rounded)[0] - out)
+    assert (err(lambda p: (128 * p).astype(np.float16) / 128.0) <= b_out).all()
+    coarse = lambda p: torch.from_numpy(p).bfloat16().double().numpy()
+    assert (err(coarse) > bound)[:2].any((1, 2)).all()          # (over 200 keys their roundings cancel)
+    missed = []
+    for j in range(200):
+        weight = []
+
+        def without(p):
+            if len(p) == 200:
+                weight.append(p[j] / p.sum())
+                p = np.where(np.arange(200) == j, 0, p)
+            return p
+        over = (err(without) > bound)[2].any(-1)
+        missed += [w for w, seen in zip(weight, over) if not seen]
+    assert max(missed, default=0) < 2.0 ** -9
