@@ -572,7 +572,8 @@ int kv4_copy_pages(uint8_t* cache, int64_t layers, int64_t pages, int64_t page_b
  * At most 65535 sequences and query heads, T * q_heads below 2^31,
  * seqs * kv_heads below 2^24 and table_width * page up to 2^30 (QMM_ERANGE).
  * Arithmetic: fp32 scores, maxima and sums; probabilities times the values'
- * scales are rounded to binary16 once.  Values whose scale lies 2^11 below the
+ * scales are rounded to binary16 (for more than 96 rows of bf16 the
+ * probabilities as well, so twice).  Values whose scale lies 2^11 below the
  * largest that the row sees of their channel group lose bits of their own
  * size, and so do bf16 queries 2^31 below the largest of their tile (at most
  * 128 rows of one sequence and kv head).  Infinities and NaN of a query stay

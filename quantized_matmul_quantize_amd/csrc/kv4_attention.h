@@ -23,11 +23,12 @@
 // offset of 64 takes one shift a word less than 16, but its rounding is the
 // scores' largest error; bf16 operands would need 128.)  bf16 queries are first
 // scaled by a power of two, their largest to 2^14 .. 2^15: exact but for what
-// lies 2^31 below it.  p' is rounded to binary16 (2^-12) for either type of q:
-// bf16 would cost 2^-9.  Its range is kept by two powers of two of each row, of
-// the keys that it sees, that are moved only when they must be: p lies below 2^15 (and reaches 2^7 where the
-// maximum was last moved, so that what is lost below 2^-25 is 2^-32 of the
-// largest), s 2^-e below 1.  The scores, maxima and sums of p stay in fp32.
+// lies 2^31 below it.  p' is rounded to binary16 (2^-11) for either type of q:
+// bf16 would cost 2^-8.  Its range is kept by two powers of two of each row, of
+// the keys that it sees, that are moved only when they must be: p lies below
+// 2^15 (and reaches 2^7 where the maximum was last moved, so that what is lost
+// below 2^-25 is 2^-32 of the largest), s 2^-e below 1.  The scores, maxima and
+// sums of p stay in fp32.
 //
 // What bounds decode is the vector unit, not the matrix cores: two operations
 // a pair of codes to make operands of them, and then the arithmetic on the
@@ -37,9 +38,9 @@
 // of their own, and are joined at the end, as the wavefronts are.  (Four steps
 // at once for 4 rows: 220 instead of 250 vector operations a step, but 70 KiB
 // of LDS a block and 58 instead of 54 us for 64 sequences of 4096 tokens.)
-// Of those 54 us (8 kv heads of 128 in one group, 243 MB: 4.5 TB/s) the loads
-// alone take 45, the arithmetic alone 44; with 2 sequences of 131072 tokens in
-// groups of 64 (293 MB) 52 and 51 of 66.
+// These take 53 us (8 kv heads of 128 in one group, 243 MB: 4.6 TB/s), of which
+// loads alone are 45, the arithmetic alone (before the row's own powers of two)
+// 44; 2 sequences of 131072 tokens in groups of 64 (293 MB) 65, of which 52, 51.
 #pragma once
 
 #include "kv4_attention_args.h"

@@ -13,17 +13,17 @@ constexpr int64_t kLeastSteps = 24;     // of a block whose sequence is split
 // How the work is cut.  Up to 96 rows the wavefronts of a block share the rows
 // and split the keys; beyond, each has rows of its own, of shared operands
 // (32 sequences of 4000 tokens, 8 kv heads, D 128 in one group, us: 64 rows
-// 71 shared, 124 own; 96 rows 107, 136; 128 rows 133, 149; 256 rows 252, 182;
-// in groups of 64: 96 rows 133, 156; 128 rows 165, 157; 256 rows 314, 305).
+// 74 shared, 130 own; 96 rows 110, 137; 128 rows 136, 148; 256 rows 259, 185;
+// in groups of 64: 96 rows 140, 160; 128 rows 172, 160; 256 rows 329, 313).
 // The fewer the rows, the more steps a wavefront takes at once; where a tile
 // for every 8 rows leaves the chip three quarters empty (half, where the keys
 // are too few to be split over blocks), blocks of 8 rows in pairs of steps are
 // the better ones, where one for every 16 leaves it not full, those of 16 are
 // (us, D 128 in groups of 64, 8 kv heads, 16 rows: 8 sequences of 2000 tokens
-// 20.0 in tiles of 8, 22.5 of 16, 16 of 1000 16.3 and 18.5, 16 of 2000 27.6
-// and 25.4, 32 of 4000 54 and 49; 20 rows: 4 of 2000 19.9 and 22.2, 8 of 2000
-// 25.3 and 22.9, there in tiles of 32 28.1; 32 of 4000 69 in tiles of 16, 61
-// of 32).
+// 17.9 in tiles of 8, 20.3 of 16, 16 of 1000 14.3 and 16.3, 16 of 2000 26.3
+// and 23.7, 32 of 4000 51 and 46; 20 rows: 4 of 2000 18.1 and 20.1, 8 of 2000
+// 24.0 and 21.2, there in tiles of 32 29.0; 32 of 4000 in tiles of 16 and of
+// 32: 20 rows 67 and 64, 48 rows 81 and 91, 64 rows 106 and 91).
 // Keys are split over blocks only where rows and heads leave compute units idle.
 AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, int64_t D, int group,
                  int64_t max_context, int64_t window, int64_t sinks) {
@@ -47,10 +47,11 @@ AttnPlan plan_of(int64_t seqs, int64_t max_q, int64_t ratio, int64_t kv_heads, i
     steps = std::min(steps, ceil_div(std::min(window, max_context) + p.rows / ratio + 1, kStep) + 1 +
                                 ceil_div(std::min(sinks, max_context), kStep));
   // Two blocks a compute unit, and no fewer than kLeastSteps each: the join of
-  // the chunks is a launch of its own (one sequence of 700 tokens: 13 us whole,
-  // 17 in three), and ragged contexts even out less in larger ones (7 sequences
-  // of up to 2301: 29 us in two chunks, 25 in four; two of 131072: 76 us in
-  // 16, 65 in 32, 73 in 64).
+  // the chunks is a launch of its own (one sequence of 700 tokens: 11.6 us a
+  // call whole, 14.3 in three; in a captured graph 11.4 and 11.0), and ragged
+  // contexts even out less in larger ones (7 sequences of up to 2301: 29 us in
+  // two chunks, 24 in three, 31 in four; two of 131072: 76 us in 16, 65 in 32,
+  // 72 in 57).
   const int64_t blocks = seqs * kv_heads * p.row_tiles;
   const int64_t want =
       4 * blocks >= 3 * fill ? 1 : std::max<int64_t>(1, std::min(ceil_div(fill, blocks), steps / kLeastSteps));

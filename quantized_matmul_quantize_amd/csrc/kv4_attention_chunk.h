@@ -12,8 +12,11 @@
 // value's scale, and the sum of the probabilities (on the matrix cores it would
 // be the sum of their roundings, 10^-4 off where a row sees few keys).
 // (The power of two of bf16 queries is the block's.)  Three chunks of 2048
-// queries on 8192 keys, 32 and 8 heads of 128 in one group: 605 GFLOP in 835
-// us, 725 TFLOP/s, 61% of what a large bf16 product of the library reaches; two
+// queries on 8192 keys, 32 and 8 heads of 128 in one group: 605 GFLOP in 855
+// us, 708 TFLOP/s, 60% of what a large bf16 product of the library reaches (with
+// powers of two shared by the rows of a tile 834 us, but a hidden token's scale
+// then cost other rows their bits); in groups of 64 each operand is read for one
+// tile of rows only, 2 x 1024 queries on 6000 keys 216 us, 403 TFLOP/s; two
 // wavefronts a SIMD (the sums hold the registers) leave part of the LDS latency
 // and of the exponentials uncovered.
 #pragma once
@@ -495,11 +498,14 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           l[n] *= fade;
         }
       }
-      // ---- the next round's scores, this one's probabilities (where the
-      // output is bf16, rounded to binary16 before the values' scale as well).
-      // The empty asm keeps a pair's sum and conversion at its exponentials:
-      // moved away by the compiler they hold registers, and with the spills a
-      // prompt's chunk took 1122 instead of 840 us.
+      // ---- the next round's scores, this one's probabilities.  Where the output
+      // is bf16 (2^-8 of it) they are rounded to binary16 here and once more with
+      // the values' scale, 2^-10 of a row's mass: held in fp32 until then, three
+      // chunks of prompts take 941 instead of 902 us, 2 x 1024 queries on 6000
+      // keys in groups of 32 349 instead of 281.  The empty asm keeps a pair's
+      // sum and conversion at its exponentials: moved away by the compiler they
+      // hold registers, and with the spills a prompt's chunk took 1122 instead of
+      // 832 us.
       u32x4 p[NT][U];
       f32x4 ahead[NT][2 * U];
       scores(&k_lds[(round + 1) & 1][0], ahead);
