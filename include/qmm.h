@@ -622,6 +622,28 @@ int qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, i
  * aligned; rows * half < 2^31 (QMM_ERANGE). */
 int rope_table(const double* inv_freq, int64_t half, int64_t rows, double m, float* table, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * kv4_rope_append -- a step's heads from the projection to the attention in
+ * one pass: q_out is what qk_norm_rope makes of q (the same bits), keys are
+ * normed and rotated by the same formulas and appended to the cache with the
+ * values by kv4_append's rule.  The keys are not rounded to dtype between: the
+ * formulas are computed in fp64 and rounded once, to fp32, before the rule, so
+ * that codes do not depend on the order of sums.
+ * Arguments as in those calls: q [T, q_heads, D] (NULL with q_heads 0), k and
+ * v [T, kv_heads, D] of dtype; rot 0 for no rotation, q_weight and k_weight
+ * NULL for no norm; slots int64 [T], a token whose slot is outside the cache
+ * has its queries computed and nothing appended.  A position outside the table
+ * gives NaN in the rotated channels (of keys: code 0).  q_out [T, q_heads, D]
+ * dense; it may be q where that is dense.  D, page and group as the cache
+ * has them; T below 2^24, q_heads up to 65535 (QMM_ERANGE).
+ * ------------------------------------------------------------------------- */
+int kv4_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads, const void* k,
+                    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                    int64_t v_head_stride, int dtype, int64_t T, const int64_t* positions, const float* table,
+                    int64_t table_rows, int64_t rot, int interleaved, const void* q_weight, const void* k_weight,
+                    int w_dtype, float eps, const int64_t* slots, uint8_t* cache, int64_t pages, int64_t kv_heads,
+                    int64_t head_dim, int64_t page, int group, void* q_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

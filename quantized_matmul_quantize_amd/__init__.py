@@ -33,6 +33,7 @@ __all__ = [
     "llm_int8_outliers", "llm_int8_workspace_bytes", "llm_int8_gemm", "awq_workspace_bytes", "awq_search", "stream_read",
     "kv4_cache", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention_workspace_bytes",
     "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope", "KvPages",
+    "kv4_rope_append",
 ]
 
 F32, F16, BF16, I32 = 0, 1, 2, 3
@@ -103,11 +104,14 @@ _SIGS = {
     "qk_norm_rope": ([_P, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I, _I64, _I64, _P, _P, _I64, _I64, _I, _P, _P, _I,
                       _F, _P, _P, _P], _I),
     "rope_table": ([_P, _I64, _I64, ctypes.c_double, _P, _P], _I),
+    "kv4_rope_append": ([_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _I, _P, _P,
+                         _I, _F, _P, _P, _I64, _I64, _I64, _I64, _I, _P, _P], _I),
 }
 # The calls of a decode step with their arguments as one block of 8-byte words (include/qmm_blocks.h): ctypes converts
 # one argument and not up to 27 (kv4_attention: 3.8 us a call by arguments, 0.7 by a block).
 _BLOCKS = {name: struct.Struct("=" + "".join("d" if t is _F else "q" for t in _SIGS[name][0]))
-           for name in ("kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention", "qk_norm_rope")}
+           for name in ("kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention", "qk_norm_rope",
+                        "kv4_rope_append")}
 _SIGS.update({name + "_block": ([ctypes.c_char_p], _I) for name in _BLOCKS})
 
 
@@ -1038,3 +1042,62 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
                 _ptr0(positions), _ptr0(table), rows, rot, interleaved, _ptr0(q_weight), _ptr0(k_weight), _DT[w_dtype],
                 eps, q_out.data_ptr(), _ptr0(k_out), _stream(q))
     return q_out, k_out
+
+
+def kv4_rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                    cache: torch.Tensor, positions: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None,
+                    q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    interleaved: bool = False, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """qk_norm_rope and kv4_append in one pass: norms and rotation of q [T, q_heads, D] and k [T, kv_heads, D], then k
+    (not rounded to its type between) and v into the slots (int64 [T]) of the cache.  Returns q_out [T, q_heads, D], bit
+    for bit qk_norm_rope's; q may be None (keys and values alone)."""
+    T, heads, D = shape = _rows(k, "k", _HALVES)
+    pages, kv_heads, page, group = _cache_shape(cache, D)
+    if heads != kv_heads:
+        raise ValueError(f"k has {heads} heads, the cache {kv_heads}")
+    dtype = k.dtype
+    if _rows(v, "v", (dtype,)) != shape:
+        _req(v, "v", (dtype,), shape=shape)
+    kt, kh = _strides(k, "k")
+    vt, vh = _strides(v, "v")
+    q_heads = qt = qh = 0
+    if q is not None:
+        q_shape = _rows(q, "q", (dtype,))
+        q_heads = q_shape[1]
+        if q_shape != (T, q_heads, D):
+            _req(q, "q", (dtype,), shape=(T, None, D))
+        qt, qh = _strides(q, "q")
+        if q_out is not None:
+            _out(q_out, q_shape, dtype, "q_out")
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    _vector(slots, "slots", torch.int64, T)
+    w_dtype = dtype
+    if q_weight is not None:
+        w_dtype = torch.float32 if q_weight.dtype is torch.float32 else dtype
+        _vector(q_weight, "q_weight", w_dtype, D)
+    if k_weight is not None:
+        if q_weight is None and k_weight.dtype is torch.float32:
+            w_dtype = torch.float32
+        _vector(k_weight, "k_weight", w_dtype, D)
+    if not eps >= 0.0:
+        raise ValueError(f"eps must be >= 0, not {eps}")
+    rows = rot = 0
+    if table is not None:
+        if type(table) is not torch.Tensor or table.dtype is not torch.float32 or table.dim() != 3 or table.shape[2] != 2:
+            _req(table, "table", (torch.float32,), shape=(None, None, 2))
+        rows, half, _ = table.shape
+        rot = 2 * half
+        if rot > D:
+            raise ValueError(f"table rotates {rot} channels of heads of {D}")
+        _vector(positions, "positions", torch.int64, T)
+    elif positions is not None:
+        raise ValueError("positions need a table")
+    _on(cache.get_device(), (q, k, v), cache=cache, slots=slots, q_weight=q_weight, k_weight=k_weight,
+        positions=positions, table=table, q_out=q_out)
+    if q is not None and q_out is None:
+        q_out = _fresh(q, q_shape)
+    _call_block("kv4_rope_append", _ptr0(q), qt, qh, q_heads, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _DT[dtype], T,
+                _ptr0(positions), _ptr0(table), rows, rot, interleaved, _ptr0(q_weight), _ptr0(k_weight), _DT[w_dtype],
+                eps, slots.data_ptr(), cache.data_ptr(), pages, heads, D, page, group, _ptr0(q_out), _stream(cache))
+    return q_out

@@ -38,3 +38,4 @@ extern "C" int kv4_read_block(const void* words) { return call(kv4_read, static_
 extern "C" int kv4_copy_pages_block(const void* words) { return call(kv4_copy_pages, static_cast<const int64_t*>(words)); }
 extern "C" int kv4_attention_block(const void* words) { return call(kv4_attention, static_cast<const int64_t*>(words)); }
 extern "C" int qk_norm_rope_block(const void* words) { return call(qk_norm_rope, static_cast<const int64_t*>(words)); }
+extern "C" int kv4_rope_append_block(const void* words) { return call(kv4_rope_append, static_cast<const int64_t*>(words)); }

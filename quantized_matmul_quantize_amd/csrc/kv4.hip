@@ -5,34 +5,14 @@
 
 #include <algorithm>
 
-#include "kv4_device.h"
+#include "kv4_quantize.h"
 
 namespace qmm {
 namespace {
 
-constexpr float kScaleMax16 = 65504.0f;      // largest finite binary16
 // Tokens of a call: four a wavefront at the least, and a launch holds 2^24
 // blocks of 256 threads.
 constexpr int64_t kMostTokens = int64_t{1} << 25;
-
-// Minimum / maximum over the L consecutive lanes of a group (4, 8 or 16 lanes
-// of one DPP row).
-template <int L>
-__device__ __forceinline__ float lanes_min(float v) {
-  v = fminf(v, dpp_f<kDppXor1>(v));
-  v = fminf(v, dpp_f<kDppXor2>(v));
-  if constexpr (L >= 8) v = fminf(v, dpp_f<kDppHalfMirror>(v));
-  if constexpr (L >= 16) v = fminf(v, dpp_f<kDppMirror>(v));
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-  v = fmaxf(v, dpp_f<kDppXor1>(v));
-  v = fmaxf(v, dpp_f<kDppXor2>(v));
-  if constexpr (L >= 8) v = fmaxf(v, dpp_f<kDppHalfMirror>(v));
-  if constexpr (L >= 16) v = fmaxf(v, dpp_f<kDppMirror>(v));
-  return v;
-}
 
 // How a call's words are dealt: a wavefront takes one head's words of 512 / D
 // tokens at a time, NQ times; the wavefronts of a block take heads, where there
@@ -62,29 +42,16 @@ __device__ __forceinline__ Place place_of(Words words) {
   return p;
 }
 
-// Byte offset of a slot's record for head 0; false for a slot outside the cache.
-__device__ __forceinline__ bool record_of(int64_t slot, const Kv4Shape& sh, uint64_t* at) {
-  const int64_t id = slot >> sh.shift;
-  *at = static_cast<uint64_t>(static_cast<uint32_t>(id)) *
-        static_cast<uint32_t>(sh.heads * static_cast<int>(sh.record_bytes()));
-  return slot >= 0 && id < sh.pages;
-}
-
-// A thread quantizes eight channels (one code word); the group's range comes
-// from its GROUP / 8 lanes.  The codes are those of exact division, through a
-// correctly rounded reciprocal and one correction (q0 = x y, q = q0 + (x - q0 s) y
-// is the correctly rounded quotient while nothing over- or underflows: s is
-// 2^-24 .. 65504, and x is first held to 32 s either way, where its code is 0
-// or 15 all the same).  Rounding to an integer is the addition of 1.5 2^23.
-// Memory is 2 bytes read and 0.5 + 4 / GROUP written per channel; the ~150
-// vector instructions a word take as long.  8191 tokens of 8 heads of 128 in
-// groups of 64: 15.1 us, 2.9 TB/s (a large copy reaches 5.1).
+// A thread quantizes eight channels (one code word: kv4_quantize.h).  Memory is
+// 2 bytes read and 0.5 + 4 / GROUP written per channel; the ~150 vector
+// instructions a word take as long.  8191 tokens of 8 heads of 128 in groups of
+// 64: 15.1 us, 2.9 TB/s (a large copy reaches 5.1).
 template <int DT, int D, int GROUP, int NQ>
 __global__ __launch_bounds__(256) void kv4_append_kernel(const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs,
                                                          const uint16_t* __restrict__ v, int64_t v_ts, int64_t v_hs,
                                                          int64_t T, const int64_t* __restrict__ slots,
                                                          uint8_t* __restrict__ cache, Kv4Shape sh, Words words) {
-  constexpr int kLanes = GROUP / 8, kTokens = kWave / (D / 8);
+  constexpr int kTokens = kWave / (D / 8);
   const Place p = place_of<D, NQ>(words);
   if (p.h >= sh.heads || p.t0 >= T) return;                    // the whole wavefront
   const uint16_t* in = p.values ? v + p.t0 * v_ts + p.h * v_hs : k + p.t0 * k_ts + p.h * k_hs;
@@ -103,47 +70,9 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(const uint16_t* __restr
       Vec8<DT>::load(in + t * ts + 8 * p.w, x[n]);
     }
   }
-  constexpr float kRound = 12582912.0f;                        // 1.5 2^23: the sum's low bits are the nearest integer
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, x[n][i]);
-      hi = fmaxf(hi, x[n][i]);
-    }
-    lo = lanes_min<kLanes>(lo);
-    hi = lanes_max<kLanes>(hi);
-    // (hi - lo) / 15, correctly rounded; beyond 2e6 the scale saturates anyway
-    const float d = fminf(hi - lo, 2.0e6f);
-    const float d0 = d * (1.0f / 15.0f);
-    float s = fmaf(fmaf(-d0, 15.0f, d), 1.0f / 15.0f, d0);
-    s = static_cast<float>(static_cast<_Float16>(fminf(s, kScaleMax16)));   // round to nearest even
-    if (s == 0.0f) s = 1.0f;
-    const float y = 1.0f / s, far = 32.0f * s;
-    auto rounded = [&](float a) {
-      a = __builtin_amdgcn_fmed3f(a, -far, far);
-      const float q0 = a * y;
-      return static_cast<int>(__float_as_uint(fmaf(fmaf(-q0, s, a), y, q0) + kRound));
-    };
-    const int bits = static_cast<int>(__builtin_bit_cast(uint32_t, kRound));
-    const int z = min(max(rounded(-lo) - bits, 0), 15);
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      word |= static_cast<uint32_t>(min(max(rounded(x[n][i]) + (z - bits), 0), 15)) << (4 * code_nibble(i));
-    uint64_t at;
-    if (record_of(slot[n], sh, &at)) {
-      const int t = static_cast<int>(slot[n]) & (sh.page - 1);
-      uint8_t* record = head + at;
-      *reinterpret_cast<uint32_t*>(record + (p.values ? kv4_v_word(t, p.w, D, sh.page) : kv4_k_word(t, p.w, D))) = word;
-      if (p.w % kLanes == 0) {
-        const uint32_t param = f32_to_f16_bits(s) | (static_cast<uint32_t>(z) << 16);
-        const int g = p.w / kLanes;
-        reinterpret_cast<uint32_t*>(record + (p.values ? sh.v_params() : sh.k_params()))[g * sh.page + t] = param;
-      }
-    }
-  }
+  for (int n = 0; n < NQ; ++n)
+    store_word<D, GROUP>(quantize_word<GROUP>(x[n]), slot[n], p.w, p.values, sh, head);
 }
 
 template <int DT>
