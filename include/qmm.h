@@ -644,6 +644,63 @@ int kv4_rope_append(const void* q, int64_t q_token_stride, int64_t q_head_stride
                     int w_dtype, float eps, const int64_t* slots, uint8_t* cache, int64_t pages, int64_t kv_heads,
                     int64_t head_dim, int64_t page, int group, void* q_out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * beam_select -- which beams go on with which tokens.  Of each sequence's
+ * beams b and tokens v the candidates
+ *   c[b, v] = scores[b] + x[b, v] - log sum_w exp(x[b, w])
+ * (x the logits of beam b); the k largest, in falling order, equal ones by the
+ * lowest b * vocabulary + v.  A finished beam has one candidate, `pad`, with
+ * its score as it is.  A logit of -inf (a banned token) or NaN is no candidate
+ * and adds nothing to the sum; nor has a beam candidates whose score is not
+ * finite, or whose logits are -inf all or hold a +inf.  Where there are fewer
+ * than k candidates the rest of out_scores is -inf, with token -1 and parent
+ * i % beams.
+ * With k = 2 beams the ones that end can be set aside with as many left; with
+ * beams = 1 this is the k most likely tokens of each row.
+ * logits  : [seqs * beams, vocabulary] of dtype (QMM_F32, QMM_BF16, QMM_F16),
+ *           rows row_stride elements apart, aligned to an element.
+ * scores  : float32 [seqs, beams]; finished: bytes [seqs, beams], not 0 where
+ *           finished, or NULL; pad in [0, vocabulary).
+ * out_scores float32, out_tokens and out_parents (a beam of the sequence)
+ *           int64, [seqs, k].
+ * workspace : beam_select_workspace_bytes bytes, 16-byte aligned, no clearing
+ *           needed.
+ * beams and k up to 64 (QMM_EUNSUPPORTED); beams * vocabulary below 2^31,
+ * seqs * beams below 2^24, and so many times the blocks of 8192 tokens
+ * (QMM_ERANGE).
+ * Arithmetic: candidates are compared in fp64; a row's sum takes each block's
+ * k largest logits (and what ties the search lets through) in fp64, the others
+ * in fp32 (each to 2^-22 or so, and 2^-24 of a distance to the maximum): beams
+ * whose candidates are nearer than that share of the rest of the row may
+ * change places.  Results do not depend on timing.
+ * ------------------------------------------------------------------------- */
+size_t beam_select_workspace_bytes(int64_t seqs, int64_t beams, int64_t vocabulary, int64_t k);
+int beam_select(const void* logits, int dtype, int64_t row_stride, int64_t seqs, int64_t beams, int64_t vocabulary,
+                const float* scores, const uint8_t* finished, int64_t pad, int64_t k, float* out_scores,
+                int64_t* out_tokens, int64_t* out_parents, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kv4_beam_reorder -- every beam goes on with the tokens of its parent.  Slot r
+ * = s * beams + b of a batch of seqs * beams goes on from slot p = s * beams +
+ * parents[s, b] (itself where that is no beam): row r of table_out is row p of
+ * page_table, context_out[r] = context[p].  Full pages are shared, but the one
+ * that is still being filled is each slot's own: where p is not r and
+ * context[p] is no multiple of `page`, the filled part of p's last page (fours
+ * of tokens, every layer and head) is copied to the spare one of slot r's two
+ * tail pages, tails[r], which takes its place in table_out.  The spare one is
+ * that which is not the page of row r at context[r] / page.
+ * cache [layers, pages, kv_heads, page, D + 8 D/g]; page_table, table_out int32
+ * [seqs * beams, table_width]; context, context_out int32 [seqs * beams]; tails
+ * int32 [seqs * beams, 2]; parents int64 [seqs, beams].  Tail pages are in no
+ * other slot's row or tails.  The outputs are other memory than the inputs (so
+ * a captured step has two tables, for every second turn).  A page outside
+ * [0, pages) is not copied.
+ * ------------------------------------------------------------------------- */
+int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_heads, int64_t head_dim, int64_t page,
+                     int group, const int32_t* page_table, int64_t table_width, const int32_t* context,
+                     const int32_t* tails, const int64_t* parents, int64_t seqs, int64_t beams, int32_t* table_out,
+                     int32_t* context_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

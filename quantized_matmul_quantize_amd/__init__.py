@@ -33,7 +33,7 @@ __all__ = [
     "llm_int8_outliers", "llm_int8_workspace_bytes", "llm_int8_gemm", "awq_workspace_bytes", "awq_search", "stream_read",
     "kv4_cache", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention_workspace_bytes",
     "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope", "KvPages",
-    "kv4_rope_append",
+    "kv4_rope_append", "beam_select_workspace_bytes", "beam_select", "kv4_beam_reorder",
 ]
 
 F32, F16, BF16, I32 = 0, 1, 2, 3
@@ -106,12 +106,15 @@ _SIGS = {
     "rope_table": ([_P, _I64, _I64, ctypes.c_double, _P, _P], _I),
     "kv4_rope_append": ([_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _I, _P, _P,
                          _I, _F, _P, _P, _I64, _I64, _I64, _I64, _I, _P, _P], _I),
+    "beam_select_workspace_bytes": ([_I64] * 4, _SZ),
+    "beam_select": ([_P, _I, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P], _I),
+    "kv4_beam_reorder": ([_P, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P], _I),
 }
 # The calls of a decode step with their arguments as one block of 8-byte words (include/qmm_blocks.h): ctypes converts
 # one argument and not up to 27 (kv4_attention: 3.8 us a call by arguments, 0.7 by a block).
 _BLOCKS = {name: struct.Struct("=" + "".join("d" if t is _F else "q" for t in _SIGS[name][0]))
            for name in ("kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention", "qk_norm_rope",
-                        "kv4_rope_append")}
+                        "kv4_rope_append", "beam_select", "kv4_beam_reorder")}
 _SIGS.update({name + "_block": ([ctypes.c_char_p], _I) for name in _BLOCKS})
 
 
@@ -1101,3 +1104,93 @@ def kv4_rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                 _ptr0(positions), _ptr0(table), rows, rot, interleaved, _ptr0(q_weight), _ptr0(k_weight), _DT[w_dtype],
                 eps, slots.data_ptr(), cache.data_ptr(), pages, heads, D, page, group, _ptr0(q_out), _stream(cache))
     return q_out
+
+
+# ---------------------------------------------------------------------------
+# Beam search over the 4-bit cache.
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=4096)      # of sizes alone
+def beam_select_workspace_bytes(seqs: int, beams: int, vocabulary: int, k: int) -> int:
+    """Bytes that beam_select needs for these sizes."""
+    return int(lib().beam_select_workspace_bytes(seqs, beams, vocabulary, k))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = None,
+                finished: Optional[torch.Tensor] = None, pad: int = 0, workspace: Optional[torch.Tensor] = None):
+    """The k (default: beams) best of scores[s, b] + log_softmax(logits[s * beams + b])[v] of each sequence: logits
+    [seqs * beams, vocabulary] (fp32, bf16 or fp16; rows may be apart), scores float32 [seqs, beams].  Returns (scores
+    float32, tokens int64, parents int64), [seqs, k], in falling order, equal ones by beam and then token.  A beam that is
+    finished (bool [seqs, beams]) goes on with `pad` alone and its score; a logit of -inf or NaN is no candidate; where
+    there are too few, scores are -inf, tokens -1, parents i % beams."""
+    if type(scores) is not torch.Tensor or scores.dtype is not torch.float32 or scores.dim() != 2:
+        _req(scores, "scores", (torch.float32,), ndim=2)
+    seqs, beams = shape = scores.shape
+    if type(logits) is not torch.Tensor or logits.dtype not in _FLOATS or logits.dim() != 2:
+        _req(logits, "logits", _FLOATS, ndim=2)
+    rows, vocabulary = logits.shape
+    if rows != seqs * beams:
+        raise ValueError(f"logits has {rows} rows for {seqs} sequences of {beams} beams")
+    stride, one = logits.stride()
+    if one != 1 and vocabulary > 1:
+        raise ValueError(f"logits must have consecutive rows, has strides {logits.stride()}")
+    if rows < 2:
+        stride = vocabulary
+    k = beams if k is None else int(k)
+    if not (1 <= k <= 64 and 1 <= beams <= 64):
+        raise ValueError(f"takes 1 to 64 beams and candidates, not {beams} and {k}")
+    if finished is not None and (type(finished) is not torch.Tensor or finished.dtype is not torch.bool
+                                 or finished.shape != shape):
+        _req(finished, "finished", (torch.bool,), shape=shape)
+    if not 0 <= pad < vocabulary:
+        raise ValueError(f"pad must be a token of {vocabulary}, not {pad}")
+    _on(logits.get_device(), (logits,), scores=scores, finished=finished, workspace=workspace)
+    need = beam_select_workspace_bytes(seqs, beams, vocabulary, k)
+    if workspace is not None:
+        _req(workspace, "workspace", (torch.uint8,), ndim=1)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes; {need} needed")
+    else:
+        workspace = logits.new_empty(need, dtype=torch.uint8)
+    best = scores.new_empty((seqs, k))
+    tokens = logits.new_empty((seqs, k), dtype=torch.int64)
+    parents = torch.empty_like(tokens)
+    _call_block("beam_select", logits.data_ptr(), _DT[logits.dtype], stride, seqs, beams, vocabulary, scores.data_ptr(),
+                _ptr0(finished), pad, k, best.data_ptr(), tokens.data_ptr(), parents.data_ptr(), workspace.data_ptr(),
+                workspace.numel(), _stream(logits))
+    return best, tokens, parents
+
+
+def kv4_beam_reorder(cache: torch.Tensor, head_dim: int, page_table: torch.Tensor, context: torch.Tensor,
+                     tails: torch.Tensor, parents: torch.Tensor, table_out: Optional[torch.Tensor] = None,
+                     context_out: Optional[torch.Tensor] = None):
+    """Every beam goes on with the tokens of its parent: slot s * beams + b from slot s * beams + parents[s, b] (int64
+    [seqs, beams]; itself where that is no beam).  Returns (page_table int32 [seqs * beams, width], context int32 [seqs *
+    beams]) after that; the part of the parent's last page that is filled is copied, in every layer of cache ([layers,]
+    pages, kv_heads, page, token), to the spare one of the slot's own two pages tails (int32 [seqs * beams, 2])."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() not in (4, 5):
+        raise ValueError("cache must be a torch.Tensor of 4 dimensions, or 5 with layers")
+    if cache.dim() == 5 and not cache.shape[0]:
+        raise ValueError("cache has no layers")
+    pages, heads, page, group = _cache_shape(cache if cache.dim() == 4 else cache[0], head_dim)
+    if type(parents) is not torch.Tensor or parents.dtype is not torch.int64 or parents.dim() != 2:
+        _req(parents, "parents", (torch.int64,), ndim=2)
+    seqs, beams = parents.shape
+    slots = seqs * beams
+    if type(page_table) is not torch.Tensor or page_table.dtype is not torch.int32 or page_table.dim() != 2 \
+            or page_table.shape[0] != slots:
+        _req(page_table, "page_table", (torch.int32,), shape=(slots, None))
+    _vector(context, "context", torch.int32, slots)
+    _req(tails, "tails", (torch.int32,), shape=(slots, 2))
+    for name, t, like in (("table_out", table_out, page_table), ("context_out", context_out, context)):
+        if t is not None:
+            _out(t, like.shape, torch.int32, name)
+            if t.numel() and t.data_ptr() == like.data_ptr():
+                raise ValueError(f"{name} must be other memory than its input")
+    _on(cache.get_device(), (), cache=cache, page_table=page_table, context=context, tails=tails, parents=parents,
+        table_out=table_out, context_out=context_out)
+    table_out = torch.empty_like(page_table) if table_out is None else table_out
+    context_out = torch.empty_like(context) if context_out is None else context_out
+    _call_block("kv4_beam_reorder", cache.data_ptr(), cache.shape[0] if cache.dim() == 5 else 1, pages, heads, head_dim,
+                page, group, page_table.data_ptr(), page_table.shape[1], context.data_ptr(), tails.data_ptr(),
+                parents.data_ptr(), seqs, beams, table_out.data_ptr(), context_out.data_ptr(), _stream(cache))
+    return table_out, context_out

@@ -1,0 +1,590 @@
+// beams.hip -- beam search over the 4-bit cache: which beams go on with which
+// tokens, and the reordering of their pages (definitions: include/qmm.h).
+
+#include <algorithm>
+
+#include "kv4_device.h"
+
+namespace qmm {
+namespace {
+
+typedef u32x4 u32x4_anywhere __attribute__((aligned(2)));
+
+constexpr int kMostBeams = 64, kMostK = 64;
+constexpr int kPerThread = 32;                     // logits of a thread
+constexpr int kChunk = 256 * kPerThread;           // of a block
+
+// What a block found in its logits of a row: their maximum, the sum of
+// exp(x - maximum), and how many of its k candidates there are.
+struct Partial {
+  float most;
+  int count;
+  double sum;
+};
+struct Candidate {
+  float x;
+  uint32_t token;
+};
+
+// Numbers in their order as unsigned ones (-0 first made 0).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint64_t ordered(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
+  return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double unordered(uint64_t k) {
+  return __builtin_bit_cast(double, k >> 63 ? k ^ 0x8000000000000000ull : ~k);
+}
+
+// The k-th largest key of the wavefront's lanes (0: fewer than k are not 0).
+template <typename K>
+__device__ __forceinline__ K kth_largest(K key, int k) {
+  K at = 0;
+  for (int bit = static_cast<int>(sizeof(K)) * 8 - 1; bit >= 0; --bit) {
+    const K next = at | K{1} << bit;
+    if (__popcll(__ballot(key >= next)) >= k) at = next;
+  }
+  return at;
+}
+
+// A bound below which no value is among the k best: the k-th best of the lanes'
+// best values, of equal ones those with the lowest indexes first.  Of a
+// wavefront at most k lanes hold values that it lets through.
+template <typename K>
+struct Bound {
+  K key;             // 0: no bound
+  uint32_t index;    // of values with that key, up to this index
+};
+// `first(key)` gives the lowest index at which the lane holds its best value.
+template <typename K, typename First>
+__device__ __forceinline__ Bound<K> bound_of(K best, int k, First first) {
+  Bound<K> b{kth_largest(best, k), 0xFFFFFFFFu};
+  if (b.key == 0) return b;
+  const int more = k - __popcll(__ballot(best > b.key));
+  if (__popcll(__ballot(best == b.key)) > more)
+    b.index = ~kth_largest<uint32_t>(best == b.key ? ~first() : 0u, more);
+  return b;
+}
+// What a block of four wavefronts lets through: the one whose bound is taken has
+// k such lanes, the others, whose own bounds are less tight, at most k - 1.
+__host__ __device__ constexpr int room_of(int k) { return (4 * k - 3) * kPerThread + 7; }
+template <typename K>
+__device__ __forceinline__ bool tighter(const Bound<K>& a, const Bound<K>& b) {
+  return a.key > b.key || (a.key == b.key && a.index < b.index);
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int i = 1; i < kWave; i <<= 1) v += __shfl_xor(v, i, kWave);
+  return v;
+}
+
+struct Select {
+  const void* logits;
+  int64_t row_stride;
+  int64_t rows;
+  int32_t vocabulary, beams, k, chunks;
+  const float* scores;
+  const uint8_t* finished;   // may be null
+  int32_t pad;
+  Partial* partial;          // [rows][chunks]
+  Candidate* list;           // [rows][chunks][k]
+  float* out_scores;
+  int64_t* out_tokens;
+  int64_t* out_parents;
+};
+
+template <int DT>
+struct Logits;               // 16-byte pieces of a row
+template <>
+struct Logits<QMM_F32> {
+  static constexpr int kOf = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;             // -inf
+  static __device__ __forceinline__ float get(u32x4 v, int e) { return __uint_as_float(v[e]); }
+  static __device__ __forceinline__ void set_none(u32x4& v, int e) { v[e] = kNone; }
+};
+template <>
+struct Logits<QMM_BF16> {
+  static constexpr int kOf = 8;
+  static constexpr uint32_t kNone = 0xFF80FF80u;
+  static __device__ __forceinline__ float get(u32x4 v, int e) {
+    return e & 1 ? bf16hi_to_f32(v[e / 2]) : bf16lo_to_f32(v[e / 2]);
+  }
+  static __device__ __forceinline__ void set_none(u32x4& v, int e) {
+    v[e / 2] = e & 1 ? (v[e / 2] & 0xFFFFu) | 0xFF800000u : (v[e / 2] & 0xFFFF0000u) | 0xFF80u;
+  }
+};
+template <>
+struct Logits<QMM_F16> {
+  static constexpr int kOf = 8;
+  static constexpr uint32_t kNone = 0xFC00FC00u;
+  static __device__ __forceinline__ float get(u32x4 v, int e) {
+    return e & 1 ? f16hi_to_f32(v[e / 2]) : f16lo_to_f32(v[e / 2]);
+  }
+  static __device__ __forceinline__ void set_none(u32x4& v, int e) {
+    v[e / 2] = e & 1 ? (v[e / 2] & 0xFFFFu) | 0xFC000000u : (v[e / 2] & 0xFFFF0000u) | 0xFC00u;
+  }
+};
+
+// A block takes 8192 logits of a row, 32 a thread in registers, reads them once
+// and finds their maximum, the sum of exponentials and the k largest.  The
+// largest: no logit below the k-th best of a wavefront's 64 lane maxima can be
+// among them (a search over the bits of a key, one comparison and a count of
+// lanes each), so a few more than k reach LDS, where each counts those before
+// it.  These, which are most of a peaked row's sum, add to it in fp64, the
+// others in fp32 by the hardware's exponential: two beams' candidates that are
+// nearly as good are told apart by their rows' sums.
+template <int DT>
+__global__ __launch_bounds__(256) void beam_rows_kernel(Select a) {
+  using L = Logits<DT>;
+  constexpr int kOf = L::kOf, kPieces = kPerThread / kOf;
+  constexpr float kLog2e = 1.44269504088896341f;
+  extern __shared__ __attribute__((aligned(16))) Candidate pool[];     // room_of(k)
+  __shared__ float s_most[4];
+  __shared__ double s_sum[4];
+  __shared__ Bound<uint32_t> s_bound[4];
+  __shared__ int s_count, s_nan[4];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int chunk = blockIdx.x;
+  const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
+  if (row >= a.rows || (a.finished && a.finished[row])) return;
+  const int room = room_of(a.k);
+
+  // Whole pieces from the row's start on, wherever that lies (the hardware takes
+  // 16 bytes from any address, and rows of the same logits have the same sums to
+  // the last bit), and what is left behind them for the first threads.
+  constexpr int kSize = 16 / kOf;
+  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + row * a.row_stride * kSize;
+  const int pieces = a.vocabulary / kOf, behind = a.vocabulary % kOf;
+  u32x4 raw[kPieces];
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    const int p = (chunk * kPieces + j) * 256 + tid;
+    raw[j] = u32x4{L::kNone, L::kNone, L::kNone, L::kNone};
+    if (p < pieces) raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_anywhere*>(base + static_cast<int64_t>(p) * 16));
+  }
+  auto index_of = [&](int j, int e) {
+    return static_cast<uint32_t>(((chunk * kPieces + j) * 256 + tid) * kOf + e);
+  };
+  float odd = -INFINITY;
+  uint32_t odd_index = 0;
+  if (chunk == 0 && tid < behind) {
+    odd_index = a.vocabulary - behind + tid;
+    if constexpr (DT == QMM_F32) odd = reinterpret_cast<const float*>(base)[odd_index];
+    else if constexpr (DT == QMM_BF16) odd = bf16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[odd_index]);
+    else odd = f16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[odd_index]);
+  }
+
+  float most, sum;
+  double large = 0.0;                 // the sum of those that reach LDS
+  for (int turn = 0;; ++turn) {
+    // ---- the lane's best, the block's maximum, the bound
+    float best = odd;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+      for (int e = 0; e < kOf; ++e) best = fmaxf(best, L::get(raw[j], e));
+    const uint32_t key = best > -INFINITY ? ordered(best) : 0u;
+    const Bound<uint32_t> mine = bound_of(key, a.k, [&] {
+      uint32_t at = odd == best ? odd_index : 0xFFFFFFFFu;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+        for (int e = 0; e < kOf; ++e) at = L::get(raw[j], e) == best ? min(at, index_of(j, e)) : at;
+      return at;
+    });
+    const float wave_most = wave_max(best);
+    if (lane == 0) {
+      s_most[wave] = wave_most;
+      s_bound[wave] = mine;
+    }
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+    Bound<uint32_t> bound = s_bound[0];
+    most = s_most[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      if (tighter(s_bound[w], bound)) bound = s_bound[w];
+      most = fmaxf(most, s_most[w]);
+    }
+    // ---- sums below the bound; what passes it goes to LDS
+    const float least = bound.key ? unordered(bound.key) : -INFINITY;
+    const float from = most == -INFINITY ? 0.0f : most;
+    sum = 0.0f;
+    auto term = [&](float x) { return __builtin_amdgcn_exp2f((x - from) * kLog2e); };
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+      for (int e = 0; e < kOf; ++e) {
+        const float x = L::get(raw[j], e);
+        sum += x >= least ? 0.0f : term(x);
+      }
+    sum += odd >= least ? 0.0f : term(odd);
+    auto take = [&](float x, uint32_t at) {
+      if (!(x >= least) || x == -INFINITY) return;
+      if (x > least || at <= bound.index) {
+        const int n = atomicAdd(&s_count, 1);
+        if (n < room) pool[n] = {x, at};
+      } else {
+        sum += term(x);
+      }
+    };
+    if (best >= least) {
+      take(odd, odd_index);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+        for (int e = 0; e < kOf; ++e) take(L::get(raw[j], e), index_of(j, e));
+    }
+    if (turn == 1) {
+      __syncthreads();
+      break;
+    }
+    // a NaN (which the sum has taken) counts as -inf: once more without them
+    const bool nan = __any(sum != sum);
+    if (lane == 0) s_nan[wave] = nan;
+    __syncthreads();
+    if (!(s_nan[0] | s_nan[1] | s_nan[2] | s_nan[3])) break;
+    if (odd != odd) odd = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+#pragma unroll
+      for (int e = 0; e < kOf; ++e) {
+        const float x = L::get(raw[j], e);
+        if (x != x) L::set_none(raw[j], e);
+      }
+    __syncthreads();                  // the count and the flags may be written again
+  }
+
+  const int n = min(s_count, room);
+  const int64_t at = row * a.chunks + chunk;
+  for (int i = tid; i < n; i += 256) {
+    const Candidate c = pool[i];
+    const uint32_t key = ordered(c.x);
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const Candidate o = pool[j];
+      const uint32_t ko = ordered(o.x);
+      rank += ko > key || (ko == key && o.token < c.token);
+    }
+    if (rank < a.k) a.list[at * a.k + rank] = c;
+    large += exp(static_cast<double>(c.x) - static_cast<double>(most));
+  }
+  large += static_cast<double>(wave_sum(sum)) * (lane == 0);
+  large = wave_sum(large);
+  if (lane == 0) s_sum[wave] = large;
+  __syncthreads();
+  if (tid == 0) a.partial[at] = {most, min(n, a.k), s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]};
+}
+
+// A block joins the rows of a sequence: each beam's log sum, then the k best of
+// the blocks' candidates, 2048 at a time, by the same bound.  Values are fp64.
+constexpr int kJoinPer = 8, kJoinRoom = 4 * kMostK * kJoinPer + kMostK;     // (as room_of, and the ones kept)
+
+__global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
+  __shared__ double s_offset[kMostBeams];
+  __shared__ int s_alive[kMostBeams];
+  __shared__ Bound<uint64_t> s_bound[4];
+  __shared__ int s_count;
+  __shared__ double value[kJoinRoom], kept_value[kMostK];
+  __shared__ uint32_t place[kJoinRoom], kept_place[kMostK];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.beams;
+  for (int b = wave; b < a.beams; b += 4) {
+    const float score = a.scores[row0 + b];
+    const bool ends = a.finished && a.finished[row0 + b];
+    double offset = 0.0;
+    bool alive = fabsf(score) < INFINITY;
+    if (!ends) {
+      const Partial* p = a.partial + (row0 + b) * a.chunks;
+      float most = -INFINITY;
+      for (int c = lane; c < a.chunks; c += kWave) most = fmaxf(most, p[c].most);
+      most = wave_max(most);
+      double sum = 0.0;
+      for (int c = lane; c < a.chunks; c += kWave)
+        if (p[c].most > -INFINITY) sum += p[c].sum * exp(static_cast<double>(p[c].most) - static_cast<double>(most));
+      sum = wave_sum(sum);
+      offset = static_cast<double>(score) - (static_cast<double>(most) + log(sum));
+      alive = alive && fabsf(most) < INFINITY;
+    }
+    if (lane == 0) {
+      s_offset[b] = offset;
+      s_alive[b] = alive ? (ends ? 2 : 1) : 0;
+    }
+  }
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+
+  const int total = a.beams * a.chunks * a.k;
+  int kept = 0;
+  for (int first = 0; first < total; first += 256 * kJoinPer) {
+    double v[kJoinPer];
+    uint32_t at[kJoinPer];
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinPer; ++i) {
+      const int e = first + i * 256 + tid;
+      v[i] = -__builtin_inf();
+      at[i] = 0;
+      if (e < total) {
+        const int list = e / a.k, r = e - list * a.k, b = list / a.chunks;
+        if (s_alive[b] == 2) {
+          if (e == b * a.chunks * a.k) {
+            v[i] = a.scores[row0 + b];
+            at[i] = static_cast<uint32_t>(b) * a.vocabulary + a.pad;
+          }
+        } else if (s_alive[b] == 1 && r < a.partial[row0 * a.chunks + list].count) {
+          const Candidate c = a.list[(row0 * a.chunks + list) * a.k + r];
+          v[i] = s_offset[b] + static_cast<double>(c.x);
+          at[i] = static_cast<uint32_t>(b) * a.vocabulary + c.token;
+        }
+      }
+      if (v[i] > -__builtin_inf()) best = max(best, ordered(v[i]));
+    }
+    const Bound<uint64_t> mine = bound_of(best, a.k, [&] {
+      uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < kJoinPer; ++i)
+        if (v[i] > -__builtin_inf() && ordered(v[i]) == best) low = min(low, at[i]);
+      return low;
+    });
+    if (lane == 0) s_bound[wave] = mine;
+    for (int i = tid; i < kept; i += 256) {                  // the best of those before
+      const int n = atomicAdd(&s_count, 1);
+      value[n] = kept_value[i];
+      place[n] = kept_place[i];
+    }
+    __syncthreads();
+    Bound<uint64_t> bound = s_bound[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+      if (tighter(s_bound[w], bound)) bound = s_bound[w];
+#pragma unroll
+    for (int i = 0; i < kJoinPer; ++i) {
+      if (!(v[i] > -__builtin_inf())) continue;
+      const uint64_t key = ordered(v[i]);
+      if (key > bound.key || (key == bound.key && at[i] <= bound.index)) {
+        const int n = atomicAdd(&s_count, 1);
+        if (n < kJoinRoom) {
+          value[n] = v[i];
+          place[n] = at[i];
+        }
+      }
+    }
+    __syncthreads();
+    const int n = min(s_count, kJoinRoom);
+    kept = min(n, a.k);
+    for (int i = tid; i < n; i += 256) {
+      const double mine_v = value[i];
+      const uint32_t mine_at = place[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) rank += value[j] > mine_v || (value[j] == mine_v && place[j] < mine_at);
+      if (rank < a.k) {
+        kept_value[rank] = mine_v;
+        kept_place[rank] = mine_at;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) s_count = 0;
+    __syncthreads();
+  }
+  for (int i = tid; i < a.k; i += 256) {
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * a.k + i;
+    const bool some = i < kept;
+    const uint32_t at = some ? kept_place[i] : 0u, b = at / a.vocabulary;
+    a.out_scores[o] = some ? static_cast<float>(kept_value[i]) : -INFINITY;
+    a.out_tokens[o] = some ? static_cast<int64_t>(at - b * a.vocabulary) : -1;
+    a.out_parents[o] = some ? b : i % a.beams;
+  }
+}
+
+int64_t chunks_of(int64_t vocabulary) { return ceil_div(vocabulary, kChunk); }
+
+size_t select_bytes(int64_t rows, int64_t vocabulary, int64_t k) {
+  return static_cast<size_t>(rows) * chunks_of(vocabulary) * (sizeof(Partial) + k * sizeof(Candidate));
+}
+
+// ---------------------------------------------------------------------------
+// Reordering of the beams' pages.
+// ---------------------------------------------------------------------------
+struct Reorder {
+  uint8_t* cache;
+  Kv4Shape sh;
+  const int32_t* table;
+  int32_t width;
+  const int32_t* context;
+  const int32_t* tails;      // [slots][2]
+  const int64_t* parents;    // [slots], a beam of the slot's sequence
+  int32_t beams;
+  int32_t* table_out;
+  int32_t* context_out;
+  int32_t heads_per;         // heads of a block
+};
+
+// blockIdx.x a slot, .y a layer, .z some of its heads: the filled part of the
+// parent's last page, four 16-byte pieces a thread in flight.  The first block
+// of a slot writes its row of the table.
+constexpr int kReorderPieces = 4;
+
+__global__ __launch_bounds__(256) void kv4_beam_reorder_kernel(Reorder a) {
+  const int slot = blockIdx.x, seq = slot / a.beams;
+  const int64_t beam = a.parents[slot];
+  const int parent = beam >= 0 && beam < a.beams ? seq * a.beams + static_cast<int>(beam) : slot;
+  const int64_t most = static_cast<int64_t>(a.width) << a.sh.shift;
+  const int n = static_cast<int>(min(max<int64_t>(a.context[parent], 0), most));
+  const int own = static_cast<int>(min(max<int64_t>(a.context[slot], 0), most));
+  const int32_t* theirs = a.table + static_cast<int64_t>(parent) * a.width;
+  const int column = n >> a.sh.shift, filled = n & (a.sh.page - 1);
+  const bool moved = parent != slot && filled != 0;
+  int from = -1, to = -1;
+  if (moved) {
+    from = theirs[column];
+    const int at = own >> a.sh.shift;
+    const int mine = at < a.width ? a.table[static_cast<int64_t>(slot) * a.width + at] : -1;
+    const int32_t t0 = a.tails[2 * slot], t1 = a.tails[2 * slot + 1];
+    to = mine == t0 ? t1 : t0;
+  }
+  if (blockIdx.y == 0 && blockIdx.z == 0) {
+    int32_t* out = a.table_out + static_cast<int64_t>(slot) * a.width;
+    for (int j = threadIdx.x; j < a.width; j += 256) out[j] = moved && j == column ? to : theirs[j];
+    if (threadIdx.x == 0) a.context_out[slot] = n;
+  }
+  const uint32_t pages = static_cast<uint32_t>(a.sh.pages);
+  if (!moved || static_cast<uint32_t>(from) >= pages || static_cast<uint32_t>(to) >= pages || from == to) return;
+
+  // fours of tokens: pieces of K codes, of V codes, then of each row of params
+  const int fours = (filled + 3) >> 2, D = a.sh.D;
+  const int codes = fours * (D / 8), record = 2 * codes + 2 * a.sh.groups() * fours;
+  const int h0 = static_cast<int>(blockIdx.z) * a.heads_per, h1 = min(h0 + a.heads_per, a.sh.heads);
+  const int64_t bytes = a.sh.record_bytes();
+  uint8_t* layer = a.cache + static_cast<int64_t>(blockIdx.y) * a.sh.pages * a.sh.heads * bytes;
+  const uint8_t* src = layer + static_cast<int64_t>(from) * a.sh.heads * bytes;
+  uint8_t* dst = layer + static_cast<int64_t>(to) * a.sh.heads * bytes;
+  const int total = (h1 - h0) * record;
+  for (int p0 = threadIdx.x; p0 < total; p0 += kReorderPieces * 256) {
+    u32x4 x[kReorderPieces];
+    int64_t at[kReorderPieces];
+#pragma unroll
+    for (int i = 0; i < kReorderPieces; ++i) {
+      const int p = p0 + i * 256;
+      if (p < total) {
+        const int h = p / record, q = p - h * record;
+        int offset = 16 * q;
+        if (q >= 2 * codes) {
+          const int r = (q - 2 * codes) / fours;
+          offset = a.sh.page * (D + 4 * r) + 16 * (q - 2 * codes - r * fours);
+        } else if (q >= codes) {
+          offset = a.sh.page * (D / 2) + 16 * (q - codes);
+        }
+        at[i] = (h0 + h) * bytes + offset;
+        x[i] = ld16_nt(src + at[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kReorderPieces; ++i)
+      if (p0 + i * 256 < total) st16_nt(dst + at[i], x[i]);
+  }
+}
+
+}  // namespace
+}  // namespace qmm
+
+extern "C" size_t beam_select_workspace_bytes(int64_t seqs, int64_t beams, int64_t vocabulary, int64_t k) {
+  using namespace qmm;
+  if (seqs <= 0 || beams <= 0 || vocabulary <= 0 || k <= 0 || beams > kMostBeams || k > kMostK ||
+      vocabulary >= (int64_t{1} << 31) / beams || seqs >= (int64_t{1} << 24) / beams)
+    return 0;
+  return select_bytes(seqs * beams, vocabulary, k);
+}
+
+extern "C" int beam_select(const void* logits, int dtype, int64_t row_stride, int64_t seqs, int64_t beams,
+                           int64_t vocabulary, const float* scores, const uint8_t* finished, int64_t pad, int64_t k,
+                           float* out_scores, int64_t* out_tokens, int64_t* out_parents, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  using namespace qmm;
+  if (seqs == 0) return QMM_OK;
+  if (!logits || !scores || !out_scores || !out_tokens || !out_parents || seqs < 0 || beams <= 0 || vocabulary <= 0 ||
+      k <= 0 || row_stride < vocabulary || pad < 0 || pad >= vocabulary || dtype < QMM_F32 || dtype > QMM_I32)
+    return QMM_EINVAL;
+  if (dtype == QMM_I32 || beams > kMostBeams || k > kMostK) return QMM_EUNSUPPORTED;
+  if (vocabulary >= (int64_t{1} << 31) / beams || seqs >= (int64_t{1} << 24) / beams) return QMM_ERANGE;
+  const int64_t rows = seqs * beams, chunks = chunks_of(vocabulary);
+  if (rows * chunks >= (int64_t{1} << 24)) return QMM_ERANGE;            // blocks of 256 threads a launch holds
+  if (!aligned(logits, dtype == QMM_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
+      !aligned(out_tokens, 8) || !aligned(out_parents, 8))
+    return QMM_EALIGN;
+  if (!workspace || workspace_bytes < select_bytes(rows, vocabulary, k)) return QMM_EWORKSPACE;
+  if (!aligned(workspace, 16)) return QMM_EALIGN;
+  Select a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.rows = rows;
+  a.vocabulary = static_cast<int32_t>(vocabulary);
+  a.beams = static_cast<int32_t>(beams);
+  a.k = static_cast<int32_t>(k);
+  a.chunks = static_cast<int32_t>(chunks);
+  a.scores = scores;
+  a.finished = finished;
+  a.pad = static_cast<int32_t>(pad);
+  a.partial = static_cast<Partial*>(workspace);
+  a.list = reinterpret_cast<Candidate*>(a.partial + rows * chunks);
+  a.out_scores = out_scores;
+  a.out_tokens = out_tokens;
+  a.out_parents = out_parents;
+  hipStream_t s = as_stream(stream);
+  const size_t lds = room_of(static_cast<int>(k)) * sizeof(Candidate);
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(rows, 65535)),
+                  static_cast<unsigned>(ceil_div(rows, 65535)));
+  if (dtype == QMM_BF16) beam_rows_kernel<QMM_BF16><<<grid, 256, lds, s>>>(a);
+  else if (dtype == QMM_F16) beam_rows_kernel<QMM_F16><<<grid, 256, lds, s>>>(a);
+  else beam_rows_kernel<QMM_F32><<<grid, 256, lds, s>>>(a);
+  beam_join_kernel<<<static_cast<unsigned>(seqs), 256, 0, s>>>(a);
+  return launch_status();
+}
+
+extern "C" int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_heads, int64_t head_dim,
+                                int64_t page, int group, const int32_t* page_table, int64_t table_width,
+                                const int32_t* context, const int32_t* tails, const int64_t* parents, int64_t seqs,
+                                int64_t beams, int32_t* table_out, int32_t* context_out, void* stream) {
+  using namespace qmm;
+  if (seqs == 0) return QMM_OK;
+  if (!cache || !page_table || !context || !tails || !parents || !table_out || !context_out || layers <= 0 ||
+      table_width <= 0 || seqs < 0 || beams <= 0)
+    return QMM_EINVAL;
+  if (page_table == table_out || context == context_out) return QMM_EINVAL;
+  Kv4Shape sh;
+  if (const int st = kv4_shape(pages, kv_heads, head_dim, page, group, &sh)) return st;
+  if (layers > 65535 || table_width >= (int64_t{1} << 31) || table_width * page > (int64_t{1} << 30) ||
+      seqs >= (int64_t{1} << 24) / beams)
+    return QMM_ERANGE;
+  if (!aligned(cache, 16) || !aligned(page_table, 4) || !aligned(context, 4) || !aligned(tails, 4) ||
+      !aligned(parents, 8) || !aligned(table_out, 4) || !aligned(context_out, 4))
+    return QMM_EALIGN;
+  Reorder a{};
+  a.cache = cache;
+  a.sh = sh;
+  a.table = page_table;
+  a.width = static_cast<int32_t>(table_width);
+  a.context = context;
+  a.tails = tails;
+  a.parents = parents;
+  a.beams = static_cast<int32_t>(beams);
+  a.table_out = table_out;
+  a.context_out = context_out;
+  // heads of a block: all, but where layers and slots are few as many blocks as fill the chip
+  const int64_t slots = seqs * beams, want = ceil_div(8 * device_cus(), slots * layers);
+  a.heads_per = static_cast<int32_t>(ceil_div(kv_heads, std::min<int64_t>(kv_heads, want)));
+  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(layers),
+                  static_cast<unsigned>(ceil_div(kv_heads, a.heads_per)));
+  if (static_cast<int64_t>(grid.x) * grid.y * grid.z >= (int64_t{1} << 24)) return QMM_ERANGE;
+  kv4_beam_reorder_kernel<<<grid, 256, 0, as_stream(stream)>>>(a);
+  return launch_status();
+}

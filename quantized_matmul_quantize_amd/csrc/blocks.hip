@@ -39,3 +39,5 @@ extern "C" int kv4_copy_pages_block(const void* words) { return call(kv4_copy_pa
 extern "C" int kv4_attention_block(const void* words) { return call(kv4_attention, static_cast<const int64_t*>(words)); }
 extern "C" int qk_norm_rope_block(const void* words) { return call(qk_norm_rope, static_cast<const int64_t*>(words)); }
 extern "C" int kv4_rope_append_block(const void* words) { return call(kv4_rope_append, static_cast<const int64_t*>(words)); }
+extern "C" int beam_select_block(const void* words) { return call(beam_select, static_cast<const int64_t*>(words)); }
+extern "C" int kv4_beam_reorder_block(const void* words) { return call(kv4_beam_reorder, static_cast<const int64_t*>(words)); }

@@ -81,3 +81,91 @@ def test_rope_append_checks():
     raises(lambda: f(q, k, v, slots, cache, q_out=t((4, 8, 64), bf16)), "q_out has shape")
     raises(lambda: f(q, k.transpose(1, 2).contiguous().transpose(1, 2), v, slots, cache), "channels consecutive")
     raises(lambda: f(q, k, v, slots, cache), "device tensors")
+
+
+# ---------------------------------------------------------------------------
+# Selection and reordering.
+# ---------------------------------------------------------------------------
+def select_args(**k):
+    g = k.get
+    return [g("x", P), g("dt", BF16), g("stride", 1000), g("seqs", 2), g("beams", 4), g("v", 1000), g("scores", P),
+            g("finished", None), g("pad", 0), g("k", 4), g("o", P), g("tok", P), g("par", P), g("ws", P), g("wsb", 10 ** 9),
+            None]
+
+
+def test_select_errors():
+    f, a = qmm.lib().beam_select, select_args
+    assert f(*a(seqs=0, x=None)) == OK
+    for kw in [dict(x=None), dict(scores=None), dict(o=None), dict(tok=None), dict(par=None), dict(seqs=-1), dict(beams=0),
+               dict(v=0), dict(k=0), dict(k=-3), dict(stride=999), dict(pad=-1), dict(pad=1000), dict(dt=8)]:
+        assert f(*a(**kw)) == EINVAL, kw
+    for kw in [dict(dt=I32), dict(beams=65), dict(k=65)]:
+        assert f(*a(**kw)) == EUNSUP, kw
+    for kw in [dict(v=1 << 30, stride=1 << 30), dict(v=1 << 40, stride=1 << 40), dict(seqs=1 << 22), dict(seqs=1 << 62),
+               dict(seqs=1 << 18, v=1 << 20, stride=1 << 20)]:
+        assert f(*a(**kw)) == ERANGE, kw
+    for kw in [dict(x=P + 1), dict(x=P + 2, dt=F32), dict(scores=P + 2), dict(o=P + 1), dict(tok=P + 4), dict(par=P + 4),
+               dict(ws=P + 8)]:
+        assert f(*a(**kw)) == EALIGN, kw
+    need = qmm.beam_select_workspace_bytes(2, 4, 1000, 4)
+    assert need == 8 * (16 + 4 * 8) and qmm.beam_select_workspace_bytes(2, 4, 8193, 4) == 2 * need
+    assert f(*a(ws=None)) == EWS and f(*a(wsb=need - 1)) == EWS
+    for bad in [(0, 4, 1000, 4), (2, 0, 1000, 4), (2, 65, 1000, 4), (2, 4, 0, 4), (2, 4, 1000, 65), (2, 4, 1 << 30, 4),
+                (1 << 24, 4, 1000, 4)]:
+        assert qmm.beam_select_workspace_bytes(*bad) == 0, bad
+
+
+def test_select_checks():
+    f, x, s = qmm.beam_select, t((8, 100), bf16), t((2, 4), f32)
+    raises(lambda: f(x, s.half()), "scores has dtype")
+    raises(lambda: f(x, s.view(-1)), "scores must have 2")
+    raises(lambda: f(x.int(), s), "logits has dtype")
+    raises(lambda: f(x[:7], s), "7 rows for 2 sequences")
+    raises(lambda: f(x.t().contiguous().t(), s), "consecutive")
+    raises(lambda: f(x, s, 0), "1 to 64")
+    raises(lambda: f(x, s, 65), "1 to 64")
+    raises(lambda: f(t((130, 100), bf16), t((2, 65), f32)), "1 to 64")
+    raises(lambda: f(x, s, 4, t((2, 4), u8)), "finished has dtype")
+    raises(lambda: f(x, s, 4, t((4, 2), torch.bool)), "finished has shape")
+    raises(lambda: f(x, s, 4, pad=100), "pad")
+    raises(lambda: f(x, s, 4), "device tensors")
+
+
+def reorder_args(**k):
+    g = k.get
+    return [g("cache", P), g("layers", 2), g("pages", 100), g("heads", 8), g("D", 128), g("page", 64), g("group", 64),
+            g("table", P), g("width", 20), g("context", P), g("tails", P), g("parents", P), g("seqs", 2), g("beams", 4),
+            g("to", P + 4096), g("co", P + 4096), None]
+
+
+def test_reorder_errors():
+    f, a = qmm.lib().kv4_beam_reorder, reorder_args
+    assert f(*a(seqs=0, cache=None)) == OK
+    for kw in [dict(cache=None), dict(table=None), dict(context=None), dict(tails=None), dict(parents=None), dict(to=None),
+               dict(co=None), dict(layers=0), dict(width=0), dict(seqs=-1), dict(beams=0), dict(to=P), dict(co=P),
+               dict(pages=0), dict(heads=0)]:
+        assert f(*a(**kw)) == EINVAL, kw
+    for kw in [dict(D=96), dict(page=48), dict(group=16)]:
+        assert f(*a(**kw)) == EUNSUP, kw
+    for kw in [dict(layers=70000), dict(width=1 << 31), dict(width=1 << 25), dict(seqs=1 << 22), dict(beams=1 << 40),
+               dict(seqs=1 << 20, layers=32), dict(heads=5000)]:
+        assert f(*a(**kw)) == ERANGE, kw
+    for kw in [dict(cache=P + 8), dict(table=P + 2), dict(context=P + 1), dict(tails=P + 2), dict(parents=P + 4),
+               dict(to=P + 2), dict(co=P + 2)]:
+        assert f(*a(**kw)) == EALIGN, kw
+
+
+def test_reorder_checks():
+    cache, table, ctx = t((3, 9, 2, 64, 144), u8), t((8, 5), i32), t(8, i32)
+    tails, parents, f = t((8, 2), i32), t((2, 4), i64), qmm.kv4_beam_reorder
+    raises(lambda: f(cache[0, 0], 128, table, ctx, tails, parents), "4 dimensions")
+    raises(lambda: f(cache[:0], 128, table, ctx, tails, parents), "no layers")
+    raises(lambda: f(cache, 64, table, ctx, tails, parents), "token of head_dim")
+    raises(lambda: f(cache, 128, table, ctx, tails, parents.int()), "parents has dtype")
+    raises(lambda: f(cache, 128, table[:7], ctx, tails, parents), "page_table has shape")
+    raises(lambda: f(cache, 128, table, ctx[:7], tails, parents), "context has shape")
+    raises(lambda: f(cache, 128, table, ctx, tails.view(-1), parents), "tails has shape")
+    raises(lambda: f(cache, 128, table, ctx, tails, parents, table_out=table), "other memory")
+    raises(lambda: f(cache, 128, table, ctx, tails, parents, context_out=ctx), "other memory")
+    raises(lambda: f(cache, 128, table, ctx, tails, parents, table_out=t((8, 4), i32)), "table_out has shape")
+    raises(lambda: f(cache, 128, table, ctx, tails, parents), "device tensors")
