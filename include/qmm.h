@@ -701,6 +701,39 @@ int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_h
                      const int32_t* tails, const int64_t* parents, int64_t seqs, int64_t beams, int32_t* table_out,
                      int32_t* context_out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * kv4_prefix_attention -- kv4_attention of a batch in groups of sequences whose
+ * first tokens are the same (branches, samples or beams of one prompt, questions
+ * on one document): those are read and attended to once for a group, with the
+ * queries of all of its sequences, and joined with each sequence's own.  The
+ * results are kv4_attention's (window 0) but for roundings.
+ * groups  : int32 [n_groups + 1], device, rising: group g are the sequences
+ *           groups[g] .. groups[g + 1] - 1 (those in none share nothing).
+ * prefix  : int32 [n_groups], device: the first prefix[g] tokens of a group's
+ *           sequences are the same, whether in the same pages or in copies of
+ *           one.  Whole steps of 32 are read once, through the pages of one of
+ *           the sequences that hold them; a sequence that is shorter (an unused
+ *           slot, context 0) is attended to by itself.
+ * max_group, max_prefix, max_tail : the most sequences of a group, tokens of a
+ *           prefix and tokens of a sequence behind it.  Hints (at least 1), like
+ *           max_q: they only shape the launch and the workspace.
+ * workspace : kv4_prefix_attention_workspace_bytes bytes with the same
+ *           arguments (max_context = table_width * page), 16-byte aligned, no
+ *           clearing needed.
+ * The other arguments, limits and the arithmetic are kv4_attention's; up to
+ * 65535 groups, and groups * kv_heads below 2^24.
+ * ------------------------------------------------------------------------- */
+size_t kv4_prefix_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t n_groups,
+                                            int64_t max_group, int64_t max_prefix, int64_t max_tail, int64_t q_heads,
+                                            int64_t kv_heads, int64_t head_dim, int group, int64_t max_context);
+int kv4_prefix_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int dtype, int64_t T,
+                         int64_t q_heads, const int32_t* cu_q, int64_t seqs, int64_t max_q, const int32_t* context,
+                         const int32_t* page_table, int64_t table_width, int64_t table_stride, const int32_t* groups,
+                         const int32_t* prefix, int64_t n_groups, int64_t max_group, int64_t max_prefix,
+                         int64_t max_tail, const uint8_t* cache, int64_t pages, int64_t kv_heads, int64_t head_dim,
+                         int64_t page, int group, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,6 +22,7 @@ int kv4_read_block(const void* words);
 int kv4_copy_pages_block(const void* words);
 int kv4_attention_block(const void* words);
 int qk_norm_rope_block(const void* words);
+int kv4_prefix_attention_block(const void* words);
 int kv4_rope_append_block(const void* words);
 int beam_select_block(const void* words);
 int kv4_beam_reorder_block(const void* words);

@@ -33,7 +33,7 @@ __all__ = [
     "llm_int8_outliers", "llm_int8_workspace_bytes", "llm_int8_gemm", "awq_workspace_bytes", "awq_search", "stream_read",
     "kv4_cache", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention_workspace_bytes",
     "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope", "KvPages",
-    "kv4_rope_append", "beam_select_workspace_bytes", "beam_select", "kv4_beam_reorder",
+    "kv4_prefix_attention_workspace_bytes", "kv4_prefix_attention", "kv4_rope_append", "beam_select_workspace_bytes", "beam_select", "kv4_beam_reorder",
 ]
 
 F32, F16, BF16, I32 = 0, 1, 2, 3
@@ -106,6 +106,9 @@ _SIGS = {
     "rope_table": ([_P, _I64, _I64, ctypes.c_double, _P, _P], _I),
     "kv4_rope_append": ([_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _P, _P, _I64, _I64, _I, _P, _P,
                          _I, _F, _P, _P, _I64, _I64, _I64, _I64, _I, _P, _P], _I),
+    "kv4_prefix_attention_workspace_bytes": ([_I64] * 10 + [_I, _I64], _SZ),
+    "kv4_prefix_attention": ([_P, _I64, _I64, _I, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I64,
+                              _I64, _P, _I64, _I64, _I64, _I64, _I, _F, _P, _P, _P, _SZ, _P], _I),
     "beam_select_workspace_bytes": ([_I64] * 4, _SZ),
     "beam_select": ([_P, _I, _I64, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P], _I),
     "kv4_beam_reorder": ([_P, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P], _I),
@@ -114,7 +117,7 @@ _SIGS = {
 # one argument and not up to 27 (kv4_attention: 3.8 us a call by arguments, 0.7 by a block).
 _BLOCKS = {name: struct.Struct("=" + "".join("d" if t is _F else "q" for t in _SIGS[name][0]))
            for name in ("kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention", "qk_norm_rope",
-                        "kv4_rope_append", "beam_select", "kv4_beam_reorder")}
+                        "kv4_prefix_attention", "kv4_rope_append", "beam_select", "kv4_beam_reorder")}
 _SIGS.update({name + "_block": ([ctypes.c_char_p], _I) for name in _BLOCKS})
 
 
@@ -932,6 +935,78 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor
                 context.data_ptr(), page_table.data_ptr(), width, stride, cache.data_ptr(), pages, kv_heads, D, page,
                 group, D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr0(lse), _ptr0(workspace),
                 need if workspace is not None else 0, _stream(q))
+    return (out, lse) if return_lse else out
+
+
+@functools.lru_cache(maxsize=4096)      # of sizes alone
+def kv4_prefix_attention_workspace_bytes(T: int, seqs: int, max_q: int, n_groups: int, max_group: int, max_prefix: int,
+                                         max_tail: int, q_heads: int, kv_heads: int, head_dim: int, group: int,
+                                         max_context: int) -> int:
+    """Bytes that kv4_prefix_attention needs for these sizes (max_context: the page table's width in tokens)."""
+    return int(lib().kv4_prefix_attention_workspace_bytes(T, seqs, max_q, n_groups, max_group, max_prefix, max_tail,
+                                                          q_heads, kv_heads, head_dim, group, max_context))
+
+
+def kv4_prefix_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, context: torch.Tensor,
+                         groups: torch.Tensor, prefix: torch.Tensor, cu_q: Optional[torch.Tensor] = None,
+                         max_q: Optional[int] = None, max_group: Optional[int] = None, max_prefix: Optional[int] = None,
+                         max_tail: Optional[int] = None, scale: Optional[float] = None, return_lse: bool = False,
+                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """kv4_attention (without a window) where sequences groups[g] .. groups[g + 1] - 1 (int32 [n + 1]) have their first
+    prefix[g] (int32 [n]) tokens in common: these are attended to once for a group.  max_group, max_prefix and max_tail,
+    hints as max_q: the most sequences of a group, tokens of a prefix and tokens of a sequence behind it."""
+    T, q_heads, D = shape = _rows(q, "q", _HALVES)
+    dtype = q.dtype
+    pages, kv_heads, page, group = _cache_shape(cache, D)
+    if q_heads % kv_heads:
+        raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {kv_heads}")
+    qt, qh = _strides(q, "q")
+    if type(page_table) is not torch.Tensor or page_table.dtype is not torch.int32 or page_table.dim() != 2:
+        _req(page_table, "page_table", (torch.int32,), ndim=2)
+    seqs, width = page_table.shape
+    _vector(context, "context", torch.int32, seqs)
+    stride, one = page_table.stride()
+    if width > 1 and one != 1:
+        raise ValueError(f"page_table must have consecutive rows, has strides {page_table.stride()}")
+    if seqs < 2:
+        stride = width
+    if type(prefix) is not torch.Tensor or prefix.dtype is not torch.int32 or prefix.dim() != 1:
+        _req(prefix, "prefix", (torch.int32,), ndim=1)
+    n = prefix.shape[0]
+    if n < 1:
+        raise ValueError("needs at least one group")
+    _vector(groups, "groups", torch.int32, n + 1)
+    if cu_q is not None:
+        _vector(cu_q, "cu_q", torch.int32, seqs + 1)
+        most = max(1, T if max_q is None else int(max_q))
+    elif T != seqs:
+        raise ValueError(f"q has {T} rows for {seqs} sequences: without cu_q each has one")
+    else:
+        most = 1
+    tokens = max(1, width * page)
+    max_group = max(1, seqs if max_group is None else int(max_group))
+    max_prefix = max(1, tokens if max_prefix is None else int(max_prefix))
+    max_tail = max(1, tokens if max_tail is None else int(max_tail))
+    if out is not None:
+        _out(out, shape, dtype)
+    _on(q.get_device(), (page_table,), cache=cache, context=context, groups=groups, prefix=prefix, cu_q=cu_q, out=out,
+        workspace=workspace)
+    need = kv4_prefix_attention_workspace_bytes(T, seqs, most, n, max_group, max_prefix, max_tail, q_heads, kv_heads, D,
+                                                group, tokens)
+    if workspace is not None:
+        _req(workspace, "workspace", (torch.uint8,), ndim=1)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes; {need} needed")
+    else:
+        workspace = cache.new_empty(need)
+    if out is None:
+        out = _fresh(q, shape)
+    lse = q.new_empty((T, q_heads), dtype=torch.float32) if return_lse else None
+    _call_block("kv4_prefix_attention", q.data_ptr(), qt, qh, _DT[dtype], T, q_heads, _ptr0(cu_q), seqs, most,
+                context.data_ptr(), page_table.data_ptr(), width, stride, groups.data_ptr(), prefix.data_ptr(), n,
+                max_group, max_prefix, max_tail, cache.data_ptr(), pages, kv_heads, D, page, group,
+                D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr0(lse), workspace.data_ptr(),
+                workspace.numel(), _stream(q))
     return (out, lse) if return_lse else out
 
 

@@ -26,6 +26,7 @@ ARCH = "gfx950"
 
 SOURCES = ["abi.hip", "quantize.hip", "w4a16.hip", "w8a8.hip", "w8a16.hip", "formats.hip", "awq.hip",
            "kv4.hip", "kv4_attention.hip", "kv4_attention_bf16.hip", "kv4_attention_f16.hip",
+           "kv4_prefix.hip", "kv4_prefix_bf16.hip", "kv4_prefix_f16.hip",
            "rope.hip", "kv4_rope.hip", "beams.hip", "blocks.hip"]
 
 # Per-source extra flags.  The MFMA kernels keep their accumulators in

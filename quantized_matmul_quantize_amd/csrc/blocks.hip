@@ -41,3 +41,4 @@ extern "C" int qk_norm_rope_block(const void* words) { return call(qk_norm_rope,
 extern "C" int kv4_rope_append_block(const void* words) { return call(kv4_rope_append, static_cast<const int64_t*>(words)); }
 extern "C" int beam_select_block(const void* words) { return call(beam_select, static_cast<const int64_t*>(words)); }
 extern "C" int kv4_beam_reorder_block(const void* words) { return call(kv4_beam_reorder, static_cast<const int64_t*>(words)); }
+extern "C" int kv4_prefix_attention_block(const void* words) { return call(kv4_prefix_attention, static_cast<const int64_t*>(words)); }

@@ -183,27 +183,39 @@ struct Shape {
   static __device__ __forceinline__ int rot(int r) { return r * kChunks / 16; }
 };
 
-template <int DT, int D, int GROUP, int PK, int NT>
-__device__ __forceinline__ void attention_block(const AttnArgs& a) {
+// Where a part's results go: chunk `split` of a row's slots in the workspace.
+template <Part PART, typename A>
+__device__ __forceinline__ int64_t slot_of(const A& a, int64_t rh, int split) {
+  if constexpr (PART == kWhole) return rh * a.splits + split;
+  else return rh * (a.p_splits + a.splits) + (PART == kPrefix ? 0 : a.p_splits) + split;
+}
+
+template <int DT, int D, int GROUP, int PK, int NT, Part PART, typename A>
+__device__ __forceinline__ void attention_block(const A& a, uint32_t id, uint8_t* lds) {
   static_assert(PK == 1 || NT == 1, "steps are taken together for few rows only");
   using L = Shape<D, GROUP, PK, NT>;
   constexpr int G = L::kG, MT = L::kMTiles, kSteps = L::kSteps;
   constexpr float kOff = Int4Magic<QMM_F16>::offset;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * L::kWaveBytes];
-
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int r = lane & 15, kb = lane >> 4;
   const int bank = PK == 1 ? 0 : r / L::kCols;              // the step of a unit that column r keeps
 
-  uint32_t id = blockIdx.x;
-  const int split = static_cast<int>(id % a.splits);
-  id /= a.splits;
+  int32_t splits = a.splits, row_tiles = a.row_tiles;
+  if constexpr (PART == kPrefix) {
+    splits = a.p_splits;
+    row_tiles = a.p_row_tiles;
+  }
+  const int split = static_cast<int>(id % splits);
+  id /= splits;
   const int kvh = static_cast<int>(id % a.sh.heads);
   id /= a.sh.heads;
-  const int tile0 = static_cast<int>(id % a.row_tiles);
-  const int b = static_cast<int>(id / a.row_tiles);
-  const Sequence sq = sequence_of(a, b);
+  const int tile0 = static_cast<int>(id % row_tiles);
+  const int b = static_cast<int>(id / row_tiles);
+  Item item;
+  if constexpr (PART == kWhole) item = item_of(a, b);
+  else item = item_of<PART>(a, b);
+  const Sequence sq = item.sq;
   const int rows = sq.n * a.ratio;
 
   // Byte offsets of this lane's loads in a record: at + place * per.
@@ -227,7 +239,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
   uint8_t* const mine = lds + wave * L::kWaveBytes;
   const uint32_t mine_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(mine));
   typedef const __attribute__((address_space(4))) int32_t* table_t;
-  const table_t table = (table_t)(a.table + b * a.table_stride);
+  const table_t table = (table_t)(a.table + item.table_row * a.table_stride);
 
   // A 16-key tile past the context, or whose page is not of this cache, is
   // read through an empty resource: zeros, so scales of 0.
@@ -242,16 +254,25 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
     int key[PK], page[2 * PK];
   };
 
-  for (int tile = tile0; tile * L::kRows < rows; tile += a.row_tiles) {
+  for (int tile = tile0; tile * L::kRows < rows; tile += row_tiles) {
     const int row_lo = tile * L::kRows;
     const int row_hi = min(row_lo + L::kCols * NT, rows) - 1;
-    const int pos_lo = sq.first + row_lo / a.ratio;
+    // (rows of a prefix see all of its keys)
+    const int pos_lo = PART == kPrefix ? kBeyond - 1 : sq.first + row_lo / a.ratio;
     const int pos_hi = row_hi < row_lo ? -1 : sq.first + row_hi / a.ratio;
-    const Steps st = steps_of(a, sq.first + tile * L::kRows / a.ratio,
-                              sq.first + (min((tile + 1) * L::kRows, rows) - 1) / a.ratio);
-    const int chunks = max(1, (st.count + a.chunk - 1) / a.chunk);
+    Steps st;
+    Chunks ch;
+    if constexpr (PART == kWhole) {
+      st = steps_of(a, sq.first + tile * L::kRows / a.ratio,
+                    sq.first + (min((tile + 1) * L::kRows, rows) - 1) / a.ratio);
+      ch = {a.chunk, max(1, (st.count + a.chunk - 1) / a.chunk)};
+    } else {
+      st = {0, item.lo, steps_in(sq.ctx - item.lo)};
+      ch = part_chunks<PART>(a, item);
+    }
+    const int chunk = ch.chunk, chunks = ch.chunks;
     if (split >= chunks) continue;
-    const int s_lo = split * a.chunk + wave * PK, s_hi = min(split * a.chunk + a.chunk, st.count);
+    const int s_lo = split * chunk + wave * PK, s_hi = min(split * chunk + chunk, st.count);
     constexpr int kStride = PK * kWaves;
 
     auto unit_of = [&](int s) {
@@ -329,7 +350,7 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
       const int row = row_lo + 16 * n + r % L::kCols;
       const bool live = row < rows;
       const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;
-      pos[n] = live ? sq.first + tok : -1;
+      pos[n] = !live ? -1 : PART == kPrefix ? kBeyond - 1 : sq.first + tok;
       const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * kb;
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
@@ -708,9 +729,10 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
           }
           const int tok = row / a.ratio;
           const int64_t rh = static_cast<int64_t>(sq.row0 + tok) * a.q_heads + kvh * a.ratio + row - tok * a.ratio;
-          if (chunks > 1) {
-            *reinterpret_cast<f32x4*>(a.part_o + (rh * a.splits + split) * D + c0) = v;
-            if (c0 == 0) a.part_ml[rh * a.splits + split] = make_float2(M, sum);
+          if (chunks > 1 || item.shared) {
+            const int64_t at = slot_of<PART>(a, rh, split);
+            *reinterpret_cast<f32x4*>(a.part_o + at * D + c0) = v;
+            if (c0 == 0) a.part_ml[at] = make_float2(M, sum);
           } else {
             v *= inverse_of(sum);
             *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack_pair<DT>(v.x, v.y), pack_pair<DT>(v.z, v.w)};
@@ -727,9 +749,11 @@ __device__ __forceinline__ void attention_block(const AttnArgs& a) {
 // accumulator form every round copied the sums out and back for the test of
 // the maximum: 35 instead of 25 us for 7 sequences of 32 heads in groups of
 // 32), where the sums (NT D / 16) and a group's products and scales fit 256.
+constexpr int attention_occupancy(int D, int group, int pk, int nt) { return nt * D + 16 * (D / group) * pk * nt <= 320 ? 2 : 1; }
 template <int DT, int D, int GROUP, int PK, int NT>
-__global__ __launch_bounds__(256, NT * D + 16 * (D / GROUP) * PK * NT <= 320 ? 2 : 1) void attention_kernel(AttnArgs a) {
-  attention_block<DT, D, GROUP, PK, NT>(a);
+__global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, NT)) void attention_kernel(AttnArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, NT>::kWaveBytes];
+  attention_block<DT, D, GROUP, PK, NT, kWhole>(a, blockIdx.x, lds);
 }
 
 // Joins the chunks of rows whose keys were split: a block a row and head,
@@ -761,6 +785,53 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int row
       const float mc = ml[c].x;
       const float f = mc == -INFINITY ? 0.0f : exp2_fast(mc - m);
       o += *reinterpret_cast<const f32x4*>(a.part_o + (rh * a.splits + c) * D + 4 * c4) * f;
+    }
+    __syncthreads();
+    sums[threadIdx.x] = o;
+    __syncthreads();
+    if (part == 0) {
+#pragma unroll
+      for (int g = 1; g < kGroups; ++g) o += sums[g * kWide + c4];
+      o *= inverse_of(l);
+      *reinterpret_cast<u32x2*>(a.out + rh * D + 4 * c4) = u32x2{pack_pair<DT>(o.x, o.y), pack_pair<DT>(o.z, o.w)};
+      if (a.lse && c4 == 0) a.lse[rh] = lse_of(m, l);
+    }
+  }
+}
+
+// The same for a batch with shared prefixes: the chunks of the prefix, then the
+// sequence's own (rows of one chunk and no prefix have their results).
+template <int DT, int D>
+__global__ __launch_bounds__(256) void attention_join_parts_kernel(SharedArgs a) {
+  constexpr int kWide = D / 4, kGroups = 256 / kWide;
+  __shared__ f32x4 sums[256];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int part = threadIdx.x / kWide, c4 = threadIdx.x % kWide;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const Item item = own_item(a, b);
+  const int own = part_chunks<kOwn>(a, item).chunks;
+  const int before = item.shared ? chunks_of(steps_in(item.lo), a.p_splits, a.p_least, a.p_round).chunks : 0;
+  const int chunks = before + own;
+  if (!item.shared && own <= 1) return;
+  for (int i = blockIdx.x; i < item.sq.n; i += gridDim.x) {
+    const int64_t rh = static_cast<int64_t>(item.sq.row0 + i) * a.q_heads + h;
+    const int64_t first = rh * (a.p_splits + a.splits);
+    auto slot = [&](int c) { return first + (c < before ? c : a.p_splits + c - before); };
+    float m = -INFINITY, l = 0.0f;
+    for (int c = lane; c < chunks; c += kWave) m = fmaxf(m, a.part_ml[slot(c)].x);
+    m = wave_max(m);
+    for (int c = lane; c < chunks; c += kWave) {
+      const float2 ml = a.part_ml[slot(c)];
+      l += sum_at(ml.y, ml.x, m);
+    }
+    l = wave_sum(l);
+    f32x4 o{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int c = part; c < chunks; c += kGroups) {
+      const int64_t at = slot(c);
+      const float mc = a.part_ml[at].x;
+      const float f = mc == -INFINITY ? 0.0f : exp2_fast(mc - m);
+      o += *reinterpret_cast<const f32x4*>(a.part_o + at * D + 4 * c4) * f;
     }
     __syncthreads();
     sums[threadIdx.x] = o;

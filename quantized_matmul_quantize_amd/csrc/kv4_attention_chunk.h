@@ -40,6 +40,7 @@ struct Chunk {
   static constexpr int kVScales = kVOps * kVStride;         // binary16 [group][key]
   static constexpr int kVBuffer = kVScales + kG * kKeys * 2;
   static_assert(kKBuffer % 16 == 0 && kVBuffer % 16 == 0, "alignment");
+  static constexpr int kLds = 2 * kKBuffer + 2 * kVBuffer;
   // what a lane expands of a round: kWords words of a key's codes; of a word of two quads of values kNibbles
   // nibbles of either its low or its high half (kShare lanes a word)
   static constexpr int kWords = kKeys * D / (512 * kWaves), kKeyWaves = D / (32 * kWords);
@@ -50,8 +51,8 @@ struct Chunk {
 // are mapped so that any 16 lanes write 16 different rows: no bank conflicts.
 __device__ __forceinline__ int op_at(int r, int kb) { return 16 * (16 * kb + r); }
 
-template <int DT, int D, int GROUP, int NT>
-__device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
+template <int DT, int D, int GROUP, int NT, Part PART, typename A>
+__device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, uint8_t* keys_lds, uint8_t* values_lds) {
   using L = Chunk<D, GROUP, NT>;
   constexpr int G = L::kG, MT = GROUP / 16, KEYS = L::kKeys, kSteps = L::kSteps;
   constexpr int U = KEYS / kStep;                  // steps of a round
@@ -59,20 +60,28 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   constexpr int kWords = L::kWords;
   constexpr int kAhead = 2;                        // operands read before they are used
   constexpr int kAluMayCross = 0x6;                // sched_barrier: scalar and vector arithmetic
-  __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][L::kKBuffer];
-  __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][L::kVBuffer];
+  auto k_lds = [&](int i) { return keys_lds + i * L::kKBuffer; };      // two buffers of each
+  auto v_lds = [&](int i) { return values_lds + i * L::kVBuffer; };
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int r = lane & 15, kb = lane >> 4;
-  uint32_t id = blockIdx.x;
+  int32_t splits = a.splits, row_tiles = a.row_tiles, items = a.seqs;
+  if constexpr (PART == kPrefix) {
+    splits = a.p_splits;
+    row_tiles = a.p_row_tiles;
+    items = a.n_groups;
+  }
   const int kvh = static_cast<int>(id % a.sh.heads);
   id /= a.sh.heads;
-  const int split = static_cast<int>(id % a.splits);
-  id /= a.splits;
-  const int b = static_cast<int>(id % a.seqs);
-  const int order = static_cast<int>(id / a.seqs);
-  const Sequence sq = sequence_of(a, b);
+  const int split = static_cast<int>(id % splits);
+  id /= splits;
+  const int b = static_cast<int>(id % items);
+  const int order = static_cast<int>(id / items);
+  Item item;
+  if constexpr (PART == kWhole) item = item_of(a, b);
+  else item = item_of<PART>(a, b);
+  const Sequence sq = item.sq;
   const int rows = sq.n * a.ratio;
   const int tiles = (rows + L::kRows - 1) / L::kRows;
   const int record = static_cast<int>(a.sh.record_bytes());
@@ -80,7 +89,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   const uint32_t pages = static_cast<uint32_t>(a.sh.pages);
   const uint8_t* head = a.cache + static_cast<int64_t>(kvh) * record;
   typedef const __attribute__((address_space(4))) int32_t* table_t;
-  const table_t table = (table_t)(a.table + b * a.table_stride);
+  const table_t table = (table_t)(a.table + item.table_row * a.table_stride);
 
   // What a lane expands of a round.  Keys: kWords words of key r of a 16-key
   // tile (kKeyWaves wavefronts a tile).  Values: of one word of both quads
@@ -98,13 +107,23 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
   const int vp_at = a.sh.page * (D + 4 * G) + v_group * a.sh.page * 4 + 16 * v_quad;
 
   // the last tiles see the most keys and go first
-  for (int tile = tiles - 1 - order; tile >= 0; tile -= a.row_tiles) {
+  for (int tile = tiles - 1 - order; tile >= 0; tile -= row_tiles) {
     const int blk_last = min((tile + 1) * L::kRows, rows) - 1;
-    const int blk_lo = sq.first + tile * L::kRows / a.ratio, blk_hi = sq.first + blk_last / a.ratio;
-    const Steps st = steps_of(a, blk_lo, blk_hi);
-    const int chunks = max(1, (st.count + a.chunk - 1) / a.chunk);
+    // (rows of a prefix see all of its keys)
+    const int blk_lo = PART == kPrefix ? sq.ctx : sq.first + tile * L::kRows / a.ratio;
+    const int blk_hi = PART == kPrefix ? sq.ctx - 1 : sq.first + blk_last / a.ratio;
+    Steps st;
+    Chunks ch;
+    if constexpr (PART == kWhole) {
+      st = steps_of(a, blk_lo, blk_hi);
+      ch = {a.chunk, max(1, (st.count + a.chunk - 1) / a.chunk)};
+    } else {
+      st = {0, item.lo, steps_in(sq.ctx - item.lo)};
+      ch = part_chunks<PART>(a, item);
+    }
+    const int chunk = ch.chunk, chunks = ch.chunks;
     if (split >= chunks) continue;
-    const int s_lo = split * a.chunk, s_hi = min(s_lo + a.chunk, st.count);
+    const int s_lo = split * chunk, s_hi = min(s_lo + chunk, st.count);
     const int rounds = (s_hi - s_lo + U - 1) / U;
     // Keys that no row of the block sees: past blk_hi, in the last round, or up to
     // `hide` and no sinks, in the step where the window begins and the one before
@@ -112,7 +131,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     const int hide = a.window > 0 ? blk_lo - a.window : -1;
     const int row_lo = tile * L::kRows + wave * 16 * NT;
     const int row_hi = min(row_lo + 16 * NT, rows) - 1;
-    const int pos_lo = sq.first + row_lo / a.ratio;
+    const int pos_lo = PART == kPrefix ? kBeyond - 1 : sq.first + row_lo / a.ratio;
     const int pos_hi = row_hi < row_lo ? -1 : sq.first + row_hi / a.ratio;
 
     // ---- queries: second operands, the block's power of two, positions
@@ -124,7 +143,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       const int row = row_lo + 16 * n + r;
       const bool live = row < rows;
       const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;
-      pos[n] = live ? sq.first + tok : -1;
+      pos[n] = !live ? -1 : PART == kPrefix ? kBeyond - 1 : sq.first + tok;
       const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * kb;
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
@@ -133,7 +152,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
     float unscale = 1.0f;
     __syncthreads();                               // LDS is free: the rows before are done
     if constexpr (DT == QMM_BF16) {
-      float* stat = reinterpret_cast<float*>(&k_lds[0][0]);
+      float* stat = reinterpret_cast<float*>(k_lds(0));
       most = wave_max(most);
       if (lane == 0) stat[wave] = most;
       __syncthreads();
@@ -409,20 +428,20 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       fetch_values(first);
       clean_keys(k0);
       clean_values(first);
-      expand_keys(&k_lds[0][0]);
-      expand_values(&v_lds[0][0]);
+      expand_keys(k_lds(0));
+      expand_values(v_lds(0));
       fetch_keys(k1);
       fetch_values(next);
       clean_keys(k1);
-      expand_keys(&k_lds[1][0]);
+      expand_keys(k_lds(1));
       fetch_keys(k_now);
       __syncthreads();
-      scores(&k_lds[0][0], x);
+      scores(k_lds(0), x);
       mask(first);
       __syncthreads();                             // the keys of round 0 may be replaced
     }
     for (int round = 0; round < rounds; ++round) {
-      const uint8_t* vb = &v_lds[round & 1][0];
+      const uint8_t* vb = v_lds(round & 1);
       const Round fourth = round_of(round + 3);
       const Mine k_fifth = mine_of(round + 4);
       // ---- the largest scale of the values, of every second key; the scales
@@ -508,7 +527,7 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       // 832 us.
       u32x4 p[NT][U];
       f32x4 ahead[NT][2 * U];
-      scores(&k_lds[(round + 1) & 1][0], ahead);
+      scores(k_lds((round + 1) & 1), ahead);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -566,8 +585,8 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
           __builtin_amdgcn_sched_barrier(kAluMayCross);
         }
       }
-      expand_keys(&k_lds[round & 1][0]);
-      expand_values(&v_lds[(round + 1) & 1][0]);
+      expand_keys(k_lds(round & 1));
+      expand_values(v_lds((round + 1) & 1));
       fetch_keys(k_next);
       fetch_values(third);
 #pragma unroll
@@ -594,7 +613,9 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
       if (row >= rows) continue;
       const int tok = row / a.ratio;
       const int64_t rh = static_cast<int64_t>(sq.row0 + tok) * a.q_heads + kvh * a.ratio + row - tok * a.ratio;
-      const float inv = chunks > 1 ? 1.0f : inverse_of(sum);
+      const bool partial = chunks > 1 || item.shared;
+      const int64_t at = slot_of<PART>(a, rh, split);
+      const float inv = partial ? 1.0f : inverse_of(sum);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const float f = inv / static_cast<float>(shrink[n][g][0]);
@@ -602,14 +623,14 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
         for (int y = 0; y < MT; ++y) {
           const f32x4 v = o[n][g][y] * f;
           const int c0 = (g * MT + y) * 16 + 4 * kb;
-          if (chunks > 1)
-            *reinterpret_cast<f32x4*>(a.part_o + (rh * a.splits + split) * D + c0) = v;
+          if (partial)
+            *reinterpret_cast<f32x4*>(a.part_o + at * D + c0) = v;
           else
             *reinterpret_cast<u32x2*>(a.out + rh * D + c0) = u32x2{pack_pair<DT>(v.x, v.y), pack_pair<DT>(v.z, v.w)};
         }
       }
       if (kb == 0) {
-        if (chunks > 1) a.part_ml[rh * a.splits + split] = make_float2(base[n], sum);
+        if (partial) a.part_ml[at] = make_float2(base[n], sum);
         else if (a.lse) a.lse[rh] = lse_of(base[n], sum);
       }
     }
@@ -622,7 +643,9 @@ __device__ __forceinline__ void attention_chunk_block(const AttnArgs& a) {
 // but half as many blocks.)
 template <int DT, int D, int GROUP, int NT>
 __global__ __launch_bounds__(256, D / GROUP < 8 ? 2 : 1) void attention_chunk_kernel(AttnArgs a) {
-  attention_chunk_block<DT, D, GROUP, NT>(a);
+  using L = Chunk<D, GROUP, NT>;
+  __shared__ __attribute__((aligned(16))) uint8_t keys[2 * L::kKBuffer], values[2 * L::kVBuffer];
+  attention_chunk_block<DT, D, GROUP, NT, kWhole>(a, blockIdx.x, keys, values);
 }
 
 }  // namespace

@@ -1,0 +1,66 @@
+// kv4_prefix_launch.h -- from the plans of a batch with shared prefixes to the
+// kernels that they name.
+#pragma once
+
+#include "kv4_attention.h"
+#include "kv4_attention_chunk.h"
+
+namespace qmm {
+namespace {
+
+template <int DT, int D, int GROUP, int PK, int NT, Part PART>
+__global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, NT)) void attention_part_kernel(SharedArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, NT>::kWaveBytes];
+  attention_block<DT, D, GROUP, PK, NT, PART>(a, blockIdx.x, lds);
+}
+template <int DT, int D, int GROUP, int NT, Part PART>
+__global__ __launch_bounds__(256, D / GROUP < 8 ? 2 : 1) void attention_part_chunk_kernel(SharedArgs a) {
+  using L = Chunk<D, GROUP, NT>;
+  __shared__ __attribute__((aligned(16))) uint8_t keys[2 * L::kKBuffer], values[2 * L::kVBuffer];
+  attention_chunk_block<DT, D, GROUP, NT, PART>(a, blockIdx.x, keys, values);
+}
+
+template <int DT, int D, int GROUP, Part PART>
+void launch_part(const SharedArgs& a, const AttnPlan& p, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.blocks));
+  constexpr int kTiles = attention_tiles(D, GROUP);
+  if (!p.ws) {
+    attention_part_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP), PART><<<grid, 256, 0, s>>>(a);
+  } else if (p.pk == 2) {
+    if constexpr (attention_pairs(D, GROUP)) attention_part_kernel<DT, D, GROUP, 2, 1, PART><<<grid, 256, 0, s>>>(a);
+  } else if (p.nt == 1) {
+    attention_part_kernel<DT, D, GROUP, 1, 1, PART><<<grid, 256, 0, s>>>(a);
+  } else {
+    attention_part_kernel<DT, D, GROUP, 1, kTiles, PART><<<grid, 256, 0, s>>>(a);
+  }
+}
+template <int DT, int D, int GROUP>
+void launch_parts(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s) {
+  launch_part<DT, D, GROUP, kPrefix>(a, prefix, s);
+  launch_part<DT, D, GROUP, kOwn>(a, own, s);
+}
+
+template <int DT>
+void launch_prefix(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s) {
+  const int D = a.sh.D, g = a.sh.group;
+  if (D == 64) {
+    if (g == 32) launch_parts<DT, 64, 32>(a, prefix, own, s);
+    else launch_parts<DT, 64, 64>(a, prefix, own, s);
+  } else if (D == 128) {
+    if (g == 32) launch_parts<DT, 128, 32>(a, prefix, own, s);
+    else if (g == 64) launch_parts<DT, 128, 64>(a, prefix, own, s);
+    else launch_parts<DT, 128, 128>(a, prefix, own, s);
+  } else {
+    if (g == 32) launch_parts<DT, 256, 32>(a, prefix, own, s);
+    else if (g == 64) launch_parts<DT, 256, 64>(a, prefix, own, s);
+    else launch_parts<DT, 256, 128>(a, prefix, own, s);
+  }
+  const dim3 grid(static_cast<unsigned>(own.max_q < 1024 ? own.max_q : 1024), static_cast<unsigned>(a.q_heads),
+                  static_cast<unsigned>(a.seqs));
+  if (D == 64) attention_join_parts_kernel<DT, 64><<<grid, 256, 0, s>>>(a);
+  else if (D == 128) attention_join_parts_kernel<DT, 128><<<grid, 256, 0, s>>>(a);
+  else attention_join_parts_kernel<DT, 256><<<grid, 256, 0, s>>>(a);
+}
+
+}  // namespace
+}  // namespace qmm

@@ -169,3 +169,59 @@ def test_reorder_checks():
     raises(lambda: f(cache, 128, table, ctx, tails, parents, context_out=ctx), "other memory")
     raises(lambda: f(cache, 128, table, ctx, tails, parents, table_out=t((8, 4), i32)), "table_out has shape")
     raises(lambda: f(cache, 128, table, ctx, tails, parents), "device tensors")
+
+
+# ---------------------------------------------------------------------------
+# Attention over shared prefixes.
+# ---------------------------------------------------------------------------
+def prefix_args(**k):
+    g = k.get
+    return [g("q", P), g("qts", 4096), g("qhs", 128), g("dt", BF16), g("T", 4), g("hq", 32), g("cu", None), g("seqs", 4),
+            g("max_q", 1), g("context", P), g("table", P), g("width", 20), g("stride", 20), g("groups", P), g("prefix", P),
+            g("n", 2), g("mg", 3), g("mp", 1000), g("mt", 100), g("cache", P), g("pages", 100), g("hk", 8), g("D", 128),
+            g("page", 64), g("group", 64), ctypes.c_float(g("scale", 0.1)), g("out", P), None, g("ws", P),
+            g("wsb", 10 ** 12), None]
+
+
+def test_prefix_attention_errors():
+    f, a = qmm.lib().kv4_prefix_attention, prefix_args
+    assert f(*a(T=0, q=None)) == OK
+    for kw in [dict(q=None), dict(context=None), dict(table=None), dict(groups=None), dict(prefix=None), dict(cache=None),
+               dict(out=None), dict(T=-1), dict(seqs=0), dict(T=5), dict(max_q=0), dict(n=0), dict(n=-1), dict(mg=0),
+               dict(mp=0), dict(mt=-2), dict(width=0), dict(stride=19), dict(scale=float("nan")), dict(hq=33), dict(hq=0),
+               dict(hk=0), dict(dt=8), dict(pages=0)]:
+        assert f(*a(**kw)) == EINVAL, kw
+    for kw in [dict(dt=F32), dict(D=96), dict(page=8), dict(group=16)]:
+        assert f(*a(**kw)) == EUNSUP, kw
+    for kw in [dict(T=1 << 31, cu=P), dict(seqs=70000, T=70000), dict(n=70000), dict(width=1 << 25, stride=1 << 25),
+               dict(hq=80000, hk=8), dict(T=1 << 27, cu=P), dict(hk=4096, hq=4096, n=65535)]:
+        assert f(*a(**kw)) == ERANGE, kw
+    for kw in [dict(q=MIS), dict(out=MIS), dict(cache=P + 8), dict(qts=4100), dict(qhs=4), dict(table=P + 2),
+               dict(context=P + 1), dict(cu=P + 2), dict(groups=P + 2), dict(prefix=P + 3), dict(ws=MIS)]:
+        assert f(*a(**kw)) == EALIGN, kw
+    need = qmm.kv4_prefix_attention_workspace_bytes(4, 4, 1, 2, 3, 1000, 100, 32, 8, 128, 64, 20 * 64)
+    assert need >= 2 * 4 * 32 * (128 + 2) * 4 and need % (4 * 32 * 4) == 0
+    assert f(*a(ws=None)) == EWS and f(*a(wsb=need - 1)) == EWS
+    w = lambda **k: qmm.lib().kv4_prefix_attention_workspace_bytes(*[k.get(x, d) for x, d in dict(
+        T=4, seqs=4, max_q=1, n=2, mg=3, mp=1000, mt=100, hq=32, hk=8, D=128, group=64, tokens=1280).items()])
+    assert w() == need
+    for kw in [dict(T=0), dict(seqs=0), dict(max_q=0), dict(n=0), dict(mg=0), dict(mp=0), dict(mt=0), dict(hq=33), dict(hk=0),
+               dict(D=0), dict(group=0), dict(tokens=0), dict(tokens=1 << 31), dict(seqs=1 << 17), dict(n=1 << 17)]:
+        assert w(**kw) == 0, kw
+
+
+def test_prefix_attention_checks():
+    q, cache, table, ctx = t((4, 8, 128), bf16), t((3, 2, 64, 144), u8), t((4, 5), i32), t(4, i32)
+    groups, prefix, f = t(3, i32), t(2, i32), qmm.kv4_prefix_attention
+    raises(lambda: f(q.float(), cache, table, ctx, groups, prefix), "q has dtype")
+    raises(lambda: f(q[:, :7], cache, table, ctx, groups, prefix), "multiple")
+    raises(lambda: f(q, cache, table.long(), ctx, groups, prefix), "page_table has dtype")
+    raises(lambda: f(q, cache, table, ctx[:3], groups, prefix), "context has shape")
+    raises(lambda: f(q, cache, table, ctx, groups[:2], prefix), "groups has shape")
+    raises(lambda: f(q, cache, table, ctx, groups.long(), prefix), "groups has dtype")
+    raises(lambda: f(q, cache, table, ctx, groups, prefix.long()), "prefix has dtype")
+    raises(lambda: f(q, cache, table, ctx, groups[:1], prefix[:0]), "at least one group")
+    raises(lambda: f(q[:3], cache, table, ctx, groups, prefix), "3 rows for 4")
+    raises(lambda: f(q, cache, table, ctx, groups, prefix, cu_q=t(4, i32)), "cu_q has shape")
+    raises(lambda: f(q, cache, table, ctx, groups, prefix, out=t((4, 8, 64), bf16)), "out has shape")
+    raises(lambda: f(q, cache, table, ctx, groups, prefix), "device tensors")
