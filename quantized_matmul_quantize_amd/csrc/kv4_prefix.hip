@@ -29,7 +29,7 @@ AttnPlan part_plan(int64_t items, int64_t rows, int64_t kv_heads, int64_t D, int
   p.row_tiles = std::min(ceil_div(rows, p.rows), std::max<int64_t>(1, (int64_t{1} << 22) / (items * kv_heads)));
   const int64_t steps = std::max<int64_t>(1, ceil_div(keys, kStep)), blocks = items * kv_heads * p.row_tiles;
   *round = p.ws ? kWaves * p.pk : D == 256 ? 1 : 2;
-  p.splits = std::max<int64_t>(1, std::min(ceil_div(fill, blocks), steps / std::max(kLeastSteps, *round)));
+  p.splits = std::max<int64_t>(1, std::min(fill / blocks, steps / std::max(kLeastSteps, *round)));
   p.blocks = blocks * p.splits;
   return p;
 }
