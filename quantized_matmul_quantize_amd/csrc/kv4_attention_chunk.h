@@ -66,18 +66,13 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int r = lane & 15, kb = lane >> 4;
-  int32_t splits = a.splits, row_tiles = a.row_tiles, items = a.seqs;
-  if constexpr (PART == kPrefix) {
-    splits = a.p_splits;
-    row_tiles = a.p_row_tiles;
-    items = a.n_groups;
-  }
+  static_assert(PART != kPrefix, "a prefix has no masks: kv4_attention_rows.h");
   const int kvh = static_cast<int>(id % a.sh.heads);
   id /= a.sh.heads;
-  const int split = static_cast<int>(id % splits);
-  id /= splits;
-  const int b = static_cast<int>(id % items);
-  const int order = static_cast<int>(id / items);
+  const int split = static_cast<int>(id % a.splits);
+  id /= a.splits;
+  const int b = static_cast<int>(id % a.seqs);
+  const int order = static_cast<int>(id / a.seqs);
   Item item;
   if constexpr (PART == kWhole) item = item_of(a, b);
   else item = item_of<PART>(a, b);
@@ -107,11 +102,9 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
   const int vp_at = a.sh.page * (D + 4 * G) + v_group * a.sh.page * 4 + 16 * v_quad;
 
   // the last tiles see the most keys and go first
-  for (int tile = tiles - 1 - order; tile >= 0; tile -= row_tiles) {
+  for (int tile = tiles - 1 - order; tile >= 0; tile -= a.row_tiles) {
     const int blk_last = min((tile + 1) * L::kRows, rows) - 1;
-    // (rows of a prefix see all of its keys)
-    const int blk_lo = PART == kPrefix ? sq.ctx : sq.first + tile * L::kRows / a.ratio;
-    const int blk_hi = PART == kPrefix ? sq.ctx - 1 : sq.first + blk_last / a.ratio;
+    const int blk_lo = sq.first + tile * L::kRows / a.ratio, blk_hi = sq.first + blk_last / a.ratio;
     Steps st;
     Chunks ch;
     if constexpr (PART == kWhole) {
@@ -131,7 +124,7 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
     const int hide = a.window > 0 ? blk_lo - a.window : -1;
     const int row_lo = tile * L::kRows + wave * 16 * NT;
     const int row_hi = min(row_lo + 16 * NT, rows) - 1;
-    const int pos_lo = PART == kPrefix ? kBeyond - 1 : sq.first + row_lo / a.ratio;
+    const int pos_lo = sq.first + row_lo / a.ratio;
     const int pos_hi = row_hi < row_lo ? -1 : sq.first + row_hi / a.ratio;
 
     // ---- queries: second operands, the block's power of two, positions
@@ -143,7 +136,7 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
       const int row = row_lo + 16 * n + r;
       const bool live = row < rows;
       const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;
-      pos[n] = !live ? -1 : PART == kPrefix ? kBeyond - 1 : sq.first + tok;
+      pos[n] = live ? sq.first + tok : -1;
       const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * kb;
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};

@@ -15,7 +15,8 @@ constexpr int64_t kLeastSteps = 8;
 
 // How a part is cut: `items` (groups, or sequences) of up to `rows` rows and
 // `keys` keys.  Which kernel: by rows, as for a batch without prefixes.
-AttnPlan part_plan(int64_t items, int64_t rows, int64_t kv_heads, int64_t D, int group, int64_t keys, int64_t* round) {
+AttnPlan part_plan(bool prefix, int64_t items, int64_t rows, int64_t kv_heads, int64_t D, int group, int64_t keys,
+                   int64_t* round) {
   AttnPlan p{};
   const int d = static_cast<int>(D);
   const int64_t fill = 2 * device_cus();
@@ -24,13 +25,14 @@ AttnPlan part_plan(int64_t items, int64_t rows, int64_t kv_heads, int64_t D, int
   const bool sixteens = eights || rows <= 16 || items * kv_heads * ceil_div(rows, 16) < fill;
   p.pk = eights && attention_pairs(d, group) ? 2 : 1;
   p.nt = !p.ws ? attention_chunk_tiles(d, group) : sixteens ? 1 : attention_tiles(d, group);
-  p.rows = 16 / p.pk * p.nt * (p.ws ? 1 : kWaves);
+  p.rows = p.ws ? 16 / p.pk * p.nt : (prefix ? 32 : 16 * p.nt) * kWaves;
   // (blocks loop over row tiles past these: a launch holds 2^24 blocks of 256 threads)
   p.row_tiles = std::min(ceil_div(rows, p.rows), std::max<int64_t>(1, (int64_t{1} << 22) / (items * kv_heads)));
   const int64_t steps = std::max<int64_t>(1, ceil_div(keys, kStep)), blocks = items * kv_heads * p.row_tiles;
   *round = p.ws ? kWaves * p.pk : D == 256 ? 1 : 2;
   p.splits = std::max<int64_t>(1, std::min(fill / blocks, steps / std::max(kLeastSteps, *round)));
   p.blocks = blocks * p.splits;
+  if (!p.ws && prefix) p.blocks = ceil_div(items * kv_heads * p.splits, 8) * 8 * p.row_tiles;
   return p;
 }
 
@@ -43,8 +45,8 @@ Plans plans_of(int64_t seqs, int64_t max_q, int64_t n_groups, int64_t max_group,
   Plans p;
   max_q = std::min(max_q, T);
   const int64_t rows = std::min(std::min(max_group, seqs) * max_q, T) * ratio;
-  p.prefix = part_plan(n_groups, rows, kv_heads, D, group, std::min(max_prefix, tokens), &p.p_round);
-  p.own = part_plan(seqs, max_q * ratio, kv_heads, D, group, std::min(max_tail, tokens), &p.round);
+  p.prefix = part_plan(true, n_groups, rows, kv_heads, D, group, std::min(max_prefix, tokens), &p.p_round);
+  p.own = part_plan(false, seqs, max_q * ratio, kv_heads, D, group, std::min(max_tail, tokens), &p.round);
   p.own.max_q = max_q;
   return p;
 }

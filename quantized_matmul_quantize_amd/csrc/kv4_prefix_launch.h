@@ -4,6 +4,7 @@
 
 #include "kv4_attention.h"
 #include "kv4_attention_chunk.h"
+#include "kv4_attention_rows.h"
 
 namespace qmm {
 namespace {
@@ -13,11 +14,11 @@ __global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, NT)) void at
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, NT>::kWaveBytes];
   attention_block<DT, D, GROUP, PK, NT, PART>(a, blockIdx.x, lds);
 }
-template <int DT, int D, int GROUP, int NT, Part PART>
-__global__ __launch_bounds__(256, D / GROUP < 8 ? 2 : 1) void attention_part_chunk_kernel(SharedArgs a) {
+template <int DT, int D, int GROUP, int NT>
+__global__ __launch_bounds__(256, D / GROUP < 8 ? 2 : 1) void attention_own_chunk_kernel(SharedArgs a) {
   using L = Chunk<D, GROUP, NT>;
   __shared__ __attribute__((aligned(16))) uint8_t keys[2 * L::kKBuffer], values[2 * L::kVBuffer];
-  attention_chunk_block<DT, D, GROUP, NT, PART>(a, blockIdx.x, keys, values);
+  attention_chunk_block<DT, D, GROUP, NT, kOwn>(a, blockIdx.x, keys, values);
 }
 
 template <int DT, int D, int GROUP, Part PART>
@@ -25,7 +26,8 @@ void launch_part(const SharedArgs& a, const AttnPlan& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.blocks));
   constexpr int kTiles = attention_tiles(D, GROUP);
   if (!p.ws) {
-    attention_part_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP), PART><<<grid, 256, 0, s>>>(a);
+    if constexpr (PART == kPrefix) attention_rows_kernel<DT, D, GROUP><<<grid, 256, 0, s>>>(a);
+    else attention_own_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP)><<<grid, 256, 0, s>>>(a);
   } else if (p.pk == 2) {
     if constexpr (attention_pairs(D, GROUP)) attention_part_kernel<DT, D, GROUP, 2, 1, PART><<<grid, 256, 0, s>>>(a);
   } else if (p.nt == 1) {

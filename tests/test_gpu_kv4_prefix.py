@@ -4,7 +4,10 @@ sequence by itself.
 Bounds: kv4_bounds.py's, of one pass over a row's keys.  Here a row has up to
 60 parts, each within that (its statistics are relative to its own largest),
 joined in fp32: a factor (2 u), a product and a sum a part, (60 + 4) u of the
-mass and of the sum of probabilities."""
+mass and of the sum of probabilities.  The kernel for prefixes of many rows
+rounds each value to binary16, (c - z) / 16 times its scale: 2^-11 of it, so
+twice the rounding of the probabilities, or half a step of 2^-24 below 2^-14,
+2^-21 of the value."""
 import math
 
 import numpy as np
@@ -79,8 +82,9 @@ class Groups:
         for _, t in plan:
             most = max(most, sum(self.queries[at:at + len(t)]))
             at += len(t)
-        # more rows than the kernel for few takes: bf16 probabilities through two roundings
-        self.roundings = 2 if dtype == BF16 and max(most, max(self.queries)) * (hq // hkv) > 96 else 1
+        # more rows than the kernel for few takes: values (of a sequence's own keys, bf16 probabilities) rounded as well
+        self.many = most * (hq // hkv) > 96
+        self.roundings = 2 if self.many or dtype == BF16 and max(self.queries) * (hq // hkv) > 96 else 1
         self.hints = dict(max_group=max(len(t) for _, t in plan), max_prefix=max(1, max(p for p, _ in plan)),
                           max_tail=max([1] + self.lens[:len(before)] + [x or 1 for _, t in plan for x in t]))
 
@@ -103,7 +107,7 @@ class Groups:
         none = np.repeat((count == 0)[:, None], hq, 1)
         assert (out.cpu().float()[torch.from_numpy(none & rows)] == 0).all()
         mass = np.abs(np.concatenate([v.reshape(-1) for v in self.v])).max()
-        bound = b_out + 64 * U * mass + OUT_HALF_ULP[self.dtype] * np.abs(o) + (2.0 ** -25 if self.dtype == F16 else 0.0)
+        bound = b_out + 64 * U * mass + self.many * 2.0 ** -21 + OUT_HALF_ULP[self.dtype] * np.abs(o) + (2.0 ** -25 if self.dtype == F16 else 0.0)
         err = np.abs(out.float().cpu().numpy() - o)
         bad = ~(err <= bound) & (rows & ~none)[..., None]
         assert not bad.any(), f"out: {bad.sum()} past their bounds, at {np.argwhere(bad)[:3]}"
