@@ -55,6 +55,8 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   using L = Rows<D, GROUP>;
   constexpr int G = L::kG, KEYS = L::kKeys, kTiles = L::kTiles, kSteps = L::kSteps, kCh = L::kChannels;
   constexpr int kGSteps = GROUP / 16, kPages = KEYS / 16;
+  constexpr int kAhead = 4;                        // operands read before they are used
+  constexpr int kAluMayCross = 0x6;                // sched_barrier: scalar and vector arithmetic
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int r = lane & 31, h = lane >> 5;
@@ -162,10 +164,10 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   auto expand_keys = [&](uint8_t* buf) {
 #pragma unroll
     for (int w = 0; w < L::kWords; ++w) {
-      // word k_part + 4 (k_first + w): k-extent 2 (k_first + w) + k_part / 2
+      // word k_part + 4 (k_first + w), in the 32 channels k_first + w
       uint32_t par = k_par[0];
 #pragma unroll
-      for (int i = 1; i < G; ++i) par = (2 * (k_first + w) + (k_part >> 1)) / kGSteps == i ? k_par[i] : par;
+      for (int i = 1; i < G; ++i) par = (k_first + w) / (GROUP / 32) == i ? k_par[i] : par;
       const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
       uint32_t p[4];
       Codes64::unpack(k_raw[w], magic, p);
@@ -245,27 +247,34 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
       const int k_after = k_page_of(round + 3), v_after = v_page_of(round + 3);
       if (active) {
         // ---- scores less the base they are taken at
-        f32x16 x[kTiles];
+        f32x16 x[kTiles], acc[kTiles];
+        {
+          constexpr int kOps = kSteps * kTiles;
+          u32x4 k[kAhead];
+          auto read = [&](int i) {
+            return *reinterpret_cast<const u32x4*>(kb + ((i % kTiles * kSteps + i / kTiles) * 2 + h) * L::kHalf + 16 * r);
+          };
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          f32x16 acc[kTiles];
+          for (int i = 0; i < kAhead; ++i) k[i] = read(i);
+          __builtin_amdgcn_sched_barrier(kAluMayCross);
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t)
+          for (int i = 0; i < kOps; ++i) {
+            const int t = i % kTiles, j = i / kTiles, grp = j / kGSteps;
+            if (j % kGSteps == 0)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
+              for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
+            acc[t] = mfma32(k[i % kAhead], qv[j], acc[t]);
+            if (i + kAhead < kOps) k[i % kAhead] = read(i + kAhead);
+            __builtin_amdgcn_sched_barrier(kAluMayCross);
+            if (j % kGSteps == kGSteps - 1)
 #pragma unroll
-          for (int j = i * kGSteps; j < (i + 1) * kGSteps; ++j)
+              for (int c = 0; c < 4; ++c) {
+                const f32x4 sc = *reinterpret_cast<const f32x4*>(kb + L::kKOps + (grp * KEYS + 32 * t + 8 * c + 4 * h) * 4);
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-              acc[t] = mfma32(*reinterpret_cast<const u32x4*>(kb + ((t * kSteps + j) * 2 + h) * L::kHalf + 16 * r), qv[j], acc[t]);
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const f32x4 sc = *reinterpret_cast<const f32x4*>(kb + L::kKOps + (i * KEYS + 32 * t + 8 * c + 4 * h) * 4);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[t][4 * c + e] = fmaf(acc[t][4 * c + e], sc[e], i == 0 ? -from : x[t][4 * c + e]);
-            }
+                for (int e = 0; e < 4; ++e)
+                  x[t][4 * c + e] = fmaf(acc[t][4 * c + e], sc[e], grp == 0 ? -from : x[t][4 * c + e]);
+              }
+          }
         }
         // ---- keys of no page
         int holes = 0;
@@ -309,14 +318,24 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
             p[t][e / 8][e / 2 % 4] = pack_pair<QMM_F16>(p0, p1);
           }
         // ---- sums
+        {
+          constexpr int kOps = kTiles * 2 * kCh;
+          u32x4 v[kAhead];
+          auto read = [&](int i) {
+            const int c = i % kCh, m = i / kCh;               // m: 16 keys
+            return *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
+          };
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+          for (int i = 0; i < kAhead; ++i) v[i] = read(i);
+          __builtin_amdgcn_sched_barrier(kAluMayCross);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int c = 0; c < kCh; ++c)
-              o[c] = mfma32(*reinterpret_cast<const u32x4*>(vb + (((t * kCh + c) * 2 + m) * 2 + h) * L::kHalf + value_row(r) * 16),
-                            p[t][m], o[c]);
+          for (int i = 0; i < kOps; ++i) {
+            const int c = i % kCh, m = i / kCh;
+            o[c] = mfma32(v[i % kAhead], p[m / 2][m % 2], o[c]);
+            if (i + kAhead < kOps) v[i % kAhead] = read(i + kAhead);
+            __builtin_amdgcn_sched_barrier(kAluMayCross);
+          }
+        }
       }
       if (round + 1 < rounds) {
         expand_keys(k_lds(round + 1));
