@@ -36,7 +36,9 @@ SOURCES = ["abi.hip", "quantize.hip", "w4a16.hip", "w8a8.hip", "w8a16.hip", "for
 EXTRA = {"w8a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
          "w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
          "w8a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-         "formats.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+         "formats.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "kv4_prefix_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+         "kv4_prefix_f16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

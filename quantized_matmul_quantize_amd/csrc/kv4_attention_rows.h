@@ -32,36 +32,57 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
 template <int D, int GROUP>
 struct Rows {
   static constexpr int kG = D / GROUP;
+  static constexpr int kW = D == 256 ? 4 : 8;                // wavefronts: by the registers of sums and queries
+  static constexpr int kThreads = kWave * kW;
   static constexpr int kStrip = 32;                          // rows of a wavefront
-  static constexpr int kKeys = D == 256 ? 32 : 64;           // of a round
-  static constexpr int kTiles = kKeys / 32, kSteps = D / 16, kChannels = D / 32;
+  static constexpr int kKeys = 8 * kW, kTiles = kKeys / 32;  // of a round
+  static constexpr int kSteps = D / 16, kChannels = D / 32;
   // Operands of 1 KiB, [tile][k-extent] of keys, [tile][32 channels][16 keys] of
   // values, each in two halves of 544 bytes: writers' eight lanes at a time then
-  // meet every bank once, as readers' do.
+  // meet every bank once, as readers' do.  Two buffers of each.
   static constexpr int kHalf = 544;
   static constexpr int kKOps = kTiles * kSteps * 2 * kHalf;
   static constexpr int kKBuffer = kKOps + kG * kKeys * 4;    // fp32 scales [group][key]
   static constexpr int kVBuffer = kTiles * kChannels * 2 * 2 * kHalf;
-  static constexpr int kLds = 2 * (kKBuffer + kVBuffer);
-  static constexpr int kWords = kKeys * D / 8 / 256;         // of keys, that a thread expands
-  static constexpr int kNibbles = D == 64 ? 2 : 4;           // channels of values
+  // Codes as they lie in memory, kRing rounds: a round of few rows takes less
+  // than memory does to answer.  Of each 16-key tile codes, then params [group][16].
+  static constexpr int kRing = 6;
+  static constexpr int kCodes = 8 * D, kParams = 64 * kG;    // of a tile
+  static constexpr int kRaw = kKeys / 16 * (kCodes + kParams);
+  static constexpr int kSlot = 2 * kRaw;                     // keys, values
+  static constexpr int kPagesAt = 2 * (kKBuffer + kVBuffer) + kRing * kSlot;      // a wavefront's next 64 pages
+  static constexpr int kLds = kPagesAt + kW * kWave * 4;
+  static constexpr int kLoads = kCodes / 1024 > 1 ? 3 : 2;   // of a wavefront a round
+  // words of keys, and channels of a word of values, that a thread expands a round
+  static constexpr int kWords = kKeys * D / 8 / kThreads;
+  static_assert(kWords == D / 64, "two threads to every fourth word of a key");
 };
 
-// Blocks a compute unit: by the registers of the sums (D / 32 x 16) and queries.
-constexpr int rows_occupancy(int D) { return D < 256 ? 2 : 1; }
+// M matrix instructions with S pieces of vector work spread between them.
+template <int M, int S, typename F, typename H>
+__device__ __forceinline__ void weave(F mfma, H piece) {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    mfma(i);
+#pragma unroll
+    for (int k = i * S / M; k < (i + 1) * S / M; ++k) piece(k);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
 
 template <int DT, int D, int GROUP>
 __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32_t id, uint8_t* lds) {
   using L = Rows<D, GROUP>;
-  constexpr int G = L::kG, KEYS = L::kKeys, kTiles = L::kTiles, kSteps = L::kSteps, kCh = L::kChannels;
-  constexpr int kGSteps = GROUP / 16, kPages = KEYS / 16;
+  constexpr int G = L::kG, KEYS = L::kKeys, T = L::kTiles, kSteps = L::kSteps, kCh = L::kChannels, kW = L::kW;
+  constexpr int kWords = L::kWords, kGSteps = GROUP / 16;
   constexpr int kAhead = 4;                        // operands read before they are used
-  constexpr int kAluMayCross = 0x6;                // sched_barrier: scalar and vector arithmetic
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
   const int r = lane & 31, h = lane >> 5;
   auto k_lds = [&](int i) { return lds + (i & 1) * L::kKBuffer; };
   auto v_lds = [&](int i) { return lds + 2 * L::kKBuffer + (i & 1) * L::kVBuffer; };
+  uint8_t* const ring = lds + 2 * (L::kKBuffer + L::kVBuffer);
+  const uint32_t ring_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ring));
 
   // row tiles of the same keys eight blocks apart: on one die, whose cache holds the codes
   const uint32_t eight = id % 8;
@@ -77,7 +98,7 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   const Sequence sq = item.sq;
   const int rows = sq.n * a.ratio;
   const Chunks ch = part_chunks<kPrefix>(a, item);
-  if (split >= ch.chunks) return;
+  if (split >= ch.chunks || sq.ctx == 0) return;
   const int key_lo = split * ch.chunk * kStep, key_hi = min(key_lo + ch.chunk * kStep, sq.ctx);
   const int rounds = (key_hi - key_lo + KEYS - 1) / KEYS;
 
@@ -85,73 +106,69 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   const uint32_t page_bytes = static_cast<uint32_t>(a.sh.heads) * static_cast<uint32_t>(record);
   const uint32_t pages = static_cast<uint32_t>(a.sh.pages);
   const uint8_t* head = a.cache + static_cast<int64_t>(kvh) * record;
-  typedef const __attribute__((address_space(4))) int32_t* table_t;
-  const table_t table = (table_t)(a.table + item.table_row * a.table_stride);
+  const int32_t* table = a.table + item.table_row * a.table_stride;
 
-  // What a thread expands of a round.  Keys: kWords words (every fourth of the
-  // key) from one piece of its row.  Values: of word v_word of two quads of
-  // tokens the even or the odd channels.
-  const int k_tile = D == 256 ? wave >> 1 : wave;             // of 16 keys
-  const int k_key = D == 256 ? (lane >> 2 & 7) + 8 * (wave & 1) : lane >> 2;
-  const int k_part = lane & 3, k_first = D == 256 ? 4 * (lane >> 5) : 0;
-  const int k_at = k_key * (D / 2) + k_part * (D / 8) + 4 * k_first, kp_at = a.sh.page * D + 4 * k_key;
-  const int k_to = ((k_tile / 2 * kSteps + 2 * k_first + (k_part >> 1)) * 2 + (k_part & 1)) * L::kHalf +
-                   (16 * (k_tile & 1) + k_key) * 16;
-  const int v_part = lane & 1, v_half = lane >> 1 & 1;
+  // What a thread expands of a round.  Keys: kWords of the words k_part + 4 i.
+  // Values: of word v_word of two quads of tokens kWords of the even or the odd channels.
+  const int k_part = lane & 3, k_side = lane >> 3 & 1;
+  const int k_key = (lane >> 2 & 1) + (lane >> 4) * 2 + 8 * wave;
+  const int k_from = k_key * (D / 2) + k_part * (D / 8) + k_side * (D / 16);
+  constexpr int kPars = kWords * 32 > GROUP ? kWords * 32 / GROUP : 1;        // groups of a thread's words
+  const int k_group = G > 1 ? k_side * kPars : 0;
+  const int kp_from = KEYS / 16 * L::kCodes + (k_key >> 4) * L::kParams + k_group * 64 + (k_key & 15) * 4;
+  const int k_to = (((k_key >> 5) * kSteps + 2 * k_side * kWords + (k_part >> 1)) * 2 + (k_part & 1)) * L::kHalf + (k_key & 31) * 16;
+  const int v_part = lane & 1, v_half = lane >> 1 & 1, v_m = wave & 1, v_tile = D == 256 ? 0 : wave >> 1 & 1;
   const int v_word = D == 64 ? lane >> 2 & 7 : D == 128 ? lane >> 2 : (lane >> 2) + 16 * (wave >> 1);
-  const int v_first = D == 64 ? 2 * (lane >> 5) : 0;          // of its nibbles
-  const int v_m = wave & 1, v_tile = D == 256 ? 0 : wave >> 1;
-  const int v_group = v_word / (GROUP / 8);
-  const int v_at = a.sh.page * (D / 2) + v_half * (2 * D) + 16 * v_word;
-  const int vp_at = a.sh.page * (D + 4 * G) + v_group * a.sh.page * 4 + 16 * v_half;
-  // (rows 8 .. 15 and 24 .. 31 of an operand lie four rows apart from their order: see value_row)
+  const int v_first = D == 64 ? (lane >> 5) + 2 * (wave >> 2) : D == 128 ? 2 * (wave >> 2) : 0;
+  const int v_from = L::kRaw + (2 * v_tile + v_m) * L::kCodes + v_half * (2 * D) + 16 * v_word;
+  const int vp_from = L::kRaw + KEYS / 16 * L::kCodes + (2 * v_tile + v_m) * L::kParams + v_word / (GROUP / 8) * 64 + 16 * v_half;
+  // (rows 8 .. 15 and 24 .. 31 of an operand change places by fours: the banks of a word and the next differ)
   auto value_row = [](int row) { return row ^ ((row >> 3 & 1) << 2); };
   const int v_to = (((v_tile * kCh + v_word / 4) * 2 + v_m) * 2 + v_half) * L::kHalf;
 
-  // A 16-key tile past the block's keys, or whose page is not of this cache, is
-  // read through an empty resource: zeros.
-  auto page_at = [&](int key) {
-    const int page = table[max(min(key, sq.ctx - 1), 0) >> a.sh.shift];
-    return key < key_hi ? page : -1;
+  // The pages of 16-key tiles, one a lane, of 64 at a time, the next 64 on their
+  // way to LDS: in order with the codes, so that nothing waits for them alone (and
+  // every wait for LDS would wait for scalar loads).  A tile past the block's keys,
+  // or whose page is not of this cache, is read through an empty resource: zeros.
+  constexpr int kTiles16 = KEYS / 16, kBatch = kWave / kTiles16;              // rounds of a batch
+  uint8_t* const my_pages = lds + L::kPagesAt + wave * kWave * 4;
+  const uint32_t pages_to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(my_pages));
+  const __amdgpu_buffer_rsrc_t table_rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<int32_t*>(table), 0, ((key_hi - 1) >> a.sh.shift) * 4 + 4, kBufferWord3);
+  auto first_key = [&](int batch) { return key_lo + (batch * kWave + lane) * 16; };
+  auto checked = [&](int page, int batch) { return first_key(batch) < key_hi && static_cast<uint32_t>(page) < pages ? page : -1; };
+  auto pages_of = [&](int batch) {
+    return checked(__builtin_amdgcn_raw_buffer_load_b32(table_rs, (first_key(batch) >> a.sh.shift) * 4, 0, 0), batch);
+  };
+  auto fetch_pages = [&](int batch) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(table_rs, (lds_ptr_t)(uintptr_t)pages_to, 4, (first_key(batch) >> a.sh.shift) * 4, 0,
+                                             0, 0);
   };
   auto tile_of = [&](int page) {
-    const bool here = static_cast<uint32_t>(page) < pages;
     return __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(head + static_cast<uint64_t>(static_cast<uint32_t>(here ? page : 0)) * page_bytes), 0,
-        here ? record : 0, kBufferWord3);
+        const_cast<uint8_t*>(head + static_cast<uint64_t>(static_cast<uint32_t>(max(page, 0))) * page_bytes), 0,
+        page < 0 ? 0 : record, kBufferWord3);
   };
-  uint32_t k_raw[L::kWords], k_par[G];
-  u32x4 v_raw[2], v_par[2];
-  auto fetch = [&](int round, int k_page, int v_page) {
-    const int key = key_lo + round * KEYS;
-    {
-      const __amdgpu_buffer_rsrc_t rs = tile_of(k_page);
-      const int place = (key + 16 * k_tile) & (a.sh.page - 1);
-      if constexpr (L::kWords == 2) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, k_at, place * (D / 2), 0));
-        k_raw[0] = v.x;
-        k_raw[1] = v.y;
-      } else {
-        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, k_at, place * (D / 2), 0));
-#pragma unroll
-        for (int w = 0; w < 4; ++w) k_raw[w] = v[w];
-      }
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        k_par[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, kp_at + i * a.sh.page * 4, place * 4, 0);
-    }
-    {
-      const __amdgpu_buffer_rsrc_t rs = tile_of(v_page);
-      const int place = (key + 32 * v_tile + 16 * v_m) & (a.sh.page - 1);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        v_raw[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, v_at + i * 4 * D, place * (D / 2), 0));
-        v_par[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, vp_at + 32 * i, place * 4, 0));
-      }
-    }
+  // A wavefront loads the keys or the values of one 16-key tile of a round.
+  const int l_tile = wave % kTiles16;
+  const bool l_values = wave >= kTiles16;
+  const int l_codes = (l_values ? a.sh.page * (D / 2) : 0) + 16 * lane;
+  const int l_params = a.sh.page * (D + (l_values ? 4 * G : 0)) + (lane >> 2) * a.sh.page * 4 + 16 * (lane & 3);
+  const uint32_t l_to = ring_at + (l_values ? L::kRaw : 0);
+  auto fetch = [&](int round, int slot, int page) {
+    const __amdgpu_buffer_rsrc_t rs = tile_of(page);
+    const int place = (key_lo + round * KEYS + 16 * l_tile) & (a.sh.page - 1);
+    const uint32_t to = l_to + slot * L::kSlot;
+    if (D != 64 || lane < 32)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(to + l_tile * L::kCodes), 16, l_codes,
+                                               place * (D / 2), 0, 0);
+    if constexpr (D == 256)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(to + l_tile * L::kCodes + 1024), 16, l_codes + 1024,
+                                               place * (D / 2), 0, 0);
+    if (lane < 4 * G)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(to + kTiles16 * L::kCodes + l_tile * L::kParams), 16,
+                                               l_params, place * 4, 0, 0);
   };
-  auto k_page_of = [&](int round) { return page_at(key_lo + round * KEYS + 16 * k_tile); };
-  auto v_page_of = [&](int round) { return page_at(key_lo + round * KEYS + 32 * v_tile + 16 * v_m); };
 
   const uint32_t magic = vgpr_const(Codes64::magic), magic_v = vgpr_const(0x44004400u);
   auto plus = [](uint32_t x, uint32_t y) {
@@ -161,46 +178,68 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, x) * __builtin_bit_cast(f16x2_t, y));
   };
   float key_scale = 0.0f;
-  auto expand_keys = [&](uint8_t* buf) {
+  // Expansions in pieces, to be put between matrix instructions; the first reads what the others need.
+  constexpr int kPieces = kWords + 1;
+  uint32_t kw[kWords], kp[kPars];
+  auto expand_keys = [&](const uint8_t* raw, uint8_t* buf, int piece) {
+    if (piece == 0) {
+      if constexpr (kWords == 1) {
+        kw[0] = *reinterpret_cast<const uint32_t*>(raw + k_from);
+      } else if constexpr (kWords == 2) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(raw + k_from);
+        kw[0] = v.x;
+        kw[1] = v.y;
+      } else {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(raw + k_from);
 #pragma unroll
-    for (int w = 0; w < L::kWords; ++w) {
-      // word k_part + 4 (k_first + w), in the 32 channels k_first + w
-      uint32_t par = k_par[0];
+        for (int w = 0; w < 4; ++w) kw[w] = v[w];
+      }
 #pragma unroll
-      for (int i = 1; i < G; ++i) par = (k_first + w) / (GROUP / 32) == i ? k_par[i] : par;
-      const uint32_t z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
-      uint32_t p[4];
-      Codes64::unpack(k_raw[w], magic, p);
-      *reinterpret_cast<u32x4*>(buf + k_to + w * 4 * L::kHalf) = u32x4{plus(p[0], z), plus(p[1], z), plus(p[2], z), plus(p[3], z)};
+      for (int i = 0; i < kPars; ++i) kp[i] = *reinterpret_cast<const uint32_t*>(raw + kp_from + 64 * i);
+      return;
     }
-    if (k_part == 0 && k_first == 0) {
-#pragma unroll
-      for (int i = 0; i < G; ++i)
-        *reinterpret_cast<float*>(buf + L::kKOps + (i * KEYS + 16 * k_tile + k_key) * 4) = kv4_scale(k_par[i]) * key_scale;
-    }
+    const int w = piece - 1;
+    const uint32_t par = kp[w * kPars / kWords], z = 0xD400D400u + ((par >> 16) & 0xFu) * 0x00100010u;
+    uint32_t p[4];
+    Codes64::unpack(kw[w], magic, p);
+    *reinterpret_cast<u32x4*>(buf + k_to + w * 4 * L::kHalf) = u32x4{plus(p[0], z), plus(p[1], z), plus(p[2], z), plus(p[3], z)};
+    if (w * kPars % kWords == 0 && k_part == 0 && (G > 1 || k_side == 0))
+      *reinterpret_cast<float*>(buf + L::kKOps + ((k_group + w * kPars / kWords) * KEYS + k_key) * 4) = kv4_scale(par) * key_scale;
   };
-  auto expand_values = [&](uint8_t* buf) {
-    uint32_t z[4], s[4], w[4];
-    const uint32_t sel = v_part ? 0x07060302u : 0x05040100u;
+  uint32_t vz[4], vs[4], vw[4];
+  auto expand_values = [&](const uint8_t* raw, uint8_t* buf, int piece) {
+    if (piece == 0) {
+      const uint32_t sel = v_part ? 0x07060302u : 0x05040100u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t p0 = v_par[e >> 1][2 * (e & 1)], p1 = v_par[e >> 1][2 * (e & 1) + 1];
-      z[e] = (__builtin_amdgcn_perm(p1, p0, 0x0c060c02u) << 4 & 0x00F000F0u) | 0xC400C400u;      // -(4 + z / 16)
-      s[e] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
-      w[e] = __builtin_amdgcn_perm(v_raw[e >> 1][2 * (e & 1) + 1], v_raw[e >> 1][2 * (e & 1)], sel) >> (4 * v_first);
+      for (int q = 0; q < 2; ++q) {
+        const u32x4 codes = *reinterpret_cast<const u32x4*>(raw + v_from + 4 * D * q);
+        const u32x4 par = *reinterpret_cast<const u32x4*>(raw + vp_from + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          vz[2 * q + e] = (__builtin_amdgcn_perm(par[2 * e + 1], par[2 * e], 0x0c060c02u) << 4 & 0x00F000F0u) | 0xC400C400u;   // -(4 + z / 16)
+          vs[2 * q + e] = __builtin_amdgcn_perm(par[2 * e + 1], par[2 * e], 0x05040100u);
+          // channel v_first at bit 4 of either token's half
+          vw[2 * q + e] = __builtin_rotateright32(__builtin_amdgcn_perm(codes[2 * e + 1], codes[2 * e], sel), (4 * v_first + 28) & 31);
+        }
+      }
+      return;
     }
+    const int y = piece - 1;
+    u32x4 v;
 #pragma unroll
-    for (int y = 0; y < L::kNibbles; ++y) {
-      u32x4 v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[e] = times(plus(((y == 0 ? w[e] << 4 : w[e] >> (4 * y - 4)) & Codes64::mask) | magic_v, z[e]), s[e]);
-      const int row = 8 * (v_word & 3) + 2 * (v_first + y) + v_part;
-      *reinterpret_cast<u32x4*>(buf + v_to + value_row(row) * 16) = v;
-    }
+    for (int e = 0; e < 4; ++e) v[e] = times(plus((__builtin_rotateright32(vw[e], 4 * y) & Codes64::mask) | magic_v, vz[e]), vs[e]);
+    const int row = 8 * (v_word & 3) + 2 * (v_first + y) + v_part;
+    *reinterpret_cast<u32x4*>(buf + v_to + value_row(row) * 16) = v;
+  };
+  // Only LDS is shared, and the codes on their way are waited for in their turn.
+  auto meet = [&] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   };
 
-  const int strips = (rows + L::kStrip - 1) / L::kStrip, tiles = (strips + kWaves - 1) / kWaves;
+  const int strips = (rows + L::kStrip - 1) / L::kStrip, tiles = (strips + kW - 1) / kW;
   for (int tile = tile0; tile < tiles; tile += a.p_row_tiles) {
     // the strips are dealt evenly to the tiles
     const int strip = tile * strips / tiles + wave;
@@ -209,27 +248,36 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
     const bool live = active && row < rows;
     const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;
     const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * h;
-    fetch(0, k_page_of(0), v_page_of(0));
+    __syncthreads();                               // LDS is free: the rows before are done
+    int now_pages = pages_of(0);                   // of the batch that is fetched
+    uint64_t there = __ballot(now_pages >= 0), there_next = 0;
+#pragma unroll
+    for (int i = 0; i < L::kRing; ++i) fetch(i, i, __builtin_amdgcn_readlane(now_pages, i * kTiles16 + l_tile));
     u32x4 qv[kSteps];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) qv[j] = live ? ld16(qp + 16 * j) : u32x4{0u, 0u, 0u, 0u};
+    fetch_pages(1);
     float unscale = 1.0f;
-    __syncthreads();                               // LDS is free: the rows before are done
     if constexpr (DT == QMM_BF16) {
       float* stat = reinterpret_cast<float*>(lds);
       float most = wave_max(largest_bf16(qv, 0.0f));
       if (lane == 0) stat[wave] = most;
       __syncthreads();
-      most = fmaxf(fmaxf(stat[0], stat[1]), fmaxf(stat[2], stat[3]));
+      most = stat[0];
+#pragma unroll
+      for (int w = 1; w < kW; ++w) most = fmaxf(most, stat[w]);
       const QueryScale qs = query_scale(most);
       __syncthreads();
       unscale = qs.up;
       to_f16(qv, qs.down);
     }
     key_scale = a.scale_log2 * unscale;
-    expand_keys(k_lds(0));
-    expand_values(v_lds(0));
-    if (rounds > 1) fetch(1, k_page_of(1), v_page_of(1));
+    wait_vm<0>();                                  // the queries came last
+    meet();
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) expand_keys(ring, k_lds(0), i);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) expand_values(ring, v_lds(0), i);
 
     f32x16 o[kCh];
 #pragma unroll
@@ -238,59 +286,92 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
       for (int i = 0; i < 16; ++i) o[c][i] = 0.0f;
     // p = 2^(x - base): at most 2^15, 2^7 where the maximum was last moved
     float base = -INFINITY, from = 0.0f, limit = -INFINITY, l = 0.0f;
-    int k_page = k_page_of(2), v_page = v_page_of(2);
-    __syncthreads();
+    int slot = 0;
+    meet();
 
+    // Every round the next one's operands are made of the codes at hand, and the
+    // codes of the sixth round from here are fetched.  Each run of matrix
+    // instructions has vector work between: the scores the keys' expansion and the
+    // scales of the tile and group before, the first tile's values the second's
+    // exponentials, the last tile's the values' expansion.
     for (int round = 0; round < rounds; ++round) {
       const uint8_t* kb = k_lds(round);
       const uint8_t* vb = v_lds(round);
-      const int k_after = k_page_of(round + 3), v_after = v_page_of(round + 3);
-      if (active) {
-        // ---- scores less the base they are taken at
-        f32x16 x[kTiles], acc[kTiles];
-        {
-          constexpr int kOps = kSteps * kTiles;
-          u32x4 k[kAhead];
-          auto read = [&](int i) {
-            return *reinterpret_cast<const u32x4*>(kb + ((i % kTiles * kSteps + i / kTiles) * 2 + h) * L::kHalf + 16 * r);
-          };
+      uint8_t* const k_next = k_lds(round + 1);
+      uint8_t* const v_next = v_lds(round + 1);
+      const int ahead = round + L::kRing;
+      if (ahead % kBatch == 0) {
+        now_pages = checked(*reinterpret_cast<const int*>(my_pages + 4 * lane), ahead / kBatch);
+        there_next = __ballot(now_pages >= 0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xc07f);        // read before its place is written
+        fetch_pages(ahead / kBatch + 1);
+      }
+      if (round % kBatch == 0 && round > 0) there = there_next;
+      fetch(ahead, slot, __builtin_amdgcn_readlane(now_pages, ahead % kBatch * kTiles16 + l_tile));
+      slot = slot + 1 == L::kRing ? 0 : slot + 1;
+      const uint8_t* raw = ring + slot * L::kSlot;
+      if (!active) {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) k[i] = read(i);
-          __builtin_amdgcn_sched_barrier(kAluMayCross);
+        for (int i = 0; i < kPieces; ++i) expand_keys(raw, k_next, i);
 #pragma unroll
-          for (int i = 0; i < kOps; ++i) {
-            const int t = i % kTiles, j = i / kTiles, grp = j / kGSteps;
-            if (j % kGSteps == 0)
+        for (int i = 0; i < kPieces; ++i) expand_values(raw, v_next, i);
+      } else {
+        // ---- scores less the base they are taken at: products of a tile and
+        // group (a unit) while the one before is scaled
+        u32x4 k[kAhead];
+        auto read_k = [&](int i) { return *reinterpret_cast<const u32x4*>(kb + (i * 2 + h) * L::kHalf + 16 * r); };
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[t][e] = 0.0f;
-            acc[t] = mfma32(k[i % kAhead], qv[j], acc[t]);
-            if (i + kAhead < kOps) k[i % kAhead] = read(i + kAhead);
-            __builtin_amdgcn_sched_barrier(kAluMayCross);
-            if (j % kGSteps == kGSteps - 1)
+        for (int i = 0; i < kAhead; ++i) k[i] = read_k(i);
+        f32x16 acc[2], x[T];
+        auto score = [&](int i) {
+          const int j = i % kSteps, unit = i / kGSteps;
+          if (j % kGSteps == 0)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const f32x4 sc = *reinterpret_cast<const f32x4*>(kb + L::kKOps + (grp * KEYS + 32 * t + 8 * c + 4 * h) * 4);
+            for (int e = 0; e < 16; ++e) acc[unit % 2][e] = 0.0f;
+          acc[unit % 2] = mfma32(k[i % kAhead], qv[j], acc[unit % 2]);
+          if (i + kAhead < T * kSteps) k[i % kAhead] = read_k(i + kAhead);
+        };
+        auto scaled = [&](int unit, int c) {
+          const int t = unit / G, grp = unit % G;
+          const f32x4 sc = *reinterpret_cast<const f32x4*>(kb + L::kKOps + (grp * KEYS + 32 * t + 8 * c + 4 * h) * 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  x[t][4 * c + e] = fmaf(acc[t][4 * c + e], sc[e], grp == 0 ? -from : x[t][4 * c + e]);
-              }
-          }
+          for (int e = 0; e < 4; ++e)
+            x[t][4 * c + e] = fmaf(acc[unit % 2][4 * c + e], sc[e], grp == 0 ? -from : x[t][4 * c + e]);
+        };
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int kUnits = T * G, kMost = (kPieces + kUnits - 1) / kUnits;      // pieces of the expansion with a unit
+#pragma unroll
+        for (int unit = 0; unit < kUnits; ++unit) {
+          weave<kGSteps, 4 + kMost>([&](int i) { score(unit * kGSteps + i); }, [&](int i) {
+            if (i < 4) {
+              if (unit > 0) scaled(unit - 1, i);
+            } else if (unit * kMost + i - 4 < kPieces) {
+              expand_keys(raw, k_next, unit * kMost + i - 4);
+            }
+          });
         }
-        // ---- keys of no page
-        int holes = 0;
+        u32x4 v[kAhead];
+        auto read_v = [&](int i) {
+          const int c = i % kCh, m = i / kCh;                 // m: 16 keys
+          return *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
+        };
 #pragma unroll
-        for (int t = 0; t < kPages; ++t)
-          holes |= static_cast<uint32_t>(page_at(key_lo + round * KEYS + 16 * t)) < pages ? 0 : 1 << t;
+        for (int i = 0; i < kAhead; ++i) v[i] = read_v(i);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) scaled(kUnits - 1, c);
+        // ---- keys of no page
+        const int holes = static_cast<int>(~there >> (round % kBatch * kTiles16)) & ((1 << kTiles16) - 1);
         if (holes) {
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t)
+          for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[t][e] = holes >> (2 * t + e / 8) & 1 ? -INFINITY : x[t][e];
         }
         // ---- running maximum
         float top = x[0][0];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int t = 0; t < T; ++t)
 #pragma unroll
           for (int e = 0; e < 16; e += 2) top = max3(top, x[t][e], x[t][e + 1]);
         if (__any(top > limit)) {
@@ -299,7 +380,7 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
           const float fade = to == -INFINITY ? 1.0f : exp2_fast(base - to);
           const float now_from = to == -INFINITY ? 0.0f : to;
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) x[t] += from - now_from;
+          for (int t = 0; t < T; ++t) x[t] += from - now_from;
 #pragma unroll
           for (int c = 0; c < kCh; ++c) o[c] *= fade;
           l *= fade;
@@ -307,50 +388,30 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
           from = now_from;
           limit = to == -INFINITY ? -INFINITY : 15.0f;
         }
-        // ---- probabilities
-        u32x4 p[kTiles][2];
+        // ---- probabilities and sums
+        u32x4 p[T][2];
+        auto exponentials = [&](int t, int i) {
+          const float p0 = exp2_fast(x[t][2 * i]), p1 = exp2_fast(x[t][2 * i + 1]);
+          l += p0 + p1;
+          p[t][i / 4][i % 4] = pack_pair<QMM_F16>(p0, p1);
+        };
+        auto value = [&](int i) {
+          const int c = i % kCh, m = i / kCh;
+          o[c] = mfma32(v[i % kAhead], p[m / 2][m % 2], o[c]);
+          if (i + kAhead < 2 * T * kCh) v[i % kAhead] = read_v(i + kAhead);
+        };
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float p0 = exp2_fast(x[t][e]), p1 = exp2_fast(x[t][e + 1]);
-            l += p0 + p1;
-            p[t][e / 8][e / 2 % 4] = pack_pair<QMM_F16>(p0, p1);
-          }
-        // ---- sums
-        {
-          constexpr int kOps = kTiles * 2 * kCh;
-          u32x4 v[kAhead];
-          auto read = [&](int i) {
-            const int c = i % kCh, m = i / kCh;               // m: 16 keys
-            return *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
-          };
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) v[i] = read(i);
-          __builtin_amdgcn_sched_barrier(kAluMayCross);
-#pragma unroll
-          for (int i = 0; i < kOps; ++i) {
-            const int c = i % kCh, m = i / kCh;
-            o[c] = mfma32(v[i % kAhead], p[m / 2][m % 2], o[c]);
-            if (i + kAhead < kOps) v[i % kAhead] = read(i + kAhead);
-            __builtin_amdgcn_sched_barrier(kAluMayCross);
-          }
-        }
+        for (int i = 0; i < 8; ++i) exponentials(0, i);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (T == 2) weave<2 * kCh, 8>(value, [&](int i) { exponentials(1, i); });
+        weave<2 * kCh, kPieces>([&](int i) { value(2 * (T - 1) * kCh + i); }, [&](int i) { expand_values(raw, v_next, i); });
       }
-      if (round + 1 < rounds) {
-        expand_keys(k_lds(round + 1));
-        expand_values(v_lds(round + 1));
-        if (round + 2 < rounds) fetch(round + 2, k_page, v_page);
-      }
-      k_page = k_after;
-      v_page = v_after;
-      // only LDS is shared: the codes on their way need not have come
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0xc07f);
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+      // the codes that the next round expands: of this wavefront's loads those of kRing - 2 rounds may be on their way
+      wait_vm<L::kLoads * (L::kRing - 2)>();
+      meet();
     }
 
+    wait_vm<0>();                                  // nothing is on its way to LDS any more
     // ---- results: row r, channels 8 c + 4 h of every 32
     l += __shfl_xor(l, 32, kWave);
     if (live) {
@@ -368,7 +429,7 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
 }
 
 template <int DT, int D, int GROUP>
-__global__ __launch_bounds__(256, rows_occupancy(D)) void attention_rows_kernel(SharedArgs a) {
+__global__ __launch_bounds__((Rows<D, GROUP>::kThreads), (Rows<D, GROUP>::kW / 4)) void attention_rows_kernel(SharedArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[Rows<D, GROUP>::kLds];
   attention_rows_block<DT, D, GROUP>(a, blockIdx.x, lds);
 }

@@ -19,13 +19,13 @@ AttnPlan part_plan(bool prefix, int64_t items, int64_t rows, int64_t kv_heads, i
                    int64_t* round) {
   AttnPlan p{};
   const int d = static_cast<int>(D);
-  const int64_t fill = 2 * device_cus();
   p.ws = rows <= 96;
+  const int64_t fill = (p.ws || !prefix ? 2 : 1) * device_cus();
   const bool eights = rows <= 8;
   const bool sixteens = eights || rows <= 16 || items * kv_heads * ceil_div(rows, 16) < fill;
   p.pk = eights && attention_pairs(d, group) ? 2 : 1;
   p.nt = !p.ws ? attention_chunk_tiles(d, group) : sixteens ? 1 : attention_tiles(d, group);
-  p.rows = p.ws ? 16 / p.pk * p.nt : (prefix ? 32 : 16 * p.nt) * kWaves;
+  p.rows = p.ws ? 16 / p.pk * p.nt : prefix ? (D == 256 ? 128 : 256) : 16 * p.nt * kWaves;
   // (blocks loop over row tiles past these: a launch holds 2^24 blocks of 256 threads)
   p.row_tiles = std::min(ceil_div(rows, p.rows), std::max<int64_t>(1, (int64_t{1} << 22) / (items * kv_heads)));
   const int64_t steps = std::max<int64_t>(1, ceil_div(keys, kStep)), blocks = items * kv_heads * p.row_tiles;

@@ -26,7 +26,7 @@ void launch_part(const SharedArgs& a, const AttnPlan& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.blocks));
   constexpr int kTiles = attention_tiles(D, GROUP);
   if (!p.ws) {
-    if constexpr (PART == kPrefix) attention_rows_kernel<DT, D, GROUP><<<grid, 256, 0, s>>>(a);
+    if constexpr (PART == kPrefix) attention_rows_kernel<DT, D, GROUP><<<grid, Rows<D, GROUP>::kThreads, 0, s>>>(a);
     else attention_own_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP)><<<grid, 256, 0, s>>>(a);
   } else if (p.pk == 2) {
     if constexpr (attention_pairs(D, GROUP)) attention_part_kernel<DT, D, GROUP, 2, 1, PART><<<grid, 256, 0, s>>>(a);
