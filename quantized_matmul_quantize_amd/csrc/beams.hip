@@ -8,18 +8,19 @@
 namespace qmm {
 namespace {
 
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_anywhere __attribute__((aligned(2)));
 
 constexpr int kMostBeams = 64, kMostK = 64;
 constexpr int kPerThread = 32;                     // logits of a thread
 constexpr int kChunk = 256 * kPerThread;           // of a block
 
-// What a block found in its logits of a row: their maximum, the sum of
-// exp(x - maximum), and how many of its k candidates there are.
+// What a block found in its logits of a row: their maximum and the sum of
+// exp(x - maximum).
 struct Partial {
-  float most;
-  int count;
   double sum;
+  float most;
+  float unused;
 };
 struct Candidate {
   float x;
@@ -42,15 +43,18 @@ __device__ __forceinline__ double unordered(uint64_t k) {
   return __builtin_bit_cast(double, k >> 63 ? k ^ 0x8000000000000000ull : ~k);
 }
 
-// The k-th largest key of the wavefront's lanes (0: fewer than k are not 0).
+// The k-th and the few-th largest key of the wavefront's lanes (0: not so many
+// are not 0), few <= k.  Two searches at once: each waits for its own counts.
 template <typename K>
-__device__ __forceinline__ K kth_largest(K key, int k) {
-  K at = 0;
-  for (int bit = static_cast<int>(sizeof(K)) * 8 - 1; bit >= 0; --bit) {
-    const K next = at | K{1} << bit;
-    if (__popcll(__ballot(key >= next)) >= k) at = next;
+__device__ __forceinline__ void kth_largest(K key, int bits, int k, int few, K* at_k, K* at_few) {
+  K a = 0, b = 0;
+  for (int bit = bits - 1; bit >= 0; --bit) {
+    const K next_a = a | K{1} << bit, next_b = b | K{1} << bit;
+    if (__popcll(__ballot(key >= next_a)) >= k) a = next_a;
+    if (__popcll(__ballot(key >= next_b)) >= few) b = next_b;
   }
-  return at;
+  *at_k = a;
+  *at_few = b;
 }
 
 // A bound below which no value is among the k best: the k-th best of the lanes'
@@ -61,23 +65,53 @@ struct Bound {
   K key;             // 0: no bound
   uint32_t index;    // of values with that key, up to this index
 };
-// `first(key)` gives the lowest index at which the lane holds its best value.
-template <typename K, typename First>
-__device__ __forceinline__ Bound<K> bound_of(K best, int k, First first) {
-  Bound<K> b{kth_largest(best, k), 0xFFFFFFFFu};
-  if (b.key == 0) return b;
-  const int more = k - __popcll(__ballot(best > b.key));
-  if (__popcll(__ballot(best == b.key)) > more)
-    b.index = ~kth_largest<uint32_t>(best == b.key ? ~first() : 0u, more);
-  return b;
-}
-// What a block of four wavefronts lets through: the one whose bound is taken has
-// k such lanes, the others, whose own bounds are less tight, at most k - 1.
-__host__ __device__ constexpr int room_of(int k) { return (4 * k - 3) * kPerThread + 7; }
 template <typename K>
 __device__ __forceinline__ bool tighter(const Bound<K>& a, const Bound<K>& b) {
   return a.key > b.key || (a.key == b.key && a.index < b.index);
 }
+// The index that belongs to the k-th largest key; `first()` gives the lowest at
+// which the lane holds its best value.  Not `exact`: any, so that all equal
+// values pass, however many.
+template <typename K, typename First>
+__device__ __forceinline__ Bound<K> bound_at(K best, K key, int k, bool exact, First first) {
+  Bound<K> b{key, 0xFFFFFFFFu};
+  if (key == 0 || !exact) return b;
+  const int more = k - __popcll(__ballot(best > key));
+  if (__popcll(__ballot(best == key)) > more) {
+    uint32_t at, unused;
+    kth_largest<uint32_t>(best == key ? ~first() : 0u, 32, more, more, &at, &unused);
+    b.index = ~at;
+  }
+  return b;
+}
+// A wavefront's bounds by its k best lanes and by its share of k best of the
+// block's; what the block then goes by: the tightest of the first, which lets
+// through no more than k lanes a wavefront, or the loosest of the second, which
+// lets through k lanes of all together and is the tighter one but for few or
+// sorted values.
+template <typename K>
+struct Bounds {
+  Bound<K> k, share;
+};
+template <typename K, typename First>
+__device__ __forceinline__ Bounds<K> bounds_of(K best, int bits, int k, int waves, bool exact, First first) {
+  const int share = (k + waves - 1) / waves;
+  K at_k, at_share;
+  kth_largest(best, bits, k, share, &at_k, &at_share);
+  return {bound_at(best, at_k, k, exact, first), bound_at(best, at_share, share, exact, first)};
+}
+template <typename K, int WAVES>
+__device__ __forceinline__ Bound<K> block_bound(const Bounds<K> (&all)[WAVES]) {
+  Bound<K> most = all[0].k, least = all[0].share;
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) {
+    if (tighter(all[w].k, most)) most = all[w].k;
+    if (tighter(least, all[w].share)) least = all[w].share;
+  }
+  return tighter(least, most) ? least : most;
+}
+// What a wavefront lets through.
+__host__ __device__ constexpr int room_of(int k) { return k * kPerThread + 7; }
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -100,19 +134,59 @@ struct Select {
   int64_t* out_parents;
 };
 
+// The compiler's maximum quiets each operand first.  (A NaN makes it wrong, and
+// is found in the sum.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+
+// The largest of 16-bit floating-point numbers by their bits: as whole numbers
+// with a sign the positive ones stand in their order, the negative ones in the
+// opposite one.
+template <int N>
+__device__ __forceinline__ uint32_t largest_bits(const u32x4 (&v)[N]) {
+  i16x2 most = __builtin_bit_cast(i16x2, static_cast<uint32_t>(v[0][0])), least = most;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t u = v[j][w];
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(i16x2, u));
+      least = __builtin_elementwise_min(least, __builtin_bit_cast(i16x2, u));
+    }
+  const int m = max(most[0], most[1]), l = min(least[0], least[1]);
+  return static_cast<uint32_t>(m >= 0 ? m : l) & 0xFFFFu;
+}
+
 template <int DT>
 struct Logits;               // 16-byte pieces of a row
 template <>
 struct Logits<QMM_F32> {
-  static constexpr int kOf = 4;
+  static constexpr int kOf = 4, kBits = 32;                  // numbers of a piece, bits of one
   static constexpr uint32_t kNone = 0xFF800000u;             // -inf
+  // the type's numbers in their order as unsigned ones (never 0 above -inf)
+  static __device__ __forceinline__ uint32_t key(float x) { return ordered(x); }
+  template <int N>
+  static __device__ __forceinline__ float largest(const u32x4 (&v)[N]) {
+    float most = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < N; ++j) most = max3(max3(most, get(v[j], 0), get(v[j], 1)), get(v[j], 2), get(v[j], 3));
+    return most;
+  }
+  static __device__ __forceinline__ float value(uint32_t k) { return unordered(k); }
   static __device__ __forceinline__ float get(u32x4 v, int e) { return __uint_as_float(v[e]); }
   static __device__ __forceinline__ void set_none(u32x4& v, int e) { v[e] = kNone; }
 };
 template <>
 struct Logits<QMM_BF16> {
-  static constexpr int kOf = 8;
+  static constexpr int kOf = 8, kBits = 16;
   static constexpr uint32_t kNone = 0xFF80FF80u;
+  static __device__ __forceinline__ uint32_t key(float x) { return ordered(x) >> 16; }
+  template <int N>
+  static __device__ __forceinline__ float largest(const u32x4 (&v)[N]) { return bf16lo_to_f32(largest_bits(v)); }
+  static __device__ __forceinline__ float value(uint32_t k) { return bf16hi_to_f32(__float_as_uint(unordered(k << 16 | (k & 0x8000u ? 0u : 0xFFFFu)))); }
   static __device__ __forceinline__ float get(u32x4 v, int e) {
     return e & 1 ? bf16hi_to_f32(v[e / 2]) : bf16lo_to_f32(v[e / 2]);
   }
@@ -122,8 +196,15 @@ struct Logits<QMM_BF16> {
 };
 template <>
 struct Logits<QMM_F16> {
-  static constexpr int kOf = 8;
+  static constexpr int kOf = 8, kBits = 16;
   static constexpr uint32_t kNone = 0xFC00FC00u;
+  template <int N>
+  static __device__ __forceinline__ float largest(const u32x4 (&v)[N]) { return f16lo_to_f32(largest_bits(v)); }
+  static __device__ __forceinline__ uint32_t key(float x) {
+    const uint32_t u = f32_to_f16_bits(x + 0.0f);
+    return u & 0x8000u ? ~u & 0xFFFFu : u | 0x8000u;
+  }
+  static __device__ __forceinline__ float value(uint32_t k) { return f16lo_to_f32(k & 0x8000u ? k ^ 0x8000u : ~k); }
   static __device__ __forceinline__ float get(u32x4 v, int e) {
     return e & 1 ? f16hi_to_f32(v[e / 2]) : f16lo_to_f32(v[e / 2]);
   }
@@ -141,15 +222,15 @@ struct Logits<QMM_F16> {
 // others in fp32 by the hardware's exponential: two beams' candidates that are
 // nearly as good are told apart by their rows' sums.
 template <int DT>
-__global__ __launch_bounds__(256) void beam_rows_kernel(Select a) {
+__global__ __launch_bounds__(256, 8) void beam_rows_kernel(Select a) {
   using L = Logits<DT>;
   constexpr int kOf = L::kOf, kPieces = kPerThread / kOf;
   constexpr float kLog2e = 1.44269504088896341f;
-  extern __shared__ __attribute__((aligned(16))) Candidate pool[];     // room_of(k)
+  extern __shared__ __attribute__((aligned(16))) Candidate pool[];     // [4][room_of(k)]
   __shared__ float s_most[4];
   __shared__ double s_sum[4];
-  __shared__ Bound<uint32_t> s_bound[4];
-  __shared__ int s_count, s_nan[4];
+  __shared__ Bounds<uint32_t> s_bound[4];
+  __shared__ int s_count[4], s_again[4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int chunk = blockIdx.x;
@@ -170,9 +251,8 @@ __global__ __launch_bounds__(256) void beam_rows_kernel(Select a) {
     raw[j] = u32x4{L::kNone, L::kNone, L::kNone, L::kNone};
     if (p < pieces) raw[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_anywhere*>(base + static_cast<int64_t>(p) * 16));
   }
-  auto index_of = [&](int j, int e) {
-    return static_cast<uint32_t>(((chunk * kPieces + j) * 256 + tid) * kOf + e);
-  };
+  uint32_t first_index = static_cast<uint32_t>(chunk * kChunk + tid * kOf);
+  auto index_of = [&](int j, int e) { return first_index + static_cast<uint32_t>(j * 256 * kOf + e); };
   float odd = -INFINITY;
   uint32_t odd_index = 0;
   if (chunk == 0 && tid < behind) {
@@ -182,22 +262,21 @@ __global__ __launch_bounds__(256) void beam_rows_kernel(Select a) {
     else odd = f16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[odd_index]);
   }
 
-  float most, sum;
-  double large = 0.0;                 // the sum of those that reach LDS
+  float most, sum, at_base;
+  int mine_n;                         // candidates of the wavefront
   for (int turn = 0;; ++turn) {
+    asm volatile("" : "+v"(first_index));                  // indexes are worked out where they are used
     // ---- the lane's best, the block's maximum, the bound
-    float best = odd;
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j)
-#pragma unroll
-      for (int e = 0; e < kOf; ++e) best = fmaxf(best, L::get(raw[j], e));
-    const uint32_t key = best > -INFINITY ? ordered(best) : 0u;
-    const Bound<uint32_t> mine = bound_of(key, a.k, [&] {
+    const float best = fmaxf(L::largest(raw), odd);
+    const uint32_t key = best > -INFINITY ? L::key(best) : 0u;
+    const Bounds<uint32_t> mine = bounds_of(key, L::kBits, a.k, 4, turn > 0, [&] {
       uint32_t at = odd == best ? odd_index : 0xFFFFFFFFu;
 #pragma unroll
-      for (int j = 0; j < kPieces; ++j)
+      for (int j = 0; j < kPieces; ++j) {
+        asm volatile("" : "+v"(raw[j]));                   // unpacked anew: 64 registers
 #pragma unroll
         for (int e = 0; e < kOf; ++e) at = L::get(raw[j], e) == best ? min(at, index_of(j, e)) : at;
+      }
       return at;
     });
     const float wave_most = wave_max(best);
@@ -205,100 +284,150 @@ __global__ __launch_bounds__(256) void beam_rows_kernel(Select a) {
       s_most[wave] = wave_most;
       s_bound[wave] = mine;
     }
-    if (tid == 0) s_count = 0;
     __syncthreads();
-    Bound<uint32_t> bound = s_bound[0];
-    most = s_most[0];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      if (tighter(s_bound[w], bound)) bound = s_bound[w];
-      most = fmaxf(most, s_most[w]);
-    }
-    // ---- sums below the bound; what passes it goes to LDS
-    const float least = bound.key ? unordered(bound.key) : -INFINITY;
+    const Bound<uint32_t> bound = block_bound(s_bound);
+    most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+    // ---- sums below the bound; what passes it goes to the wavefront's part of LDS
+    // (without a bound all but -inf does)
+    const float least = bound.key ? L::value(bound.key) : -3.402823466e38f;
+    const bool ties = bound.index != 0xFFFFFFFFu;          // not all that equal the bound
     const float from = most == -INFINITY ? 0.0f : most;
+    at_base = from * kLog2e;
+    const bool far = fabsf(from) > 0x1p24f;                // where the rounding of at_base is no small number
     sum = 0.0f;
-    auto term = [&](float x) { return __builtin_amdgcn_exp2f((x - from) * kLog2e); };
+    mine_n = 0;
+    auto term = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -at_base)); };
+    auto take = [&](float x, uint32_t at, uint64_t who) {  // lanes whose x does
+      if (ties) {
+        const bool less = x == least && at > bound.index && (who >> lane & 1);
+        sum += less ? term(x) : 0.0f;
+        who &= ~__ballot(less);
+      }
+      const int n = mine_n + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who >> 32),
+                                                                        __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who), 0u)));
+      if ((who >> lane & 1) && n < room) pool[wave * room + n] = {x, at};
+      mine_n += __popcll(who);
+    };
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j)
+    for (int j = 0; j < kPieces; ++j) {
+      asm volatile("" : "+v"(raw[j]));
+      uint64_t any = 0;
+      float x[kOf];
 #pragma unroll
       for (int e = 0; e < kOf; ++e) {
-        const float x = L::get(raw[j], e);
-        sum += x >= least ? 0.0f : term(x);
+        x[e] = L::get(raw[j], e);
+        const bool below = !(x[e] >= least);               // or NaN
+        any |= ~__ballot(below);
+        sum += below ? term(x[e]) : 0.0f;
       }
-    sum += odd >= least ? 0.0f : term(odd);
-    auto take = [&](float x, uint32_t at) {
-      if (!(x >= least) || x == -INFINITY) return;
-      if (x > least || at <= bound.index) {
-        const int n = atomicAdd(&s_count, 1);
-        if (n < room) pool[n] = {x, at};
-      } else {
-        sum += term(x);
+      if (any) {
+#pragma unroll
+        for (int e = 0; e < kOf; ++e)
+          if (const uint64_t who = ~__ballot(!(x[e] >= least))) take(x[e], index_of(j, e), who);
       }
-    };
-    if (best >= least) {
-      take(odd, odd_index);
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j)
-#pragma unroll
-        for (int e = 0; e < kOf; ++e) take(L::get(raw[j], e), index_of(j, e));
     }
+    sum += odd >= least ? 0.0f : term(odd);
+    if (far) {
+      // once more, the distance to the maximum first
+      sum = odd >= least && !(odd == least && odd_index > bound.index) ? 0.0f : __builtin_amdgcn_exp2f((odd - from) * kLog2e);
+      for (int j = 0; j < kPieces; ++j)
+        for (int e = 0; e < kOf; ++e) {
+          const uint32_t at = index_of(j, e);
+          if (at >= static_cast<uint32_t>(pieces * kOf)) continue;
+          float x;
+          if constexpr (DT == QMM_F32) x = reinterpret_cast<const float*>(base)[at];
+          else if constexpr (DT == QMM_BF16) x = bf16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[at]);
+          else x = f16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[at]);
+          if (turn == 1 && x != x) x = -INFINITY;
+          if (!(x >= least) || (x == least && at > bound.index)) sum += __builtin_amdgcn_exp2f((x - from) * kLog2e);
+        }
+    }
+    if (const uint64_t who = __ballot(odd >= least)) take(odd, odd_index, who);
+    if (lane == 0) s_count[wave] = min(mine_n, room);
     if (turn == 1) {
       __syncthreads();
       break;
     }
-    // a NaN (which the sum has taken) counts as -inf: once more without them
+    // Once more where a NaN (which the sum has taken, and which counts as -inf) was
+    // met, or so many equal values that they need their indexes: 16-bit lane maxima
+    // are often equal, and those that pass besides are few (the indexes of every
+    // bound looked for at once: 400 of 750 vector instructions).
     const bool nan = __any(sum != sum);
-    if (lane == 0) s_nan[wave] = nan;
+    if (lane == 0) s_again[wave] = nan || mine_n > room;
     __syncthreads();
-    if (!(s_nan[0] | s_nan[1] | s_nan[2] | s_nan[3])) break;
+    if (!(s_again[0] | s_again[1] | s_again[2] | s_again[3])) break;
     if (odd != odd) odd = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j)
+    for (int j = 0; j < kPieces; ++j) {
+      asm volatile("" : "+v"(raw[j]));
 #pragma unroll
       for (int e = 0; e < kOf; ++e) {
         const float x = L::get(raw[j], e);
         if (x != x) L::set_none(raw[j], e);
       }
-    __syncthreads();                  // the count and the flags may be written again
+    }
+    __syncthreads();                  // counts and flags may be written again
   }
 
-  const int n = min(s_count, room);
+  // each candidate counts those before it
+  const int n1 = s_count[0], n2 = n1 + s_count[1], n3 = n2 + s_count[2], n = n3 + s_count[3];
+  auto candidate = [&](int i) {
+    return pool[i < n1 ? i : i < n2 ? room + i - n1 : i < n3 ? 2 * room + i - n2 : 3 * room + i - n3];
+  };
   const int64_t at = row * a.chunks + chunk;
+  Candidate* list = a.list + at * a.k;
+  double large = 0.0;                 // the sum of those that reached LDS
   for (int i = tid; i < n; i += 256) {
-    const Candidate c = pool[i];
+    const Candidate c = candidate(i);
     const uint32_t key = ordered(c.x);
     int rank = 0;
-    for (int j = 0; j < n; ++j) {
-      const Candidate o = pool[j];
-      const uint32_t ko = ordered(o.x);
-      rank += ko > key || (ko == key && o.token < c.token);
-    }
-    if (rank < a.k) a.list[at * a.k + rank] = c;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      for (int j = 0; j < s_count[w]; ++j) {
+        const Candidate o = pool[w * room + j];
+        const uint32_t ko = ordered(o.x);
+        rank += ko > key || (ko == key && o.token < c.token);
+      }
+    if (rank < a.k) list[rank] = c;
     large += exp(static_cast<double>(c.x) - static_cast<double>(most));
   }
-  large += static_cast<double>(wave_sum(sum)) * (lane == 0);
-  large = wave_sum(large);
-  if (lane == 0) s_sum[wave] = large;
+  for (int i = n + tid; i < a.k; i += 256) list[i] = {-INFINITY, 0u};
+  const double small = wave_sum(sum);
+  if (wave == 0 || n > kWave) large = wave_sum(large);       // (64 or fewer are all the first's)
+  // the fp32 terms' own base back to the maximum: what its rounding left
+  const double back = fabsf(most) > 0x1p24f ? 1.0 : exp2(static_cast<double>(at_base) - static_cast<double>(most) * static_cast<double>(kLog2e));
+  if (lane == 0) s_sum[wave] = fma(small, back, large);
   __syncthreads();
-  if (tid == 0) a.partial[at] = {most, min(n, a.k), s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]};
+  if (tid == 0) a.partial[at] = {s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3], most, 0.0f};
 }
 
 // A block joins the rows of a sequence: each beam's log sum, then the k best of
 // the blocks' candidates, 2048 at a time, by the same bound.  Values are fp64.
-constexpr int kJoinPer = 8, kJoinRoom = 4 * kMostK * kJoinPer + kMostK;     // (as room_of, and the ones kept)
+constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinPer = 4;
+constexpr int kJoinRoom = kJoinWaves * kMostK * kJoinPer + kMostK;     // (as room_of, and the ones kept)
 
-__global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
+__global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
   __shared__ double s_offset[kMostBeams];
   __shared__ int s_alive[kMostBeams];
-  __shared__ Bound<uint64_t> s_bound[4];
+  __shared__ Bounds<uint64_t> s_bound[kJoinWaves];
   __shared__ int s_count;
   __shared__ double value[kJoinRoom], kept_value[kMostK];
   __shared__ uint32_t place[kJoinRoom], kept_place[kMostK];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.beams;
-  for (int b = wave; b < a.beams; b += 4) {
+  const int total = a.beams * a.chunks * a.k, row_of = a.chunks * a.k;
+  // the first candidates are on their way while the sums are joined
+  Candidate c[kJoinPer];
+  auto fetch = [&](int first) {
+#pragma unroll
+    for (int i = 0; i < kJoinPer; ++i) {
+      const int e = first + i * kJoinThreads + tid;
+      c[i] = e < total ? a.list[row0 * row_of + e] : Candidate{-INFINITY, 0u};
+    }
+  };
+  fetch(0);
+  for (int b = wave; b < a.beams; b += kJoinWaves) {
     const float score = a.scores[row0 + b];
     const bool ends = a.finished && a.finished[row0 + b];
     double offset = 0.0;
@@ -306,11 +435,11 @@ __global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
     if (!ends) {
       const Partial* p = a.partial + (row0 + b) * a.chunks;
       float most = -INFINITY;
-      for (int c = lane; c < a.chunks; c += kWave) most = fmaxf(most, p[c].most);
+      for (int i = lane; i < a.chunks; i += kWave) most = fmaxf(most, p[i].most);
       most = wave_max(most);
       double sum = 0.0;
-      for (int c = lane; c < a.chunks; c += kWave)
-        if (p[c].most > -INFINITY) sum += p[c].sum * exp(static_cast<double>(p[c].most) - static_cast<double>(most));
+      for (int i = lane; i < a.chunks; i += kWave)
+        if (p[i].most > -INFINITY) sum += p[i].sum * exp(static_cast<double>(p[i].most) - static_cast<double>(most));
       sum = wave_sum(sum);
       offset = static_cast<double>(score) - (static_cast<double>(most) + log(sum));
       alive = alive && fabsf(most) < INFINITY;
@@ -323,33 +452,31 @@ __global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
   if (tid == 0) s_count = 0;
   __syncthreads();
 
-  const int total = a.beams * a.chunks * a.k;
   int kept = 0;
-  for (int first = 0; first < total; first += 256 * kJoinPer) {
+  for (int first = 0; first < total; first += kJoinThreads * kJoinPer) {
+    if (first > 0) fetch(first);
     double v[kJoinPer];
     uint32_t at[kJoinPer];
     uint64_t best = 0;
 #pragma unroll
     for (int i = 0; i < kJoinPer; ++i) {
-      const int e = first + i * 256 + tid;
+      const int e = first + i * kJoinThreads + tid;
       v[i] = -__builtin_inf();
       at[i] = 0;
       if (e < total) {
-        const int list = e / a.k, r = e - list * a.k, b = list / a.chunks;
-        if (s_alive[b] == 2) {
-          if (e == b * a.chunks * a.k) {
-            v[i] = a.scores[row0 + b];
-            at[i] = static_cast<uint32_t>(b) * a.vocabulary + a.pad;
-          }
-        } else if (s_alive[b] == 1 && r < a.partial[row0 * a.chunks + list].count) {
-          const Candidate c = a.list[(row0 * a.chunks + list) * a.k + r];
-          v[i] = s_offset[b] + static_cast<double>(c.x);
-          at[i] = static_cast<uint32_t>(b) * a.vocabulary + c.token;
+        const int b = e / row_of, alive = s_alive[b];
+        at[i] = static_cast<uint32_t>(b) * a.vocabulary;
+        if (alive == 1) {
+          v[i] = s_offset[b] + static_cast<double>(c[i].x);
+          at[i] += c[i].token;
+        } else if (alive == 2 && e == b * row_of) {            // a finished beam's one
+          v[i] = a.scores[row0 + b];
+          at[i] += a.pad;
         }
       }
       if (v[i] > -__builtin_inf()) best = max(best, ordered(v[i]));
     }
-    const Bound<uint64_t> mine = bound_of(best, a.k, [&] {
+    const Bounds<uint64_t> mine = bounds_of(best, 64, a.k, kJoinWaves, true, [&] {
       uint32_t low = 0xFFFFFFFFu;
 #pragma unroll
       for (int i = 0; i < kJoinPer; ++i)
@@ -357,16 +484,13 @@ __global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
       return low;
     });
     if (lane == 0) s_bound[wave] = mine;
-    for (int i = tid; i < kept; i += 256) {                  // the best of those before
+    for (int i = tid; i < kept; i += kJoinThreads) {           // the best of those before
       const int n = atomicAdd(&s_count, 1);
       value[n] = kept_value[i];
       place[n] = kept_place[i];
     }
     __syncthreads();
-    Bound<uint64_t> bound = s_bound[0];
-#pragma unroll
-    for (int w = 1; w < 4; ++w)
-      if (tighter(s_bound[w], bound)) bound = s_bound[w];
+    const Bound<uint64_t> bound = block_bound(s_bound);
 #pragma unroll
     for (int i = 0; i < kJoinPer; ++i) {
       if (!(v[i] > -__builtin_inf())) continue;
@@ -382,7 +506,7 @@ __global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
     __syncthreads();
     const int n = min(s_count, kJoinRoom);
     kept = min(n, a.k);
-    for (int i = tid; i < n; i += 256) {
+    for (int i = tid; i < n; i += kJoinThreads) {
       const double mine_v = value[i];
       const uint32_t mine_at = place[i];
       int rank = 0;
@@ -396,7 +520,7 @@ __global__ __launch_bounds__(256) void beam_join_kernel(Select a) {
     if (tid == 0) s_count = 0;
     __syncthreads();
   }
-  for (int i = tid; i < a.k; i += 256) {
+  for (int i = tid; i < a.k; i += kJoinThreads) {
     const int64_t o = static_cast<int64_t>(blockIdx.x) * a.k + i;
     const bool some = i < kept;
     const uint32_t at = some ? kept_place[i] : 0u, b = at / a.vocabulary;
@@ -540,13 +664,13 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t row_stride, in
   a.out_tokens = out_tokens;
   a.out_parents = out_parents;
   hipStream_t s = as_stream(stream);
-  const size_t lds = room_of(static_cast<int>(k)) * sizeof(Candidate);
+  const size_t lds = 4 * room_of(static_cast<int>(k)) * sizeof(Candidate);
   const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(std::min<int64_t>(rows, 65535)),
                   static_cast<unsigned>(ceil_div(rows, 65535)));
   if (dtype == QMM_BF16) beam_rows_kernel<QMM_BF16><<<grid, 256, lds, s>>>(a);
   else if (dtype == QMM_F16) beam_rows_kernel<QMM_F16><<<grid, 256, lds, s>>>(a);
   else beam_rows_kernel<QMM_F32><<<grid, 256, lds, s>>>(a);
-  beam_join_kernel<<<static_cast<unsigned>(seqs), 256, 0, s>>>(a);
+  beam_join_kernel<<<static_cast<unsigned>(seqs), kJoinThreads, 0, s>>>(a);
   return launch_status();
 }
 
