@@ -12,8 +12,7 @@ typedef short i16x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_anywhere __attribute__((aligned(2)));
 
 constexpr int kMostBeams = 64, kMostK = 64;
-constexpr int kPerThread = 32;                     // logits of a thread
-constexpr int kChunk = 256 * kPerThread;           // of a block
+constexpr int kThreadBytes = 128;                  // logits of a thread
 
 // What a block found in its logits of a row: their maximum and the sum of
 // exp(x - maximum).
@@ -110,8 +109,8 @@ __device__ __forceinline__ Bound<K> block_bound(const Bounds<K> (&all)[WAVES]) {
   }
   return tighter(least, most) ? least : most;
 }
-// What a wavefront lets through.
-__host__ __device__ constexpr int room_of(int k) { return k * kPerThread + 7; }
+// Candidates that a wavefront has room for.
+__host__ __device__ constexpr int room_of(int k) { return 2 * k + 32; }
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
@@ -213,23 +212,28 @@ struct Logits<QMM_F16> {
   }
 };
 
-// A block takes 8192 logits of a row, 32 a thread in registers, reads them once
-// and finds their maximum, the sum of exponentials and the k largest.  The
-// largest: no logit below the k-th best of a wavefront's 64 lane maxima can be
-// among them (a search over the bits of a key, one comparison and a count of
-// lanes each), so a few more than k reach LDS, where each counts those before
-// it.  These, which are most of a peaked row's sum, add to it in fp64, the
-// others in fp32 by the hardware's exponential: two beams' candidates that are
-// nearly as good are told apart by their rows' sums.
+// A block takes 8192 fp32 logits of a row or 16384 of 16 bits, 128 bytes a thread
+// in registers, reads them once and finds their maximum, the sum of exponentials
+// and the k largest.  The largest: no logit below the k-th best of a wavefront's
+// 64 lane maxima can be among them (a search over the bits of a key, one
+// comparison and a count of lanes each), so a few more than k reach LDS, where
+// each counts those before it.  These, which are most of a peaked row's sum, add
+// to it in fp64, the others in fp32 by the hardware's exponential: two beams'
+// candidates that are nearly as good are told apart by their rows' sums.
+//   Where values equal to the bound, or sorted ones, are more than LDS has room
+// for, or a NaN is met (the sum has taken it), the k largest are found one by one.
 template <int DT>
-__global__ __launch_bounds__(256, 8) void beam_rows_kernel(Select a) {
+__global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
   using L = Logits<DT>;
-  constexpr int kOf = L::kOf, kPieces = kPerThread / kOf;
+  constexpr int kOf = L::kOf, kPieces = kThreadBytes / 16;
+  constexpr int kChunk = 256 * kPieces * kOf;
   constexpr float kLog2e = 1.44269504088896341f;
-  extern __shared__ __attribute__((aligned(16))) Candidate pool[];     // [4][room_of(k)]
-  __shared__ float s_most[4];
-  __shared__ double s_sum[4];
+  extern __shared__ __attribute__((aligned(16))) float pool_x[];       // [4][room_of(k)], then as many tokens
+  __shared__ float s_most[4], s_sum[4];
+  __shared__ double s_large[4];
   __shared__ Bounds<uint32_t> s_bound[4];
+  __shared__ uint64_t s_best[4];
+  __shared__ int s_rank[4][kWave];
   __shared__ int s_count[4], s_again[4];
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -237,6 +241,7 @@ __global__ __launch_bounds__(256, 8) void beam_rows_kernel(Select a) {
   const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
   if (row >= a.rows || (a.finished && a.finished[row])) return;
   const int room = room_of(a.k);
+  uint32_t* const pool_token = reinterpret_cast<uint32_t*>(pool_x + 4 * room);
 
   // Whole pieces from the row's start on, wherever that lies (the hardware takes
   // 16 bytes from any address, and rows of the same logits have the same sums to
@@ -262,143 +267,175 @@ __global__ __launch_bounds__(256, 8) void beam_rows_kernel(Select a) {
     else odd = f16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[odd_index]);
   }
 
-  float most, sum, at_base;
-  int mine_n;                         // candidates of the wavefront
-  for (int turn = 0;; ++turn) {
-    asm volatile("" : "+v"(first_index));                  // indexes are worked out where they are used
-    // ---- the lane's best, the block's maximum, the bound
-    const float best = fmaxf(L::largest(raw), odd);
-    const uint32_t key = best > -INFINITY ? L::key(best) : 0u;
-    const Bounds<uint32_t> mine = bounds_of(key, L::kBits, a.k, 4, turn > 0, [&] {
-      uint32_t at = odd == best ? odd_index : 0xFFFFFFFFu;
-#pragma unroll
-      for (int j = 0; j < kPieces; ++j) {
-        asm volatile("" : "+v"(raw[j]));                   // unpacked anew: 64 registers
-#pragma unroll
-        for (int e = 0; e < kOf; ++e) at = L::get(raw[j], e) == best ? min(at, index_of(j, e)) : at;
-      }
-      return at;
-    });
-    const float wave_most = wave_max(best);
-    if (lane == 0) {
-      s_most[wave] = wave_most;
-      s_bound[wave] = mine;
-    }
-    __syncthreads();
-    const Bound<uint32_t> bound = block_bound(s_bound);
-    most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
-    // ---- sums below the bound; what passes it goes to the wavefront's part of LDS
-    // (without a bound all but -inf does)
-    const float least = bound.key ? L::value(bound.key) : -3.402823466e38f;
-    const bool ties = bound.index != 0xFFFFFFFFu;          // not all that equal the bound
-    const float from = most == -INFINITY ? 0.0f : most;
-    at_base = from * kLog2e;
-    const bool far = fabsf(from) > 0x1p24f;                // where the rounding of at_base is no small number
-    sum = 0.0f;
-    mine_n = 0;
-    auto term = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -at_base)); };
-    auto take = [&](float x, uint32_t at, uint64_t who) {  // lanes whose x does
-      if (ties) {
-        const bool less = x == least && at > bound.index && (who >> lane & 1);
-        sum += less ? term(x) : 0.0f;
-        who &= ~__ballot(less);
-      }
-      const int n = mine_n + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who >> 32),
-                                                                        __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who), 0u)));
-      if ((who >> lane & 1) && n < room) pool[wave * room + n] = {x, at};
-      mine_n += __popcll(who);
-    };
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      asm volatile("" : "+v"(raw[j]));
-      uint64_t any = 0;
-      float x[kOf];
-#pragma unroll
-      for (int e = 0; e < kOf; ++e) {
-        x[e] = L::get(raw[j], e);
-        const bool below = !(x[e] >= least);               // or NaN
-        any |= ~__ballot(below);
-        sum += below ? term(x[e]) : 0.0f;
-      }
-      if (any) {
-#pragma unroll
-        for (int e = 0; e < kOf; ++e)
-          if (const uint64_t who = ~__ballot(!(x[e] >= least))) take(x[e], index_of(j, e), who);
-      }
-    }
-    sum += odd >= least ? 0.0f : term(odd);
-    if (far) {
-      // once more, the distance to the maximum first
-      sum = odd >= least && !(odd == least && odd_index > bound.index) ? 0.0f : __builtin_amdgcn_exp2f((odd - from) * kLog2e);
-      for (int j = 0; j < kPieces; ++j)
-        for (int e = 0; e < kOf; ++e) {
-          const uint32_t at = index_of(j, e);
-          if (at >= static_cast<uint32_t>(pieces * kOf)) continue;
-          float x;
-          if constexpr (DT == QMM_F32) x = reinterpret_cast<const float*>(base)[at];
-          else if constexpr (DT == QMM_BF16) x = bf16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[at]);
-          else x = f16lo_to_f32(reinterpret_cast<const uint16_t*>(base)[at]);
-          if (turn == 1 && x != x) x = -INFINITY;
-          if (!(x >= least) || (x == least && at > bound.index)) sum += __builtin_amdgcn_exp2f((x - from) * kLog2e);
-        }
-    }
-    if (const uint64_t who = __ballot(odd >= least)) take(odd, odd_index, who);
-    if (lane == 0) s_count[wave] = min(mine_n, room);
-    if (turn == 1) {
-      __syncthreads();
-      break;
-    }
-    // Once more where a NaN (which the sum has taken, and which counts as -inf) was
-    // met, or so many equal values that they need their indexes: 16-bit lane maxima
-    // are often equal, and those that pass besides are few (the indexes of every
-    // bound looked for at once: 400 of 750 vector instructions).
-    const bool nan = __any(sum != sum);
-    if (lane == 0) s_again[wave] = nan || mine_n > room;
-    __syncthreads();
-    if (!(s_again[0] | s_again[1] | s_again[2] | s_again[3])) break;
-    if (odd != odd) odd = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      asm volatile("" : "+v"(raw[j]));
-#pragma unroll
-      for (int e = 0; e < kOf; ++e) {
-        const float x = L::get(raw[j], e);
-        if (x != x) L::set_none(raw[j], e);
-      }
-    }
-    __syncthreads();                  // counts and flags may be written again
+  // ---- the lane's best, the block's maximum, the bound
+  const float best = fmaxf(L::largest(raw), odd);
+  const Bounds<uint32_t> mine =
+      bounds_of(best > -INFINITY ? L::key(best) : 0u, L::kBits, a.k, 4, false, [] { return 0u; });
+  float most = wave_max(best);
+  if (lane == 0) {
+    s_most[wave] = most;
+    s_bound[wave] = mine;
   }
-
-  // each candidate counts those before it
-  const int n1 = s_count[0], n2 = n1 + s_count[1], n3 = n2 + s_count[2], n = n3 + s_count[3];
-  auto candidate = [&](int i) {
-    return pool[i < n1 ? i : i < n2 ? room + i - n1 : i < n3 ? 2 * room + i - n2 : 3 * room + i - n3];
+  __syncthreads();
+  const Bound<uint32_t> bound = block_bound(s_bound);
+  most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
+  // ---- sums below the bound; what passes it (without one all but -inf does)
+  // goes to the wavefront's part of LDS
+  const float least = bound.key ? L::value(bound.key) : -3.402823466e38f;
+  const float at_base = most == -INFINITY ? 0.0f : most * kLog2e;
+  float sum = 0.0f;
+  int mine_n = 0;
+  auto term = [&](float x) { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -at_base)); };
+  constexpr int kNotGreaterOrEqual = 12;                   // (the compiler's number of that comparison, true for NaN)
+  auto take = [&](float x, uint32_t at, uint64_t who) {
+    const int n = mine_n + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who >> 32),
+                                                                      __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who), 0u)));
+    if (x >= least && n < room) {
+      pool_x[wave * room + n] = x;
+      pool_token[wave * room + n] = at;
+    }
+    mine_n += __popcll(who);
   };
+#pragma unroll
+  for (int j = 0; j < kPieces; ++j) {
+    asm volatile("" : "+v"(raw[j]), "+v"(first_index));    // numbers are unpacked where they are used, indexes worked out
+    uint64_t below[kOf], all = ~uint64_t{0};               // lanes, NaN among them
+    float x[kOf];
+#pragma unroll
+    for (int e = 0; e < kOf; ++e) {
+      x[e] = L::get(raw[j], e);
+      below[e] = __builtin_amdgcn_fcmpf(x[e], least, kNotGreaterOrEqual);
+      all &= below[e];
+      sum += __builtin_amdgcn_inverse_ballot_w64(below[e]) ? term(x[e]) : 0.0f;
+    }
+    if (~all) {
+#pragma unroll
+      for (int e = 0; e < kOf; ++e)
+        if (~below[e]) take(x[e], index_of(j, e), ~below[e]);
+    }
+  }
+  sum += odd >= least ? 0.0f : term(odd);
+  if (const uint64_t who = __ballot(odd >= least)) take(odd, odd_index, who);
+  const bool nan = __any(sum != sum);
+  sum = wave_sum(sum);
+  if (lane == 0) {
+    // (past 2^24 the rounding of at_base is no small number)
+    s_again[wave] = nan || mine_n > room || fabsf(most) > 0x1p24f;
+    s_count[wave] = mine_n;
+    s_sum[wave] = sum;
+  }
+  __syncthreads();
+
   const int64_t at = row * a.chunks + chunk;
   Candidate* list = a.list + at * a.k;
-  double large = 0.0;                 // the sum of those that reached LDS
-  for (int i = tid; i < n; i += 256) {
-    const Candidate c = candidate(i);
-    const uint32_t key = ordered(c.x);
-    int rank = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-      for (int j = 0; j < s_count[w]; ++j) {
-        const Candidate o = pool[w * room + j];
-        const uint32_t ko = ordered(o.x);
-        rank += ko > key || (ko == key && o.token < c.token);
+  double small, large = 0.0;          // the sums of those that were not and those that were taken
+  double back;                        // from the first's base to the maximum
+  if (!(s_again[0] | s_again[1] | s_again[2] | s_again[3])) {
+    // each candidate counts those before it
+    const int n1 = s_count[0], n2 = n1 + s_count[1], n3 = n2 + s_count[2], n = n3 + s_count[3];
+    auto place_of = [&](int i) { return i < n1 ? i : i < n2 ? room + i - n1 : i < n3 ? 2 * room + i - n2 : 3 * room + i - n3; };
+    // (of few, every wavefront counts among its own)
+    if (n <= kWave) {
+      if (lane < n) {
+        const float x = pool_x[place_of(lane)];
+        const uint32_t key = ordered(x), token = pool_token[place_of(lane)];
+        int rank = 0;
+        const int count = s_count[wave];
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) {
+          const uint32_t ko = ordered(pool_x[wave * room + j]);
+          rank += ko > key || (ko == key && pool_token[wave * room + j] < token);
+        }
+        s_rank[wave][lane] = rank;
       }
-    if (rank < a.k) list[rank] = c;
-    large += exp(static_cast<double>(c.x) - static_cast<double>(most));
+      __syncthreads();
+      if (tid < n) {
+        const int rank = s_rank[0][tid] + s_rank[1][tid] + s_rank[2][tid] + s_rank[3][tid];
+        const Candidate c{pool_x[place_of(tid)], pool_token[place_of(tid)]};
+        if (rank < a.k) list[rank] = c;
+        large = exp(static_cast<double>(c.x) - static_cast<double>(most));
+      }
+    } else for (int i = tid; i < n; i += 256) {
+      const int place = place_of(i);
+      const Candidate c{pool_x[place], pool_token[place]};
+      const uint32_t key = ordered(c.x);
+      int rank = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int count = s_count[w];
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) {
+          const uint32_t ko = ordered(pool_x[w * room + j]);
+          rank += ko > key || (ko == key && pool_token[w * room + j] < c.token);
+        }
+      }
+      if (rank < a.k) list[rank] = c;
+      large += exp(static_cast<double>(c.x) - static_cast<double>(most));
+    }
+    for (int i = n + tid; i < a.k; i += 256) list[i] = {-INFINITY, 0u};
+    if (wave == 0 || n > kWave) large = wave_sum(large);     // (64 or fewer are all the first's)
+    small = static_cast<double>(s_sum[0]) + s_sum[1] + s_sum[2] + s_sum[3];
+    back = 0.0;
+  } else {
+    // ---- one by one, in their order: the largest below the last one taken, of
+    // logits read again (registers would hold them for this path alone)
+    auto each = [&](auto&& f) {
+      f(odd, odd_index);
+#pragma unroll 1
+      for (int j = 0; j < kPieces; ++j) {
+        const int p = (chunk * kPieces + j) * 256 + tid;
+        if (p >= pieces) break;
+        const u32x4 v = *reinterpret_cast<const u32x4_anywhere*>(base + static_cast<int64_t>(p) * 16);
+#pragma unroll
+        for (int e = 0; e < kOf; ++e) f(L::get(v, e), static_cast<uint32_t>(p * kOf + e));
+      }
+    };
+    auto key_of = [](float x, uint32_t index) { return static_cast<uint64_t>(ordered(x)) << 32 | static_cast<uint32_t>(~index); };
+    auto best_below = [&](uint64_t last) {
+      uint64_t top = 0;               // key, then the index the other way round; 0: none
+      each([&](float x, uint32_t index) {
+        const uint64_t key = key_of(x, index);
+        if (x > -INFINITY && key < last) top = max(top, key);
+      });
+#pragma unroll 1
+      for (int i = 1; i < kWave; i <<= 1)
+        top = max(top, static_cast<uint64_t>(__shfl_xor(static_cast<long long>(top), i, kWave)));
+      __syncthreads();
+      if (lane == 0) s_best[wave] = top;
+      __syncthreads();
+      return max(max(s_best[0], s_best[1]), max(s_best[2], s_best[3]));
+    };
+    uint64_t last = ~uint64_t{0};
+    most = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < a.k; ++i) {
+      const uint64_t next = last ? best_below(last) : 0;
+      const float x = next ? unordered(static_cast<uint32_t>(next >> 32)) : -INFINITY;
+      if (i == 0) most = x;
+      if (tid == 0) list[i] = {x, next ? ~static_cast<uint32_t>(next) : 0u};
+      if (next && tid == 0) large += exp(static_cast<double>(x) - static_cast<double>(most));
+      last = next;
+    }
+    const float from = most == -INFINITY ? 0.0f : most;
+    sum = 0.0f;
+    each([&](float x, uint32_t index) {
+      if (x > -INFINITY && key_of(x, index) < last) sum += __builtin_amdgcn_exp2f((x - from) * kLog2e);
+    });
+    sum = wave_sum(sum);
+    __syncthreads();
+    if (lane == 0) s_sum[wave] = sum;
+    __syncthreads();
+    small = static_cast<double>(s_sum[0]) + s_sum[1] + s_sum[2] + s_sum[3];
+    back = 1.0;
   }
-  for (int i = n + tid; i < a.k; i += 256) list[i] = {-INFINITY, 0u};
-  const double small = wave_sum(sum);
-  if (wave == 0 || n > kWave) large = wave_sum(large);       // (64 or fewer are all the first's)
-  // the fp32 terms' own base back to the maximum: what its rounding left
-  const double back = fabsf(most) > 0x1p24f ? 1.0 : exp2(static_cast<double>(at_base) - static_cast<double>(most) * static_cast<double>(kLog2e));
-  if (lane == 0) s_sum[wave] = fma(small, back, large);
+  if (lane == 0) s_large[wave] = large;
   __syncthreads();
-  if (tid == 0) a.partial[at] = {s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3], most, 0.0f};
+  if (tid == 0) {
+    // the fp32 terms' own base back to the maximum: what its rounding left
+    if (back == 0.0) back = exp2(static_cast<double>(at_base) - static_cast<double>(most) * static_cast<double>(kLog2e));
+    if (most == -INFINITY) back = 1.0;
+    a.partial[at] = {fma(small, back, s_large[0] + s_large[1] + s_large[2] + s_large[3]), most, 0.0f};
+  }
 }
 
 // A block joins the rows of a sequence: each beam's log sum, then the k best of
@@ -530,10 +567,10 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
   }
 }
 
-int64_t chunks_of(int64_t vocabulary) { return ceil_div(vocabulary, kChunk); }
+int64_t chunks_of(int64_t vocabulary, int bytes) { return ceil_div(vocabulary, 256 * kThreadBytes / bytes); }
 
 size_t select_bytes(int64_t rows, int64_t vocabulary, int64_t k) {
-  return static_cast<size_t>(rows) * chunks_of(vocabulary) * (sizeof(Partial) + k * sizeof(Candidate));
+  return static_cast<size_t>(rows) * chunks_of(vocabulary, 4) * (sizeof(Partial) + k * sizeof(Candidate));
 }
 
 // ---------------------------------------------------------------------------
@@ -640,7 +677,7 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t row_stride, in
     return QMM_EINVAL;
   if (dtype == QMM_I32 || beams > kMostBeams || k > kMostK) return QMM_EUNSUPPORTED;
   if (vocabulary >= (int64_t{1} << 31) / beams || seqs >= (int64_t{1} << 24) / beams) return QMM_ERANGE;
-  const int64_t rows = seqs * beams, chunks = chunks_of(vocabulary);
+  const int64_t rows = seqs * beams, chunks = chunks_of(vocabulary, dtype == QMM_F32 ? 4 : 2);
   if (rows * chunks >= (int64_t{1} << 24)) return QMM_ERANGE;            // blocks of 256 threads a launch holds
   if (!aligned(logits, dtype == QMM_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
       !aligned(out_tokens, 8) || !aligned(out_parents, 8))
