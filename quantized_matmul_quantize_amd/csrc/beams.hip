@@ -112,10 +112,20 @@ __device__ __forceinline__ Bound<K> block_bound(const Bounds<K> (&all)[WAVES]) {
 // Candidates that a wavefront has room for.
 __host__ __device__ constexpr int room_of(int k) { return 2 * k + 32; }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int i = 1; i < kWave; i <<= 1) v += __shfl_xor(v, i, kWave);
-  return v;
+  v += dpp_d<kDppXor1>(v);
+  v += dpp_d<kDppXor2>(v);
+  v += dpp_d<kDppHalfMirror>(v);
+  v += dpp_d<kDppMirror>(v);
+  v += __shfl_xor(v, 16, kWave);
+  return v + __shfl_xor(v, 32, kWave);
 }
 
 struct Select {
@@ -472,11 +482,14 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
     if (!ends) {
       const Partial* p = a.partial + (row0 + b) * a.chunks;
       float most = -INFINITY;
-      for (int i = lane; i < a.chunks; i += kWave) most = fmaxf(most, p[i].most);
-      most = wave_max(most);
       double sum = 0.0;
-      for (int i = lane; i < a.chunks; i += kWave)
-        if (p[i].most > -INFINITY) sum += p[i].sum * exp(static_cast<double>(p[i].most) - static_cast<double>(most));
+      for (int i = 0; i < a.chunks; i += kWave) {            // (64 blocks hold most vocabularies)
+        const Partial mine = i + lane < a.chunks ? p[i + lane] : Partial{0.0, -INFINITY, 0.0f};
+        const float now = fmaxf(most, wave_max(mine.most));
+        if (now > most) sum *= exp(static_cast<double>(most) - static_cast<double>(now));
+        most = now;
+        if (mine.most > -INFINITY) sum += mine.sum * exp(static_cast<double>(mine.most) - static_cast<double>(most));
+      }
       sum = wave_sum(sum);
       offset = static_cast<double>(score) - (static_cast<double>(most) + log(sum));
       alive = alive && fabsf(most) < INFINITY;
@@ -486,22 +499,22 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
       s_alive[b] = alive ? (ends ? 2 : 1) : 0;
     }
   }
-  if (tid == 0) s_count = 0;
   __syncthreads();
 
+  const double per_row = 1.0 / row_of;
   int kept = 0;
   for (int first = 0; first < total; first += kJoinThreads * kJoinPer) {
     if (first > 0) fetch(first);
     double v[kJoinPer];
     uint32_t at[kJoinPer];
-    uint64_t best = 0;
+    double best = -__builtin_inf();
 #pragma unroll
     for (int i = 0; i < kJoinPer; ++i) {
       const int e = first + i * kJoinThreads + tid;
       v[i] = -__builtin_inf();
       at[i] = 0;
       if (e < total) {
-        const int b = e / row_of, alive = s_alive[b];
+        const int b = static_cast<int>((e + 0.5) * per_row), alive = s_alive[b];      // e / row_of
         at[i] = static_cast<uint32_t>(b) * a.vocabulary;
         if (alive == 1) {
           v[i] = s_offset[b] + static_cast<double>(c[i].x);
@@ -511,50 +524,56 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
           at[i] += a.pad;
         }
       }
-      if (v[i] > -__builtin_inf()) best = max(best, ordered(v[i]));
+      best = fmax(best, v[i]);
     }
-    const Bounds<uint64_t> mine = bounds_of(best, 64, a.k, kJoinWaves, true, [&] {
-      uint32_t low = 0xFFFFFFFFu;
+    // The bound by fp32 keys first (all that round to the bound's pass); where
+    // that lets through more than there is room for, by fp64 ones and indexes.
+    for (int turn = 0;; ++turn) {
+      const bool some = best > -__builtin_inf();
+      const uint64_t key = !some ? 0 : turn ? ordered(best) : ordered(static_cast<float>(best));
+      const Bounds<uint64_t> mine = bounds_of(key, turn ? 64 : 32, a.k, kJoinWaves, turn > 0, [&] {
+        uint32_t low = 0xFFFFFFFFu;
 #pragma unroll
-      for (int i = 0; i < kJoinPer; ++i)
-        if (v[i] > -__builtin_inf() && ordered(v[i]) == best) low = min(low, at[i]);
-      return low;
-    });
-    if (lane == 0) s_bound[wave] = mine;
-    for (int i = tid; i < kept; i += kJoinThreads) {           // the best of those before
-      const int n = atomicAdd(&s_count, 1);
-      value[n] = kept_value[i];
-      place[n] = kept_place[i];
-    }
-    __syncthreads();
-    const Bound<uint64_t> bound = block_bound(s_bound);
+        for (int i = 0; i < kJoinPer; ++i)
+          if (v[i] == best) low = min(low, at[i]);
+        return low;
+      });
+      if (lane == 0) s_bound[wave] = mine;
+      for (int i = tid; i < kept; i += kJoinThreads) {         // the best of those before
+        value[i] = kept_value[i];
+        place[i] = kept_place[i];
+      }
+      if (tid == 0) s_count = kept;
+      __syncthreads();
+      const Bound<uint64_t> bound = block_bound(s_bound);
 #pragma unroll
-    for (int i = 0; i < kJoinPer; ++i) {
-      if (!(v[i] > -__builtin_inf())) continue;
-      const uint64_t key = ordered(v[i]);
-      if (key > bound.key || (key == bound.key && at[i] <= bound.index)) {
-        const int n = atomicAdd(&s_count, 1);
-        if (n < kJoinRoom) {
-          value[n] = v[i];
-          place[n] = at[i];
+      for (int i = 0; i < kJoinPer; ++i) {
+        const uint64_t own = turn ? ordered(v[i]) : ordered(static_cast<float>(v[i]));
+        if (v[i] > -__builtin_inf() && (own > bound.key || (own == bound.key && at[i] <= bound.index))) {
+          const int n = atomicAdd(&s_count, 1);
+          if (n < kJoinRoom) {
+            value[n] = v[i];
+            place[n] = at[i];
+          }
         }
       }
+      __syncthreads();
+      if (s_count <= kJoinRoom) break;
+      __syncthreads();                 // the count may be written again
     }
-    __syncthreads();
-    const int n = min(s_count, kJoinRoom);
+    const int n = s_count;
     kept = min(n, a.k);
     for (int i = tid; i < n; i += kJoinThreads) {
       const double mine_v = value[i];
       const uint32_t mine_at = place[i];
       int rank = 0;
+#pragma unroll 4
       for (int j = 0; j < n; ++j) rank += value[j] > mine_v || (value[j] == mine_v && place[j] < mine_at);
       if (rank < a.k) {
         kept_value[rank] = mine_v;
         kept_place[rank] = mine_at;
       }
     }
-    __syncthreads();
-    if (tid == 0) s_count = 0;
     __syncthreads();
   }
   for (int i = tid; i < a.k; i += kJoinThreads) {
