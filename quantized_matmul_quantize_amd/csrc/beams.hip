@@ -606,13 +606,15 @@ struct Reorder {
   int32_t beams;
   int32_t* table_out;
   int32_t* context_out;
-  int32_t heads_per;         // heads of a block
 };
 
-// blockIdx.x a slot, .y a layer, .z some of its heads: the filled part of the
+// blockIdx.x a slot, .y a layer, .z two of its heads: the filled part of the
 // parent's last page, four 16-byte pieces a thread in flight.  The first block
-// of a slot writes its row of the table.
-constexpr int kReorderPieces = 4;
+// of a slot writes its row of the table.  Bound by memory and, before the first
+// piece, by four loads that wait for each other (parent, its length, its page,
+// the piece): 16 x 8 beams in 16 layers of 8 heads of 128, 77 MB read and written,
+// 33 us with all heads in a block, 28 with one, 24.5 with two.
+constexpr int kReorderPieces = 4, kReorderHeads = 2;
 
 __global__ __launch_bounds__(256) void kv4_beam_reorder_kernel(Reorder a) {
   const int slot = blockIdx.x, seq = slot / a.beams;
@@ -643,7 +645,8 @@ __global__ __launch_bounds__(256) void kv4_beam_reorder_kernel(Reorder a) {
   // fours of tokens: pieces of K codes, of V codes, then of each row of params
   const int fours = (filled + 3) >> 2, D = a.sh.D;
   const int codes = fours * (D / 8), record = 2 * codes + 2 * a.sh.groups() * fours;
-  const int h0 = static_cast<int>(blockIdx.z) * a.heads_per, h1 = min(h0 + a.heads_per, a.sh.heads);
+  const int h0 = static_cast<int>(blockIdx.z) * kReorderHeads, h1 = min(h0 + kReorderHeads, a.sh.heads);
+  const float per_four = 1.0f / fours;
   const int64_t bytes = a.sh.record_bytes();
   uint8_t* layer = a.cache + static_cast<int64_t>(blockIdx.y) * a.sh.pages * a.sh.heads * bytes;
   const uint8_t* src = layer + static_cast<int64_t>(from) * a.sh.heads * bytes;
@@ -656,10 +659,10 @@ __global__ __launch_bounds__(256) void kv4_beam_reorder_kernel(Reorder a) {
     for (int i = 0; i < kReorderPieces; ++i) {
       const int p = p0 + i * 256;
       if (p < total) {
-        const int h = p / record, q = p - h * record;
+        const int h = p >= record ? 1 : 0, q = p - h * record;
         int offset = 16 * q;
         if (q >= 2 * codes) {
-          const int r = (q - 2 * codes) / fours;
+          const int r = static_cast<int>((q - 2 * codes + 0.5f) * per_four);          // (q - 2 codes) / fours
           offset = a.sh.page * (D + 4 * r) + 16 * (q - 2 * codes - r * fours);
         } else if (q >= codes) {
           offset = a.sh.page * (D / 2) + 16 * (q - codes);
@@ -759,11 +762,8 @@ extern "C" int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, i
   a.beams = static_cast<int32_t>(beams);
   a.table_out = table_out;
   a.context_out = context_out;
-  // heads of a block: all, but where layers and slots are few as many blocks as fill the chip
-  const int64_t slots = seqs * beams, want = ceil_div(8 * device_cus(), slots * layers);
-  a.heads_per = static_cast<int32_t>(ceil_div(kv_heads, std::min<int64_t>(kv_heads, want)));
-  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(layers),
-                  static_cast<unsigned>(ceil_div(kv_heads, a.heads_per)));
+  const dim3 grid(static_cast<unsigned>(seqs * beams), static_cast<unsigned>(layers),
+                  static_cast<unsigned>(ceil_div(kv_heads, kReorderHeads)));
   if (static_cast<int64_t>(grid.x) * grid.y * grid.z >= (int64_t{1} << 24)) return QMM_ERANGE;
   kv4_beam_reorder_kernel<<<grid, 256, 0, as_stream(stream)>>>(a);
   return launch_status();
