@@ -18,6 +18,8 @@
 // So nothing is left per score and group but one operation with the key's scale.
 #pragma once
 
+#include <utility>
+
 #include "kv4_attention.h"
 
 namespace qmm {
@@ -58,16 +60,14 @@ struct Rows {
   static_assert(kWords == D / 64, "two threads to every fourth word of a key");
 };
 
-// M matrix instructions with S pieces of vector work spread between them.
-template <int M, int S, typename F, typename H>
-__device__ __forceinline__ void weave(F mfma, H piece) {
-#pragma unroll
-  for (int i = 0; i < M; ++i) {
-    mfma(i);
-#pragma unroll
-    for (int k = i * S / M; k < (i + 1) * S / M; ++k) piece(k);
-    __builtin_amdgcn_sched_barrier(0);
-  }
+// f(0), f(1), .. f(N - 1), their arguments constants
+template <typename F, int... I>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each(f, std::make_integer_sequence<int, N>{});
 }
 
 template <int DT, int D, int GROUP>
@@ -82,7 +82,6 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   auto k_lds = [&](int i) { return lds + (i & 1) * L::kKBuffer; };
   auto v_lds = [&](int i) { return lds + 2 * L::kKBuffer + (i & 1) * L::kVBuffer; };
   uint8_t* const ring = lds + 2 * (L::kKBuffer + L::kVBuffer);
-  const uint32_t ring_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ring));
 
   // row tiles of the same keys eight blocks apart: on one die, whose cache holds the codes
   const uint32_t eight = id % 8;
@@ -154,11 +153,12 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   const bool l_values = wave >= kTiles16;
   const int l_codes = (l_values ? a.sh.page * (D / 2) : 0) + 16 * lane;
   const int l_params = a.sh.page * (D + (l_values ? 4 * G : 0)) + (lane >> 2) * a.sh.page * 4 + 16 * (lane & 3);
-  const uint32_t l_to = ring_at + (l_values ? L::kRaw : 0);
-  auto fetch = [&](int round, int slot, int page) {
+  const int l_ahead = l_values ? 0 : 1;            // a deal: the values of a round, the keys of the next
+  auto fetch = [&](int deal, const uint8_t* place_to, int page) {
+    const int round = deal + l_ahead;
     const __amdgpu_buffer_rsrc_t rs = tile_of(page);
     const int place = (key_lo + round * KEYS + 16 * l_tile) & (a.sh.page - 1);
-    const uint32_t to = l_to + slot * L::kSlot;
+    const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(place_to)) + (l_values ? L::kRaw : 0);
     if (D != 64 || lane < 32)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(uintptr_t)(to + l_tile * L::kCodes), 16, l_codes,
                                                place * (D / 2), 0, 0);
@@ -250,165 +250,214 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
     const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * h;
     __syncthreads();                               // LDS is free: the rows before are done
     int now_pages = pages_of(0);                   // of the batch that is fetched
-    uint64_t there = __ballot(now_pages >= 0), there_next = 0;
-#pragma unroll
-    for (int i = 0; i < L::kRing; ++i) fetch(i, i, __builtin_amdgcn_readlane(now_pages, i * kTiles16 + l_tile));
     u32x4 qv[kSteps];
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) qv[j] = live ? ld16(qp + 16 * j) : u32x4{0u, 0u, 0u, 0u};
+    uint64_t there = __ballot(now_pages >= 0), there_next = 0;
+    auto page_at = [&](int deal) { return __builtin_amdgcn_readlane(now_pages, (deal + l_ahead) % kBatch * kTiles16 + l_tile); };
+    // The first round's keys go where the second's operands will be.
+    if (!l_values) fetch(-1, k_lds(1), page_at(-1));
+#pragma unroll
+    for (int i = 0; i < L::kRing; ++i) fetch(i, ring + i * L::kSlot, page_at(i));
     fetch_pages(1);
     float unscale = 1.0f;
     if constexpr (DT == QMM_BF16) {
       float* stat = reinterpret_cast<float*>(lds);
       float most = wave_max(largest_bf16(qv, 0.0f));
       if (lane == 0) stat[wave] = most;
-      __syncthreads();
+      meet();
       most = stat[0];
 #pragma unroll
       for (int w = 1; w < kW; ++w) most = fmaxf(most, stat[w]);
       const QueryScale qs = query_scale(most);
-      __syncthreads();
+      meet();
       unscale = qs.up;
       to_f16(qv, qs.down);
     }
     key_scale = a.scale_log2 * unscale;
-    wait_vm<0>();                                  // the queries came last
+    wait_vm<L::kLoads * (L::kRing - 1) + 1>();     // the first keys and deal
     meet();
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) expand_keys(ring, k_lds(0), i);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) expand_values(ring, v_lds(0), i);
+    for (int i = 0; i < kPieces; ++i) expand_keys(k_lds(1), k_lds(0), i);
+    for (int i = threadIdx.x; i < L::kVBuffer / 16; i += L::kThreads) reinterpret_cast<u32x4*>(v_lds(1))[i] = u32x4{0u, 0u, 0u, 0u};
 
-    f32x16 o[kCh];
+    f32x16 o[kCh], x[T];
 #pragma unroll
     for (int c = 0; c < kCh; ++c)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[c][i] = 0.0f;
+    u32x4 p[T][2] = {};                              // nothing of the round before the first, whose values are zeros
     // p = 2^(x - base): at most 2^15, 2^7 where the maximum was last moved
     float base = -INFINITY, from = 0.0f, limit = -INFINITY, l = 0.0f;
-    int slot = 0;
-    meet();
 
-    // Every round the next one's operands are made of the codes at hand, and the
-    // codes of the sixth round from here are fetched.  Each run of matrix
-    // instructions has vector work between: the scores the keys' expansion and the
-    // scales of the tile and group before, the first tile's values the second's
-    // exponentials, the last tile's the values' expansion.
-    for (int round = 0; round < rounds; ++round) {
-      const uint8_t* kb = k_lds(round);
-      const uint8_t* vb = v_lds(round);
-      uint8_t* const k_next = k_lds(round + 1);
-      uint8_t* const v_next = v_lds(round + 1);
-      const int ahead = round + L::kRing;
-      if (ahead % kBatch == 0) {
-        now_pages = checked(*reinterpret_cast<const int*>(my_pages + 4 * lane), ahead / kBatch);
+    // The next deal but kRing, once all have read the one whose place it takes.
+    int slot = 0;
+    auto fetch_deal = [&](int deal) {
+      const int mine = deal + l_ahead;
+      if (mine % kBatch == 0) {
+        now_pages = checked(*reinterpret_cast<const int*>(my_pages + 4 * lane), mine / kBatch);
         there_next = __ballot(now_pages >= 0);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0xc07f);        // read before its place is written
-        fetch_pages(ahead / kBatch + 1);
+        fetch_pages(mine / kBatch + 1);
       }
-      if (round % kBatch == 0 && round > 0) there = there_next;
-      fetch(ahead, slot, __builtin_amdgcn_readlane(now_pages, ahead % kBatch * kTiles16 + l_tile));
+      fetch(deal, ring + slot * L::kSlot, page_at(deal));
       slot = slot + 1 == L::kRing ? 0 : slot + 1;
+    };
+    // a deal's codes to operands
+    auto expand = [&](int deal, int piece) {
       const uint8_t* raw = ring + slot * L::kSlot;
-      if (!active) {
+      if (piece % 2 == 0) expand_keys(raw, k_lds(deal + 1), piece / 2);
+      else expand_values(raw, v_lds(deal), piece / 2);
+    };
+
+    // The matrix instructions of a round: the values of the round before, then
+    // scores less the base they are taken at, products of a tile and group (a
+    // unit) while the unit before is scaled.  Operands are read kAhead
+    // instructions, scales a unit before their use: a wait for a read just sent
+    // waits for all before it.
+    constexpr bool kHalves = kW == 8;
+    constexpr int kV = 2 * T * kCh, kN = kV + T * kSteps, kUnits = T * G;
+    auto matrices = [&](int round) {
+      const uint8_t* vb = v_lds(round + 1);
+      const uint8_t* kb = k_lds(round);
+      auto read = [&](int i) {
+        const int c = i % kCh, m = i / kCh;                   // m: 16 keys
+        return i < kV ? *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16)
+                      : *reinterpret_cast<const u32x4*>(kb + ((i - kV) * 2 + h) * L::kHalf + 16 * r);
+      };
+      u32x4 ops[kAhead];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) expand_keys(raw, k_next, i);
+      for (int i = 0; i < kAhead; ++i) ops[i] = read(i);
+      f32x16 acc[2];
+      f32x4 sc[4];
+      auto scaled = [&](int unit, int c) {
+        const int t = unit / G, grp = unit % G;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) expand_values(raw, v_next, i);
-      } else {
-        // ---- scores less the base they are taken at: products of a tile and
-        // group (a unit) while the one before is scaled
-        u32x4 k[kAhead];
-        auto read_k = [&](int i) { return *reinterpret_cast<const u32x4*>(kb + (i * 2 + h) * L::kHalf + 16 * r); };
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) k[i] = read_k(i);
-        f32x16 acc[2], x[T];
-        auto score = [&](int i) {
-          const int j = i % kSteps, unit = i / kGSteps;
-          if (j % kGSteps == 0)
+        for (int e = 0; e < 4; ++e)
+          x[t][4 * c + e] = fmaf(acc[unit % 2][4 * c + e], sc[c][e], grp == 0 ? -from : x[t][4 * c + e]);
+      };
+      __builtin_amdgcn_sched_barrier(0);
+      each<kN>([&](auto index) {
+        constexpr int i = index;
+        const u32x4 op = ops[i % kAhead];
+        if constexpr (i < kV) {
+          o[i % kCh] = mfma32(op, p[i / kCh / 2][i / kCh % 2], o[i % kCh]);
+          if constexpr (i + kAhead < kN) ops[i % kAhead] = read(i + kAhead);
+          if constexpr (!kHalves) {
+            constexpr int first = i * 2 * kPieces / kV, last = (i + 1) * 2 * kPieces / kV;
+            each<last - first>([&](auto k) { expand(round, first + k); });
+          }
+        } else {
+          constexpr int j = (i - kV) % kSteps, unit = (i - kV) / kGSteps, at = j % kGSteps;
+          if constexpr (at == 0)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[unit % 2][e] = 0.0f;
-          acc[unit % 2] = mfma32(k[i % kAhead], qv[j], acc[unit % 2]);
-          if (i + kAhead < T * kSteps) k[i % kAhead] = read_k(i + kAhead);
-        };
-        auto scaled = [&](int unit, int c) {
-          const int t = unit / G, grp = unit % G;
-          const f32x4 sc = *reinterpret_cast<const f32x4*>(kb + L::kKOps + (grp * KEYS + 32 * t + 8 * c + 4 * h) * 4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[t][4 * c + e] = fmaf(acc[unit % 2][4 * c + e], sc[e], grp == 0 ? -from : x[t][4 * c + e]);
-        };
-        __builtin_amdgcn_sched_barrier(0);
-        constexpr int kUnits = T * G, kMost = (kPieces + kUnits - 1) / kUnits;      // pieces of the expansion with a unit
-#pragma unroll
-        for (int unit = 0; unit < kUnits; ++unit) {
-          weave<kGSteps, 4 + kMost>([&](int i) { score(unit * kGSteps + i); }, [&](int i) {
-            if (i < 4) {
-              if (unit > 0) scaled(unit - 1, i);
-            } else if (unit * kMost + i - 4 < kPieces) {
-              expand_keys(raw, k_next, unit * kMost + i - 4);
-            }
+          acc[unit % 2] = mfma32(op, qv[j], acc[unit % 2]);
+          constexpr int first = at * 4 / kGSteps, last = (at + 1) * 4 / kGSteps;
+          each<last - first>([&](auto k) {
+            constexpr int c = first + k;
+            if constexpr (unit > 0) scaled(unit - 1, c);
+            sc[c] = *reinterpret_cast<const f32x4*>(kb + L::kKOps + (unit % G * KEYS + 32 * (unit / G) + 8 * c + 4 * h) * 4);
           });
+          if constexpr (i + kAhead < kN) ops[i % kAhead] = read(i + kAhead);
         }
-        u32x4 v[kAhead];
-        auto read_v = [&](int i) {
-          const int c = i % kCh, m = i / kCh;                 // m: 16 keys
-          return *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
-        };
+        __builtin_amdgcn_sched_barrier(0);
+      });
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) v[i] = read_v(i);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) scaled(kUnits - 1, c);
-        // ---- keys of no page
-        const int holes = static_cast<int>(~there >> (round % kBatch * kTiles16)) & ((1 << kTiles16) - 1);
-        if (holes) {
-#pragma unroll
-          for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[t][e] = holes >> (2 * t + e / 8) & 1 ? -INFINITY : x[t][e];
-        }
-        // ---- running maximum
-        float top = x[0][0];
+      for (int c = 0; c < 4; ++c) scaled(kUnits - 1, c);
+    };
+    auto softmax = [&](int round) {
+      // ---- keys of no page
+      if (round % kBatch == 0 && round > 0) there = there_next;
+      const int holes = static_cast<int>(~there >> (round % kBatch * kTiles16)) & ((1 << kTiles16) - 1);
+      if (holes) {
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) top = max3(top, x[t][e], x[t][e + 1]);
-        if (__any(top > limit)) {
-          const float both = fmaxf(top, __shfl_xor(top, 32, kWave));
-          const float to = fmaxf(base, both + from - 7.0f);
-          const float fade = to == -INFINITY ? 1.0f : exp2_fast(base - to);
-          const float now_from = to == -INFINITY ? 0.0f : to;
+          for (int e = 0; e < 16; ++e) x[t][e] = holes >> (2 * t + e / 8) & 1 ? -INFINITY : x[t][e];
+      }
+      // ---- running maximum
+      float top = x[0][0];
 #pragma unroll
-          for (int t = 0; t < T; ++t) x[t] += from - now_from;
+      for (int t = 0; t < T; ++t)
 #pragma unroll
-          for (int c = 0; c < kCh; ++c) o[c] *= fade;
-          l *= fade;
-          base = to;
-          from = now_from;
-          limit = to == -INFINITY ? -INFINITY : 15.0f;
-        }
-        // ---- probabilities and sums
-        u32x4 p[T][2];
-        auto exponentials = [&](int t, int i) {
+        for (int e = 0; e < 16; e += 2) top = max3(top, x[t][e], x[t][e + 1]);
+      if (__any(top > limit)) {
+        const float both = fmaxf(top, __shfl_xor(top, 32, kWave));
+        const float to = fmaxf(base, both + from - 7.0f);
+        const float fade = to == -INFINITY ? 1.0f : exp2_fast(base - to);
+        const float now_from = to == -INFINITY ? 0.0f : to;
+#pragma unroll
+        for (int t = 0; t < T; ++t) x[t] += from - now_from;
+#pragma unroll
+        for (int c = 0; c < kCh; ++c) o[c] *= fade;
+        l *= fade;
+        base = to;
+        from = now_from;
+        limit = to == -INFINITY ? -INFINITY : 15.0f;
+      }
+      // ---- probabilities and sums
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
           const float p0 = exp2_fast(x[t][2 * i]), p1 = exp2_fast(x[t][2 * i + 1]);
           l += p0 + p1;
           p[t][i / 4][i % 4] = pack_pair<QMM_F16>(p0, p1);
-        };
-        auto value = [&](int i) {
-          const int c = i % kCh, m = i / kCh;
-          o[c] = mfma32(v[i % kAhead], p[m / 2][m % 2], o[c]);
-          if (i + kAhead < 2 * T * kCh) v[i % kAhead] = read_v(i + kAhead);
-        };
-#pragma unroll
-        for (int i = 0; i < 8; ++i) exponentials(0, i);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (T == 2) weave<2 * kCh, 8>(value, [&](int i) { exponentials(1, i); });
-        weave<2 * kCh, kPieces>([&](int i) { value(2 * (T - 1) * kCh + i); }, [&](int i) { expand_values(raw, v_next, i); });
-      }
-      // the codes that the next round expands: of this wavefront's loads those of kRing - 2 rounds may be on their way
-      wait_vm<L::kLoads * (L::kRing - 2)>();
+        }
+    };
+
+    // A round is a phase of matrix instructions and one of vector work: the softmax
+    // and the expansion of a deal.  The second four wavefronts, which share the
+    // SIMDs with the first four, are a phase behind, so that the one's matrix
+    // instructions run under the other's vector work.  Deal i is expanded in phase
+    // 2 i by the second half and 2 i + 1 by the first, and used from phase 2 i + 2
+    // on, when its place in the ring is filled again.  (Four wavefronts have a SIMD
+    // each and expand between matrix instructions.)
+    const bool second = kHalves && wave >= 4;
+    // (the first two pieces read the codes)
+    auto expand_rest = [&](int deal) { each<2 * kPieces - 2>([&](auto k) { expand(deal, k + 2); }); };
+    meet();
+    if (second) {
+      expand(0, 0), expand(0, 1);
+      expand_rest(0);
       meet();
+    }
+    for (int round = 0; round < rounds; ++round) {
+      if (!second && round > 0) fetch_deal(round - 1 + L::kRing);
+      if (active) {
+        __builtin_amdgcn_s_setprio(1);
+        matrices(round);
+        __builtin_amdgcn_s_setprio(0);
+      } else if constexpr (!kHalves) {
+        expand(round, 0), expand(round, 1);
+        expand_rest(round);
+      }
+      if constexpr (kHalves) {
+        if (second) wait_vm<L::kLoads * (L::kRing - 2)>();
+        meet();
+        if (second) fetch_deal(round + L::kRing);
+        const int deal = second ? round + 1 : round;
+        expand(deal, 0), expand(deal, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (active) softmax(round);
+        expand_rest(deal);
+        if (second && round + 1 == rounds) break;
+      } else if (active) {
+        softmax(round);
+      }
+      if (!second) wait_vm<L::kLoads * (L::kRing - 2)>();
+      meet();
+    }
+    if (active) {
+      const uint8_t* vb = v_lds(rounds - 1);
+#pragma unroll
+      for (int i = 0; i < kV; ++i) {
+        const int c = i % kCh, m = i / kCh;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
+        o[c] = mfma32(v, p[m / 2][m % 2], o[c]);
+      }
     }
 
     wait_vm<0>();                                  // nothing is on its way to LDS any more
