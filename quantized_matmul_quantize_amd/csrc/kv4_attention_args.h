@@ -188,7 +188,8 @@ struct AttnPlan {
 void attention_bf16(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 void attention_f16(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 
-void prefix_attention_bf16(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s);
-void prefix_attention_f16(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s);
+// (together: both parts in one launch, by the prefix's kernel)
+void prefix_attention_bf16(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, bool together, hipStream_t s);
+void prefix_attention_f16(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, bool together, hipStream_t s);
 
 }  // namespace qmm

@@ -2,6 +2,6 @@
 
 #include "kv4_prefix_launch.h"
 
-void qmm::prefix_attention_bf16(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s) {
-  launch_prefix<QMM_BF16>(a, prefix, own, s);
+void qmm::prefix_attention_bf16(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, bool together, hipStream_t s) {
+  launch_prefix<QMM_BF16>(a, prefix, own, together, s);
 }

@@ -14,6 +14,16 @@ __global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, NT)) void at
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, NT>::kWaveBytes];
   attention_block<DT, D, GROUP, PK, NT, PART>(a, blockIdx.x, lds);
 }
+// (a type of its own: the host's pass compiles no device function for two kernels)
+struct BothArgs : SharedArgs {
+  uint32_t prefix_blocks;
+};
+template <int DT, int D, int GROUP, int PK>
+__global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, 1)) void attention_both_kernel(BothArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, 1>::kWaveBytes];
+  if (blockIdx.x < a.prefix_blocks) attention_block<DT, D, GROUP, PK, 1, kPrefix>(a, blockIdx.x, lds);
+  else attention_block<DT, D, GROUP, PK, 1, kOwn>(a, blockIdx.x - a.prefix_blocks, lds);
+}
 template <int DT, int D, int GROUP, int NT>
 __global__ __launch_bounds__(256, D / GROUP < 8 ? 2 : 1) void attention_own_chunk_kernel(SharedArgs a) {
   using L = Chunk<D, GROUP, NT>;
@@ -37,25 +47,32 @@ void launch_part(const SharedArgs& a, const AttnPlan& p, hipStream_t s) {
   }
 }
 template <int DT, int D, int GROUP>
-void launch_parts(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s) {
+void launch_parts(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, bool together, hipStream_t s) {
+  if (together) {
+    const dim3 grid(static_cast<unsigned>(prefix.blocks + own.blocks));
+    const BothArgs both{a, static_cast<uint32_t>(prefix.blocks)};
+    if (prefix.pk == 1) attention_both_kernel<DT, D, GROUP, 1><<<grid, 256, 0, s>>>(both);
+    else if constexpr (attention_pairs(D, GROUP)) attention_both_kernel<DT, D, GROUP, 2><<<grid, 256, 0, s>>>(both);
+    return;
+  }
   launch_part<DT, D, GROUP, kPrefix>(a, prefix, s);
   launch_part<DT, D, GROUP, kOwn>(a, own, s);
 }
 
 template <int DT>
-void launch_prefix(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, hipStream_t s) {
+void launch_prefix(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, bool together, hipStream_t s) {
   const int D = a.sh.D, g = a.sh.group;
   if (D == 64) {
-    if (g == 32) launch_parts<DT, 64, 32>(a, prefix, own, s);
-    else launch_parts<DT, 64, 64>(a, prefix, own, s);
+    if (g == 32) launch_parts<DT, 64, 32>(a, prefix, own, together, s);
+    else launch_parts<DT, 64, 64>(a, prefix, own, together, s);
   } else if (D == 128) {
-    if (g == 32) launch_parts<DT, 128, 32>(a, prefix, own, s);
-    else if (g == 64) launch_parts<DT, 128, 64>(a, prefix, own, s);
-    else launch_parts<DT, 128, 128>(a, prefix, own, s);
+    if (g == 32) launch_parts<DT, 128, 32>(a, prefix, own, together, s);
+    else if (g == 64) launch_parts<DT, 128, 64>(a, prefix, own, together, s);
+    else launch_parts<DT, 128, 128>(a, prefix, own, together, s);
   } else {
-    if (g == 32) launch_parts<DT, 256, 32>(a, prefix, own, s);
-    else if (g == 64) launch_parts<DT, 256, 64>(a, prefix, own, s);
-    else launch_parts<DT, 256, 128>(a, prefix, own, s);
+    if (g == 32) launch_parts<DT, 256, 32>(a, prefix, own, together, s);
+    else if (g == 64) launch_parts<DT, 256, 64>(a, prefix, own, together, s);
+    else launch_parts<DT, 256, 128>(a, prefix, own, together, s);
   }
   const dim3 grid(static_cast<unsigned>(own.max_q < 1024 ? own.max_q : 1024), static_cast<unsigned>(a.q_heads),
                   static_cast<unsigned>(a.seqs));
