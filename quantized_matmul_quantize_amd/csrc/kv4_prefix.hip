@@ -20,7 +20,14 @@ AttnPlan part_plan(bool prefix, int64_t items, int64_t rows, int64_t kv_heads, i
                    int64_t* round, int pk = 0) {
   AttnPlan p{};
   const int d = static_cast<int>(D);
-  p.ws = rows <= 96;
+  const int64_t steps = std::max<int64_t>(1, ceil_div(keys, kStep));
+  // The kernel for many rows starts later and leaves more to join: prefixes of few
+  // steps (of 16 rows, for each of the blocks at once) stay with the kernel for few.
+  // 256 rows after 4096 tokens in 8 heads of 128 (32 steps) 48 us by rows, 41 here;
+  // 8192 tokens 52.5 both; 12288 56 against 64.  216 rows of 12 prefixes of 1500
+  // tokens in 2 heads of 64 (31) 45 against 49; 256 rows of 256 after 2048 (16) 58 against 53.
+  const int64_t short_of = (D == 64 ? 16 : 32) * 2 * device_cus();
+  p.ws = rows <= 96 || (prefix && items * kv_heads * ceil_div(rows, 16) * steps <= short_of);
   const int64_t fill = (p.ws || !prefix ? 2 : 1) * device_cus();
   const bool eights = rows <= 8;
   const bool sixteens = eights || rows <= 16 || items * kv_heads * ceil_div(rows, 16) < fill;
@@ -29,7 +36,7 @@ AttnPlan part_plan(bool prefix, int64_t items, int64_t rows, int64_t kv_heads, i
   p.rows = p.ws ? 16 / p.pk * p.nt : prefix ? (D == 256 ? 128 : 256) : 16 * p.nt * kWaves;
   // (blocks loop over row tiles past these: a launch holds 2^24 blocks of 256 threads)
   p.row_tiles = std::min(ceil_div(rows, p.rows), std::max<int64_t>(1, (int64_t{1} << 22) / (items * kv_heads)));
-  const int64_t steps = std::max<int64_t>(1, ceil_div(keys, kStep)), blocks = items * kv_heads * p.row_tiles;
+  const int64_t blocks = items * kv_heads * p.row_tiles;
   *round = p.ws ? kWaves * p.pk : D == 256 ? 1 : 2;
   p.splits = std::max<int64_t>(1, std::min(fill / blocks, steps / std::max(kLeastSteps, *round)));
   p.blocks = blocks * p.splits;
