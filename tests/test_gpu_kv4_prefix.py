@@ -294,3 +294,64 @@ def test_no_queries_another_stream_and_a_replayed_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
         b.check(got, q=q.cpu())
+
+
+def long_table(b):
+    """A table and a hint by which prefixes could be long: the kernel for many rows is chosen by what they allow."""
+    return dict(table=torch.nn.functional.pad(b.table, (0, 20000 // (b.cache.shape[2])), value=-1), max_prefix=10 ** 9)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+def test_many_rows_of_prefixes_that_may_be_long(dtype, D, group):
+    """Chunks of few rounds, one round and half a round, of one row tile and of several."""
+    note(f"kv4_prefix_attention, many rows of long prefixes, D={D} group={group} {dtype}")
+    b = Groups(D - group, dtype, D, group, 32, 4, 1, [(1000, [1 + 3 * i for i in range(37)]), (333, [20] * 2), (95, [1] * 26),
+                                                      (170, [2] * 90), (0, [5]), (40, [])], after=[9])
+    b.check(b.run(**long_table(b)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+@pytest.mark.parametrize("page", [16, 256])
+def test_many_rows_of_long_chunks(dtype, D, group, page):
+    """So many groups, all but one empty, that a prefix is one chunk: its pages are read in several batches."""
+    note(f"kv4_prefix_attention, long chunks, D={D} group={group} page={page} {dtype}")
+    b = Groups(D + group, dtype, D, group, page, 4, 1, [(2700, [3] * 25)] + [(16, [])] * 300)
+    b.check(b.run())
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (128, 128), (256, 32)])
+def test_several_queries_of_a_sequence_after_a_prefix_that_may_be_long(D, group):
+    note(f"kv4_prefix_attention, several queries, long, D={D} group={group}")
+    plan = [(200, [3, 40, 12, 5, None]), (97, [60, 1])]
+    b = Groups(D + group, F16, D, group, 32, 6, 2, plan, queries=[3, 5, 0, 9, 0, 60, 2])
+    b.check(b.run(**long_table(b)))
+
+
+def test_a_query_that_is_not_finite_among_many():
+    for dtype in (BF16, F16):
+        b = Groups(9, dtype, 128, 64, 32, 4, 1, [(256, [5] * 40), (64, [9])])
+        q = b.q.clone()
+        q[1, 2, 7], q[2, 0, 100], q[3, 1, 3] = math.inf, math.nan, -math.inf
+        rows = np.ones(q.shape[:2], bool)
+        rows[1, 2] = rows[2, 0] = rows[3, 1] = False
+        out, lse = b.run(q=q, **long_table(b))
+        b.check((out, lse), q=torch.where(q.isfinite(), q, 0), rows=rows)
+        assert out[2, 0].isnan().all() and lse[2, 0].isnan()
+
+
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (256, 128)])
+@pytest.mark.parametrize("many", [False, True], ids=["few", "many"])
+def test_pages_that_the_table_does_not_name(D, group, many):
+    """Keys of a page outside of the cache are left out, in the prefix for the whole group."""
+    b = Groups(14, F16, D, group, 32, 4, 1, [(400, [7] * (40 if many else 3)), (64, [9])])
+    members = 40 if many else 3
+    kept = np.ones(407, bool)
+    for column, name in ((0, -1), (5, b.cache.shape[0]), (6, 2 ** 31 - 1), (11, -2 ** 31)):
+        b.table[:members, column] = name
+        kept[32 * column:32 * column + 32] = False
+    for s in range(members):
+        b.k[s], b.v[s], b.sk[s], b.sv[s] = (x[s][kept] for x in (b.k, b.v, b.sk, b.sv))
+        b.lens[s] = int(kept.sum())
+    b.check(b.run(**(long_table(b) if many else {})))
