@@ -20,6 +20,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
+from .kv_beams import KvBeams
 from .kv_pages import KvPages
 
 __all__ = [
@@ -32,7 +33,7 @@ __all__ = [
     "fp8_quantize", "fp8_gemm", "fp8_w8a8_gemm",
     "llm_int8_outliers", "llm_int8_workspace_bytes", "llm_int8_gemm", "awq_workspace_bytes", "awq_search", "stream_read",
     "kv4_cache", "kv4_page_bytes", "kv4_append", "kv4_read", "kv4_copy_pages", "kv4_attention_workspace_bytes",
-    "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope", "KvPages",
+    "kv4_attention", "rope_frequencies", "rope_table", "qk_norm_rope", "KvPages", "KvBeams",
     "kv4_prefix_attention_workspace_bytes", "kv4_prefix_attention", "kv4_rope_append", "beam_select_workspace_bytes", "beam_select", "kv4_beam_reorder",
 ]
 

@@ -33,6 +33,7 @@ class KvPages:
         self._length: Dict[int, int] = {}
         self._gone: Dict[int, Dict[int, Tuple[int, int]]] = {}     # by window: the tokens that it let go, first and end
         self._next = 0
+        self._beams = 0                                            # KvBeams that hold pages too
 
     @property
     def free_pages(self) -> int:
@@ -145,7 +146,9 @@ class KvPages:
 
     def compact(self) -> Tuple[torch.Tensor, torch.Tensor]:
         """Move the pages in use to the lowest ids.  Returns (src, dst), int64, to copy before the next append or
-        attention; no page is both."""
+        attention; no page is both.  ValueError while there are KvBeams, whose tables are on the device."""
+        if self._beams:
+            raise ValueError("beams hold pages that cannot be moved")
         used = self.pages - len(self._free)
         to = sorted(page for page in self._free if page < used)
         move = dict(zip((page for page in range(used, self.pages) if self._users[page]), to))
@@ -168,6 +171,27 @@ class KvPages:
         rows = [self._held[s] + [-1] * (width - len(self._held[s])) for s in seqs]
         return (torch.tensor(rows, dtype=torch.int32).reshape(len(seqs), width),
                 torch.tensor([self._length[s] for s in seqs], dtype=torch.int32))
+
+    def shared(self, seqs: Sequence[int]) -> Tuple[torch.Tensor, torch.Tensor]:
+        """(groups int32 [n + 1], prefix int32 [n]) of ``kv4_prefix_attention``: of the sequences in their order, runs
+        that begin in the same page, and the tokens in the pages that all of a run have in common."""
+        seqs = list(seqs)
+        self._check(seqs, distinct=False)
+        starts, prefix = [], []
+        for i, seq in enumerate(seqs):
+            held, last = self._held[seq], self._held[seqs[i - 1]] if i else []
+            if held and last and held[0] == last[0] >= 0:
+                same = 0
+                while same < min(len(held), prefix[-1] // self.page) and held[same] == last[same]:
+                    same += 1
+                prefix[-1] = min(prefix[-1], same * self.page)
+            else:
+                starts.append(i)
+                prefix.append(len(held) * self.page)
+        for i, start in enumerate(starts):
+            run = seqs[start:(starts + [len(seqs)])[i + 1]]
+            prefix[i] = min([prefix[i]] + [self._length[s] for s in run])
+        return torch.tensor(starts + [len(seqs)], dtype=torch.int32), torch.tensor(prefix, dtype=torch.int32)
 
     def _check(self, seqs, distinct: bool = True) -> None:
         for seq in seqs:

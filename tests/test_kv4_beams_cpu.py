@@ -225,3 +225,161 @@ def test_prefix_attention_checks():
     raises(lambda: f(q, cache, table, ctx, groups, prefix, cu_q=t(4, i32)), "cu_q has shape")
     raises(lambda: f(q, cache, table, ctx, groups, prefix, out=t((4, 8, 64), bf16)), "out has shape")
     raises(lambda: f(q, cache, table, ctx, groups, prefix), "device tensors")
+
+
+# ---------------------------------------------------------------------------
+# Which pages hold which beam's tokens.
+# ---------------------------------------------------------------------------
+class Store:
+    """A cache of one integer a slot, moved as kv4_copy_pages and kv4_beam_reorder move theirs."""
+
+    def __init__(self, pages, page):
+        self.k, self.page, self.cells = qmm.KvPages(pages, page), page, torch.full((pages, page), -7)
+
+    def prompt(self, n, g):
+        s = self.k.add()
+        slots, _, _ = self.k.extend([s], [n])
+        tokens = torch.randint(0, 10 ** 6, (n,), generator=g)
+        self.cells.view(-1)[slots] = tokens
+        return s, tokens.tolist()
+
+    def reorder(self, table, context, tails, parents):
+        new, cells = table.clone(), self.cells.clone()
+        for slot in range(len(table)):
+            src = slot // parents.shape[1] * parents.shape[1] + int(parents.view(-1)[slot])
+            new[slot] = table[src]
+            column, filled = divmod(int(context[src]), self.page)
+            if filled and src != slot:
+                spare = tails[slot, 1] if table[slot, column] == tails[slot, 0] else tails[slot, 0]
+                cells[spare, :filled] = self.cells[table[src, column], :filled]
+                new[slot, column] = spare
+        self.cells = cells
+        return new
+
+    def read(self, table, slot, n):
+        j = torch.arange(n)
+        return self.cells[table[slot, j // self.page].long(), j % self.page].tolist()
+
+
+@pytest.mark.parametrize("page", [1, 4, 16])
+@pytest.mark.parametrize("beams", [1, 2, 5])
+def test_beams_hold_their_tokens(page, beams):
+    g = torch.Generator().manual_seed(100 * page + beams)
+    m = Store(600, page)
+    prompts = [m.prompt(n, g) for n in (3 * page + 1, 2 * page, 7, 0)]
+    free = m.k.free_pages
+    b = qmm.KvBeams(m.k, [s for s, _ in prompts], beams, 40)
+    assert b.groups.tolist() == list(range(0, 4 * beams + 1, beams)) and b.prefix.tolist() == [len(t) for _, t in prompts]
+    m.cells[b.dst] = m.cells[b.src]
+    table, context, tails = b.table, b.context, b.tails
+    want = [list(t) for _, t in prompts for _ in range(beams)]
+    for step in range(40):
+        if step == 5:
+            m.k.free(prompts[0][0])                          # the beams hold what they need
+        if step == 7:
+            slots, src, dst = m.k.extend([prompts[2][0]], [3])
+            m.cells[dst] = m.cells[src]
+            m.cells.view(-1)[slots] = -9                     # a prompt goes on by itself
+        grown = b.room(table)
+        assert (grown is not None) == bool((context % page == 0).any())
+        if grown is not None:
+            table, tails = grown
+        at = torch.arange(len(table))
+        slots = table[at, (context // page).long()].long() * page + context % page
+        assert len(set(slots.tolist())) == len(slots)
+        new = torch.randint(0, 10 ** 6, slots.shape, generator=g)
+        m.cells.view(-1)[slots] = new
+        want = [w + [int(x)] for w, x in zip(want, new)]
+        context = context + 1
+        parents = torch.randint(0, beams, (4, beams), generator=g)
+        table = m.reorder(table, context, tails, parents)
+        want = [want[i // beams * beams + int(parents.view(-1)[i])] for i in range(len(want))]
+        want = [list(w) for w in want]
+        for slot, w in enumerate(want):
+            assert m.read(table, slot, len(w)) == w
+    assert m.read(m.k.table([prompts[2][0]])[0], 0, 10) == prompts[2][1] + [-9] * 3
+    with pytest.raises(ValueError, match="no room"):
+        b.room(table)
+    with pytest.raises(ValueError, match="cannot be moved"):
+        m.k.compact()
+    kept = [(b.keep(table, slot), want[slot]) for slot in (0, len(table) - 1)]
+    b.free()
+    for seq, w in kept:
+        row, n = m.k.table([seq])
+        assert m.read(row, 0, int(n)) == w
+        m.k.free(seq)
+    for s, _ in prompts[1:]:
+        m.k.free(s)
+    assert m.k.free_pages == 600
+    m.k.compact()
+    for f in (lambda: b.room(table), lambda: b.keep(table, 0), b.free):
+        raises(f, "were freed")
+
+
+def test_beams_need_few_pages():
+    """The pages in use never exceed the prompt's, those that the beams' histories can hold and two a slot."""
+    m = Store(200, 4)
+    s, _ = m.prompt(20, torch.Generator().manual_seed(0))
+    b = qmm.KvBeams(m.k, [s], 3, 100)
+    table, context, tails = b.table, b.context, b.tails
+    for step in range(100):
+        grown = b.room(table)
+        if grown is not None:
+            table, tails = grown
+        context = context + 1
+        table = m.reorder(table, context, tails, torch.zeros((1, 3), dtype=i64))      # all go on from the first
+        assert 200 - m.k.free_pages <= 5 + step // 4 + 3 + 6
+    b.free()
+
+
+def test_beams_refusals():
+    m = Store(20, 4)
+    s, _ = m.prompt(10, torch.Generator().manual_seed(0))
+    for f, match in [(lambda: qmm.KvBeams(m.k, [], 2, 5), "needs sequences"), (lambda: qmm.KvBeams(m.k, [s], 0, 5), "needs sequences"),
+                     (lambda: qmm.KvBeams(m.k, [s], 2, -1), "needs sequences"), (lambda: qmm.KvBeams(m.k, [s, s], 2, 5), "twice"),
+                     (lambda: qmm.KvBeams(m.k, [s + 1], 2, 5), "no sequence")]:
+        raises(f, match)
+    with pytest.raises(RuntimeError, match="18 needed, 17 of 20 free"):
+        qmm.KvBeams(m.k, [s], 9, 5)
+    assert m.k.free_pages == 17
+    b = qmm.KvBeams(m.k, [s], 5, 20)
+    assert m.k.free_pages == 7
+    raises(lambda: b.room(b.table[:4]), "shape")
+    raises(lambda: b.keep(b.table, 5), "no slot")
+    strange = b.table.clone()
+    strange[0, 0] = 19
+    raises(lambda: b.keep(strange, 0), "does not hold")
+    assert b.room(b.table) is None and b.room(b.table) is None         # tokens 10 and 11
+    raises(lambda: b.room(strange), "does not hold")
+    with pytest.raises(RuntimeError, match="out of pages: 10 needed"):
+        other = m.k.add()
+        m.k.extend([other], [20])
+        b.room(b.table)
+    m.k.free(other)
+    table, tails = b.room(b.table)
+    assert sorted(tails.flatten().tolist()) == sorted(set(tails.flatten().tolist())) and (table[:, 3] == tails[:, 0]).all()
+    w = m.k.add()
+    m.k.extend([w], [8])
+    m.k.forget(w, 1)
+    m.k.shrink(w, 8)
+    with pytest.raises(ValueError):
+        qmm.KvBeams(m.k, [w, 99], 1, 1)
+
+
+def test_runs_of_sequences_that_share_pages():
+    k = qmm.KvPages(50, 4)
+    a = k.add()
+    k.extend([a], [13])
+    forks = [k.fork(a) for _ in range(3)]
+    k.extend([forks[0]], [5])
+    b, empty = k.add(), k.add()
+    k.extend([b], [9])
+    c = k.fork(b)
+    groups, prefix = k.shared([a, *forks, b, empty, c, b])
+    assert groups.tolist() == [0, 4, 5, 6, 8] and prefix.tolist() == [12, 9, 0, 9]
+    assert groups.dtype == prefix.dtype == i32
+    k.shrink(forks[1], 6)                                    # in the middle of the second page
+    assert k.shared([a, forks[1], forks[0]])[1].tolist() == [7]
+    assert k.shared([a, a])[1].tolist() == [13]
+    assert [t.tolist() for t in k.shared([])] == [[0], []]
+    raises(lambda: k.shared([99]), "no sequence")
