@@ -74,11 +74,18 @@ void launch_prefix(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& 
     else if (g == 64) launch_parts<DT, 256, 64>(a, prefix, own, together, s);
     else launch_parts<DT, 256, 128>(a, prefix, own, together, s);
   }
-  const dim3 grid(static_cast<unsigned>(own.max_q < 1024 ? own.max_q : 1024), static_cast<unsigned>(a.q_heads),
-                  static_cast<unsigned>(a.seqs));
-  if (D == 64) attention_join_parts_kernel<DT, 64><<<grid, 256, 0, s>>>(a);
-  else if (D == 128) attention_join_parts_kernel<DT, 128><<<grid, 256, 0, s>>>(a);
-  else attention_join_parts_kernel<DT, 256><<<grid, 256, 0, s>>>(a);
+  const unsigned queries = static_cast<unsigned>(own.max_q < 1024 ? own.max_q : 1024), seqs = static_cast<unsigned>(a.seqs);
+  if (static_cast<int64_t>(a.T) * a.q_heads >= 8 * device_cus()) {
+    const dim3 grid(queries, static_cast<unsigned>(ceil_div(a.q_heads, kWaves)), seqs);
+    if (D == 64) attention_join_rows_kernel<DT, 64><<<grid, 256, 0, s>>>(a);
+    else if (D == 128) attention_join_rows_kernel<DT, 128><<<grid, 256, 0, s>>>(a);
+    else attention_join_rows_kernel<DT, 256><<<grid, 256, 0, s>>>(a);
+  } else {
+    const dim3 grid(queries, static_cast<unsigned>(a.q_heads), seqs);
+    if (D == 64) attention_join_parts_kernel<DT, 64><<<grid, 256, 0, s>>>(a);
+    else if (D == 128) attention_join_parts_kernel<DT, 128><<<grid, 256, 0, s>>>(a);
+    else attention_join_parts_kernel<DT, 256><<<grid, 256, 0, s>>>(a);
+  }
 }
 
 }  // namespace

@@ -355,3 +355,11 @@ def test_pages_that_the_table_does_not_name(D, group, many):
         b.k[s], b.v[s], b.sk[s], b.sv[s] = (x[s][kept] for x in (b.k, b.v, b.sk, b.sv))
         b.lens[s] = int(kept.sum())
     b.check(b.run(**(long_table(b) if many else {})))
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+def test_rows_enough_for_a_wavefront_each(D, group):
+    """In the join: heads that do not fill its blocks, sequences without and with a prefix, of one chunk and of several."""
+    b = Groups(15, BF16, D, group, 16, 15, 5, [(100, [3] * 40), (64, [400, 1]), (600, [2] * 60), (48, [None, -5])] + [(16, [1])] * 70, before=[1, 300])
+    assert b.q.shape[0] * 15 >= 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    b.check(b.run())
