@@ -720,8 +720,14 @@ int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_h
  * workspace : kv4_prefix_attention_workspace_bytes bytes with the same
  *           arguments (max_context = table_width * page), 16-byte aligned, no
  *           clearing needed.
- * The other arguments, limits and the arithmetic are kv4_attention's; up to
- * 65535 groups, and groups * kv_heads below 2^24.
+ * The other arguments, limits and the arithmetic are kv4_attention's, but that a
+ * long prefix of a group of more than 96 rows (queries times the heads that
+ * share a kv head) is taken with each value, (c - z) times its scale, rounded to
+ * binary16 (2^-11; a step of 2^-20 below 2^-10) instead of the products of
+ * probabilities and scales, and with bf16 queries brought into binary16's range
+ * by one power of two for up to 256 rows.  Which kernels run is chosen by the
+ * hints; results differ by these roundings and do not depend on timing.  Up to
+ * 65535 groups, and the blocks of a launch below 2^24.
  * ------------------------------------------------------------------------- */
 size_t kv4_prefix_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t n_groups,
                                             int64_t max_group, int64_t max_prefix, int64_t max_tail, int64_t q_heads,

@@ -40,7 +40,6 @@ struct Chunk {
   static constexpr int kVScales = kVOps * kVStride;         // binary16 [group][key]
   static constexpr int kVBuffer = kVScales + kG * kKeys * 2;
   static_assert(kKBuffer % 16 == 0 && kVBuffer % 16 == 0, "alignment");
-  static constexpr int kLds = 2 * kKBuffer + 2 * kVBuffer;
   // what a lane expands of a round: kWords words of a key's codes; of a word of two quads of values kNibbles
   // nibbles of either its low or its high half (kShare lanes a word)
   static constexpr int kWords = kKeys * D / (512 * kWaves), kKeyWaves = D / (32 * kWords);

@@ -1,6 +1,13 @@
 // kv4_prefix.hip -- entry points of the attention of a batch in groups that share
 // a prefix: argument checks and the launch plan (kernels: kv4_attention.h,
-// kv4_attention_chunk.h).
+// kv4_attention_chunk.h for own parts, kv4_attention_rows.h for prefixes).
+//
+// A prefix is a part of its own: attended to once for a group with all of its
+// rows, which turns loads and expansions of codes per sequence into matrix
+// products, and joined with each sequence's own part by log-sum-exp in fp32.
+// Two launches where both parts take the kernel for few rows, else three.  24
+// questions on each of two documents of 100000 tokens (64/8 heads of 128) 240
+// us, 4 beams after 1000 tokens (32/8) 13.5.
 
 #include <algorithm>
 
@@ -21,12 +28,13 @@ AttnPlan part_plan(bool prefix, int64_t items, int64_t rows, int64_t kv_heads, i
   AttnPlan p{};
   const int d = static_cast<int>(D);
   const int64_t steps = std::max<int64_t>(1, ceil_div(keys, kStep));
-  // The kernel for many rows starts later and leaves more to join: prefixes of few
-  // steps (of 16 rows, for each of the blocks at once) stay with the kernel for few.
-  // 256 rows after 4096 tokens in 8 heads of 128 (32 steps) 48 us by rows, 41 here;
-  // 8192 tokens 52.5 both; 12288 56 against 64.  216 rows of 12 prefixes of 1500
-  // tokens in 2 heads of 64 (31) 45 against 49; 256 rows of 256 after 2048 (16) 58 against 53.
-  const int64_t short_of = (D == 64 ? 16 : 32) * 2 * device_cus();
+  // The kernel for many rows starts later, leaves more to join and shares no launch
+  // with the own parts: prefixes of few steps (of 16 rows, for each of the blocks
+  // at once) stay with the kernel for few.  256 rows in 8 heads of 128 after 4096
+  // tokens (32 steps) 48 us by rows, 30 here; 8192 50 and 40; 12288 54 and 52;
+  // 16384 59 and 64.  216 rows of 12 prefixes in 2 heads of 64 after 1500 tokens (31)
+  // 40 and 30; 3000 42.5 and 44.  256 rows of 256 after 4096 (32) 62 and 54; 8192 73 both.
+  const int64_t short_of = (D == 128 ? 96 : 48) * 2 * device_cus();
   p.ws = rows <= 96 || (prefix && items * kv_heads * ceil_div(rows, 16) * steps <= short_of);
   const int64_t fill = (p.ws || !prefix ? 2 : 1) * device_cus();
   const bool eights = rows <= 8;
@@ -57,17 +65,13 @@ Plans plans_of(int64_t seqs, int64_t max_q, int64_t n_groups, int64_t max_group,
   p.prefix = part_plan(true, n_groups, rows, kv_heads, D, group, std::min(max_prefix, tokens), &p.p_round);
   p.own = part_plan(false, seqs, max_q * ratio, kv_heads, D, group, std::min(max_tail, tokens), &p.round);
   p.own.max_q = max_q;
-  // Where the blocks of both are resident at once a launch less counts for more
-  // than the own parts' best kernel: 4 beams after 1000 tokens 21 us in two, 14 in one.
-  if (p.prefix.ws && p.own.ws && p.prefix.nt == 1) {
-    int64_t round;
-    AttnPlan own = part_plan(false, seqs, max_q * ratio, kv_heads, D, group, std::min(max_tail, tokens), &round, p.prefix.pk);
-    if (p.prefix.blocks + own.blocks <= 2 * device_cus()) {
-      own.max_q = max_q;
-      p.own = own;
-      p.round = round;
-      p.together = true;
-    }
+  // Kernels of few rows run in one launch, the own parts by the prefix's number of
+  // steps at once: 4 beams after 1000 tokens 21 us in two launches, 13.5 in one; 64
+  // samples after 4096 tokens 39 and 30; 30000 tokens of 4 beams 32 and 24.
+  if (p.prefix.ws && p.own.ws) {
+    p.own = part_plan(false, seqs, max_q * ratio, kv_heads, D, group, std::min(max_tail, tokens), &p.round, p.prefix.pk);
+    p.own.max_q = max_q;
+    p.together = true;
   }
   return p;
 }
@@ -121,7 +125,7 @@ extern "C" int kv4_prefix_attention(const void* q, int64_t q_token_stride, int64
                            tokens, T);
   if (!workspace || workspace_bytes < bytes_of(p, T, q_heads, head_dim)) return QMM_EWORKSPACE;
   if (!aligned(workspace, 16)) return QMM_EALIGN;
-  if (p.prefix.blocks >= (int64_t{1} << 24) || p.own.blocks >= (int64_t{1} << 24)) return QMM_ERANGE;
+  if (p.prefix.blocks + p.own.blocks >= (int64_t{1} << 24)) return QMM_ERANGE;
   SharedArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_ts = q_token_stride;

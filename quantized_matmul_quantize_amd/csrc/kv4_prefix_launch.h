@@ -14,14 +14,16 @@ __global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, NT)) void at
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, NT>::kWaveBytes];
   attention_block<DT, D, GROUP, PK, NT, PART>(a, blockIdx.x, lds);
 }
-// (a type of its own: the host's pass compiles no device function for two kernels)
+// (types of their own: the host's pass compiles no device function for two kernels)
+template <int NT>
 struct BothArgs : SharedArgs {
   uint32_t prefix_blocks;
 };
-template <int DT, int D, int GROUP, int PK>
-__global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, 1)) void attention_both_kernel(BothArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, 1>::kWaveBytes];
-  if (blockIdx.x < a.prefix_blocks) attention_block<DT, D, GROUP, PK, 1, kPrefix>(a, blockIdx.x, lds);
+template <int DT, int D, int GROUP, int PK, int NT>
+__global__ __launch_bounds__(256, attention_occupancy(D, GROUP, PK, NT)) void attention_both_kernel(BothArgs<NT> a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * Shape<D, GROUP, PK, NT>::kWaveBytes];
+  static_assert(Shape<D, GROUP, PK, 1>::kWaveBytes <= Shape<D, GROUP, PK, NT>::kWaveBytes, "the own parts' memory");
+  if (blockIdx.x < a.prefix_blocks) attention_block<DT, D, GROUP, PK, NT, kPrefix>(a, blockIdx.x, lds);
   else attention_block<DT, D, GROUP, PK, 1, kOwn>(a, blockIdx.x - a.prefix_blocks, lds);
 }
 template <int DT, int D, int GROUP, int NT>
@@ -39,7 +41,8 @@ void launch_part(const SharedArgs& a, const AttnPlan& p, hipStream_t s) {
     if constexpr (PART == kPrefix) attention_rows_kernel<DT, D, GROUP><<<grid, Rows<D, GROUP>::kThreads, 0, s>>>(a);
     else attention_own_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP)><<<grid, 256, 0, s>>>(a);
   } else if (p.pk == 2) {
-    if constexpr (attention_pairs(D, GROUP)) attention_part_kernel<DT, D, GROUP, 2, 1, PART><<<grid, 256, 0, s>>>(a);
+    // (a prefix of up to 8 rows has own parts of as few: both are in one launch)
+    if constexpr (PART == kOwn && attention_pairs(D, GROUP)) attention_part_kernel<DT, D, GROUP, 2, 1, PART><<<grid, 256, 0, s>>>(a);
   } else if (p.nt == 1) {
     attention_part_kernel<DT, D, GROUP, 1, 1, PART><<<grid, 256, 0, s>>>(a);
   } else {
@@ -50,9 +53,15 @@ template <int DT, int D, int GROUP>
 void launch_parts(const SharedArgs& a, const AttnPlan& prefix, const AttnPlan& own, bool together, hipStream_t s) {
   if (together) {
     const dim3 grid(static_cast<unsigned>(prefix.blocks + own.blocks));
-    const BothArgs both{a, static_cast<uint32_t>(prefix.blocks)};
-    if (prefix.pk == 1) attention_both_kernel<DT, D, GROUP, 1><<<grid, 256, 0, s>>>(both);
-    else if constexpr (attention_pairs(D, GROUP)) attention_both_kernel<DT, D, GROUP, 2><<<grid, 256, 0, s>>>(both);
+    const uint32_t first = static_cast<uint32_t>(prefix.blocks);
+    constexpr int kTiles = attention_tiles(D, GROUP);
+    if (prefix.pk == 2) {
+      if constexpr (attention_pairs(D, GROUP)) attention_both_kernel<DT, D, GROUP, 2, 1><<<grid, 256, 0, s>>>({a, first});
+    } else if (prefix.nt == 1) {
+      attention_both_kernel<DT, D, GROUP, 1, 1><<<grid, 256, 0, s>>>({a, first});
+    } else {
+      attention_both_kernel<DT, D, GROUP, 1, kTiles><<<grid, 256, 0, s>>>({a, first});
+    }
     return;
   }
   launch_part<DT, D, GROUP, kPrefix>(a, prefix, s);
