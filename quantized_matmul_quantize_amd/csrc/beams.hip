@@ -232,6 +232,10 @@ struct Logits<QMM_F16> {
 // candidates that are nearly as good are told apart by their rows' sums.
 //   Where values equal to the bound, or sorted ones, are more than LDS has room
 // for, or a NaN is met (the sum has taken it), the k largest are found one by one.
+//   64 x 8 rows of 131072 bf16 logits 43 us, 3.1 TB/s: bound by vector operations,
+// about ten a logit (unpacking, maximum, exponential at a quarter of the rate, sum,
+// comparison).  With 64 bytes of logits a thread the call took 67 us instead of
+// 60.6: its searches come twice as often.
 template <int DT>
 __global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
   using L = Logits<DT>;
@@ -450,6 +454,8 @@ __global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
 
 // A block joins the rows of a sequence: each beam's log sum, then the k best of
 // the blocks' candidates, 2048 at a time, by the same bound.  Values are fp64.
+// One block to a sequence: 64 x 8 rows 14.6 us, a chain of loads, searches and
+// barriers; their fp32 keys bound first (32 steps of a search, not 64) 18 -> 14.6.
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinPer = 4;
 constexpr int kJoinRoom = kJoinWaves * kMostK * kJoinPer + kMostK;     // (as room_of, and the ones kept)
 
