@@ -15,6 +15,9 @@
 // Values are expanded with their scales: (c - z) / 16 is exact, its product with
 // the scale is rounded to binary16 (2^-11; below 2^-14 a step of 2^-24, 2^-20 of
 // a value), and no scale overflows; probabilities are rounded once to binary16.
+// Beside bf16 results that is little.  For binary16 ones what the rounding left, 5
+// bits, is a second operand, and a value exact down to that step: with one of
+// them 216 rows of 12 prefixes of 6000 tokens were 3.3e-4 off, 2.8e-4 with both.
 // So nothing is left per score and group but one operation with the key's scale.
 //
 // Why so: two documents of 100000 tokens, 192 rows, D 128 in groups of 64.  Codes
@@ -41,8 +44,9 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-template <int D, int GROUP>
+template <int DT, int D, int GROUP>
 struct Rows {
+  static constexpr int kParts = DT == QMM_F16 ? 2 : 1;       // operands of a value
   static constexpr int kG = D / GROUP;
   static constexpr int kW = D == 256 ? 4 : 8;                // wavefronts: by the registers of sums and queries
   static constexpr int kThreads = kWave * kW;
@@ -50,18 +54,18 @@ struct Rows {
   static constexpr int kKeys = 8 * kW, kTiles = kKeys / 32;  // of a round
   static constexpr int kSteps = D / 16, kChannels = D / 32;
   // Operands of 1 KiB, [tile][k-extent] of keys, [tile][32 channels][16 keys] of
-  // values, each in two halves of 544 bytes: writers' eight lanes at a time then
+  // values (twice for two parts), each in two halves of 544 bytes: writers' eight lanes at a time then
   // meet every bank once, as readers' do.  Two buffers of each.
   static constexpr int kHalf = 544;
   static constexpr int kKOps = kTiles * kSteps * 2 * kHalf;
   static constexpr int kKBuffer = kKOps + kG * kKeys * 4;    // fp32 scales [group][key]
-  static constexpr int kVBuffer = kTiles * kChannels * 2 * 2 * kHalf;
+  static constexpr int kVPart = kTiles * kChannels * 2 * 2 * kHalf, kVBuffer = kParts * kVPart;
   // Codes as they lie in memory, kRing rounds: a round of few rows takes less
   // than memory does to answer.  Of each 16-key tile codes, then params [group][16].
-  static constexpr int kRing = 6;
   static constexpr int kCodes = 8 * D, kParams = 64 * kG;    // of a tile
   static constexpr int kRaw = kKeys / 16 * (kCodes + kParams);
   static constexpr int kSlot = 2 * kRaw;                     // keys, values
+  static constexpr int kFit = (163840 - kW * kWave * 4 - 2 * (kKBuffer + kVBuffer)) / kSlot, kRing = kFit < 6 ? kFit : 6;
   static constexpr int kPagesAt = 2 * (kKBuffer + kVBuffer) + kRing * kSlot;      // a wavefront's next 64 pages
   static constexpr int kLds = kPagesAt + kW * kWave * 4;
   static constexpr int kLoads = kCodes / 1024 > 1 ? 3 : 2;   // of a wavefront a round
@@ -82,7 +86,7 @@ __device__ __forceinline__ void each(F&& f) {
 
 template <int DT, int D, int GROUP>
 __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32_t id, uint8_t* lds) {
-  using L = Rows<D, GROUP>;
+  using L = Rows<DT, D, GROUP>;
   constexpr int G = L::kG, KEYS = L::kKeys, T = L::kTiles, kSteps = L::kSteps, kCh = L::kChannels, kW = L::kW;
   constexpr int kWords = L::kWords, kGSteps = GROUP / 16;
   constexpr int kAhead = 4;                        // operands read before they are used
@@ -235,11 +239,19 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
       return;
     }
     const int y = piece - 1;
-    u32x4 v;
+    u32x4 v, rest;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = times(plus((__builtin_rotateright32(vw[e], 4 * y) & Codes64::mask) | magic_v, vz[e]), vs[e]);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t n = plus((__builtin_rotateright32(vw[e], 4 * y) & Codes64::mask) | magic_v, vz[e]);
+      const uint32_t most = times(n, vs[e]);       // (a cast of v[e] in place would be one of v[0])
+      v[e] = most;
+      if constexpr (L::kParts == 2)
+        rest[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, n), __builtin_bit_cast(f16x2_t, vs[e]),
+                                                                         -__builtin_bit_cast(f16x2_t, most)));
+    }
     const int row = 8 * (v_word & 3) + 2 * (v_first + y) + v_part;
     *reinterpret_cast<u32x4*>(buf + v_to + value_row(row) * 16) = v;
+    if constexpr (L::kParts == 2) *reinterpret_cast<u32x4*>(buf + L::kVPart + v_to + value_row(row) * 16) = rest;
   };
   // Only LDS is shared, and the codes on their way are waited for in their turn.
   auto meet = [&] {
@@ -327,14 +339,17 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
     // instructions, scales a unit before their use: a wait for a read just sent
     // waits for all before it.
     constexpr bool kHalves = kW == 8;
-    constexpr int kV = 2 * T * kCh, kN = kV + T * kSteps, kUnits = T * G;
+    constexpr int kV = L::kParts * 2 * T * kCh, kN = kV + T * kSteps, kUnits = T * G;
+    auto read_v = [&](const uint8_t* vb, int i) {
+      const int c = i % kCh, m = i / kCh % (2 * T);           // m: 16 keys
+      return *reinterpret_cast<const u32x4*>(vb + i / (2 * T * kCh) * L::kVPart +
+                                             (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
+    };
     auto matrices = [&](int round) {
       const uint8_t* vb = v_lds(round + 1);
       const uint8_t* kb = k_lds(round);
       auto read = [&](int i) {
-        const int c = i % kCh, m = i / kCh;                   // m: 16 keys
-        return i < kV ? *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16)
-                      : *reinterpret_cast<const u32x4*>(kb + ((i - kV) * 2 + h) * L::kHalf + 16 * r);
+        return i < kV ? read_v(vb, i) : *reinterpret_cast<const u32x4*>(kb + ((i - kV) * 2 + h) * L::kHalf + 16 * r);
       };
       u32x4 ops[kAhead];
 #pragma unroll
@@ -352,7 +367,7 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
         constexpr int i = index;
         const u32x4 op = ops[i % kAhead];
         if constexpr (i < kV) {
-          o[i % kCh] = mfma32(op, p[i / kCh / 2][i / kCh % 2], o[i % kCh]);
+          o[i % kCh] = mfma32(op, p[i / kCh % (2 * T) / 2][i / kCh % 2], o[i % kCh]);
           if constexpr (i + kAhead < kN) ops[i % kAhead] = read(i + kAhead);
           if constexpr (!kHalves) {
             constexpr int first = i * 2 * kPieces / kV, last = (i + 1) * 2 * kPieces / kV;
@@ -464,9 +479,7 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
       const uint8_t* vb = v_lds(rounds - 1);
 #pragma unroll
       for (int i = 0; i < kV; ++i) {
-        const int c = i % kCh, m = i / kCh;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(vb + (((m / 2 * kCh + c) * 2 + m % 2) * 2 + h) * L::kHalf + value_row(r) * 16);
-        o[c] = mfma32(v, p[m / 2][m % 2], o[c]);
+        o[i % kCh] = mfma32(read_v(vb, i), p[i / kCh % (2 * T) / 2][i / kCh % 2], o[i % kCh]);
       }
     }
 
@@ -488,8 +501,8 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
 }
 
 template <int DT, int D, int GROUP>
-__global__ __launch_bounds__((Rows<D, GROUP>::kThreads), (Rows<D, GROUP>::kW / 4)) void attention_rows_kernel(SharedArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Rows<D, GROUP>::kLds];
+__global__ __launch_bounds__((Rows<DT, D, GROUP>::kThreads), (Rows<DT, D, GROUP>::kW / 4)) void attention_rows_kernel(SharedArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Rows<DT, D, GROUP>::kLds];
   attention_rows_block<DT, D, GROUP>(a, blockIdx.x, lds);
 }
 

@@ -38,7 +38,7 @@ void launch_part(const SharedArgs& a, const AttnPlan& p, hipStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.blocks));
   constexpr int kTiles = attention_tiles(D, GROUP);
   if (!p.ws) {
-    if constexpr (PART == kPrefix) attention_rows_kernel<DT, D, GROUP><<<grid, Rows<D, GROUP>::kThreads, 0, s>>>(a);
+    if constexpr (PART == kPrefix) attention_rows_kernel<DT, D, GROUP><<<grid, Rows<DT, D, GROUP>::kThreads, 0, s>>>(a);
     else attention_own_chunk_kernel<DT, D, GROUP, attention_chunk_tiles(D, GROUP)><<<grid, 256, 0, s>>>(a);
   } else if (p.pk == 2) {
     // (a prefix of up to 8 rows has own parts of as few: both are in one launch)

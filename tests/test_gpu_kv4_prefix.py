@@ -298,7 +298,7 @@ def test_no_queries_another_stream_and_a_replayed_graph():
 
 def long_table(b):
     """A table and a hint by which prefixes could be long: the kernel for many rows is chosen by what they allow."""
-    return dict(table=torch.nn.functional.pad(b.table, (0, 60000 // (b.cache.shape[2])), value=-1), max_prefix=10 ** 9)
+    return dict(table=torch.nn.functional.pad(b.table, (0, 200000 // (b.cache.shape[2])), value=-1), max_prefix=10 ** 9)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
