@@ -722,8 +722,9 @@ int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_h
  *           clearing needed.
  * The other arguments, limits and the arithmetic are kv4_attention's, but that a
  * long prefix of a group of more than 96 rows (queries times the heads that
- * share a kv head) is taken with each value, (c - z) times its scale, rounded to
- * binary16 (2^-11; a step of 2^-20 below 2^-10) instead of the products of
+ * share a kv head) is taken with each value, (c - z) times its scale, in binary16
+ * (bf16 queries: rounded, 2^-11 or a step of 2^-20 below 2^-10; fp16 ones: exact
+ * to that step) and probabilities rounded to it, instead of the products of
  * probabilities and scales, and with bf16 queries brought into binary16's range
  * by one power of two for up to 256 rows.  Which kernels run is chosen by the
  * hints; results differ by these roundings and do not depend on timing.  Up to
