@@ -125,7 +125,9 @@ extern "C" int kv4_prefix_attention(const void* q, int64_t q_token_stride, int64
                            tokens, T);
   if (!workspace || workspace_bytes < bytes_of(p, T, q_heads, head_dim)) return QMM_EWORKSPACE;
   if (!aligned(workspace, 16)) return QMM_EALIGN;
-  if (p.prefix.blocks + p.own.blocks >= (int64_t{1} << 24)) return QMM_ERANGE;
+  // (a launch holds 2^32 threads; those for many rows have up to 512 a block)
+  if (p.prefix.blocks >= int64_t{1} << (p.prefix.ws ? 24 : 23) || p.prefix.blocks + p.own.blocks >= (int64_t{1} << 24))
+    return QMM_ERANGE;
   SharedArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_ts = q_token_stride;

@@ -194,7 +194,8 @@ def test_prefix_attention_errors():
     for kw in [dict(dt=F32), dict(D=96), dict(page=8), dict(group=16)]:
         assert f(*a(**kw)) == EUNSUP, kw
     for kw in [dict(T=1 << 31, cu=P), dict(seqs=70000, T=70000), dict(n=70000), dict(width=1 << 25, stride=1 << 25),
-               dict(hq=80000, hk=8), dict(T=1 << 27, cu=P), dict(hk=4096, hq=4096, n=65535)]:
+               dict(hq=80000, hk=8), dict(T=1 << 27, cu=P), dict(hk=4096, hq=4096, n=65535),
+               dict(hk=200, hq=5000, n=65535, mg=4)]:        # (blocks of 512 threads)
         assert f(*a(**kw)) == ERANGE, kw
     for kw in [dict(q=MIS), dict(out=MIS), dict(cache=P + 8), dict(qts=4100), dict(qhs=4), dict(table=P + 2),
                dict(context=P + 1), dict(cu=P + 2), dict(groups=P + 2), dict(prefix=P + 3), dict(ws=MIS)]:
