@@ -874,8 +874,7 @@ __global__ __launch_bounds__(256) void attention_join_rows_kernel(SharedArgs a) 
       const float weight = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - m);
       l += sum_at(ml.y, ml.x, m);
       const int n = min(chunks - c0, kWave);
-#pragma unroll 8
-      for (int c = 0; c < n; c += kParts) {
+      for (int c = 0; c < n; c += kParts) {        // (eight loads at once gained nothing)
         const float f = __shfl(weight, min(c + part, kWave - 1), kWave);
         if (c + part < n) o += *reinterpret_cast<const f32x4*>(a.part_o + slot(c0 + c + part) * D + 4 * c4) * f;
       }
