@@ -7,7 +7,8 @@ have the same number of tokens.  A slot shares every page that is full and has
 two tail pages of its own, one that it fills and a spare one that a parent's
 tokens are copied to.  The host hears of the moves only when a page is full:
 then it reads the table, gives back what no beam of the sequence names any more
-and hands out two pages a slot.
+and hands out two pages a slot.  (And when a beam was kept: a page that a kept
+sequence ends in is no longer a slot's to copy to, which gets another one.)
 """
 from __future__ import annotations
 
@@ -43,6 +44,7 @@ class KvBeams:
         self.pages, self.beams, self._length, self._tokens = pages, beams, lengths, [tokens] * len(seqs)
         self._prompts: Optional[List[int]] = [pages.fork(s) for s in seqs]      # hold the pages that are full
         self._own: List[Set[int]] = [set() for _ in seqs]
+        self._kept: Set[int] = set()                    # tail pages that sequences which were kept end in
         width = max(1, max(-(-(n + tokens) // pages.page) for n in lengths))
         slots = len(seqs) * beams
         table = pages.table(self._prompts, width)[0].repeat_interleave(beams, 0)
@@ -65,8 +67,8 @@ class KvBeams:
     def room(self, table: torch.Tensor) -> Optional[Tuple[torch.Tensor, torch.Tensor]]:
         """Before the append of each step: room for one more token of every beam, in the place table[slot, context //
         page] * page + context % page.  None where the slots have it; else the (table, tails) to go on with, on the CPU,
-        made from the table as the beams were last moved (on any device: only then is it read).  RuntimeError if there
-        are not enough free pages; then nothing has changed."""
+        made from the table as the beams were last moved (on any device: only then is it read).  So also where a beam was
+        kept since the last call.  RuntimeError if there are not enough free pages; then nothing has changed."""
         self._alive()
         page, beams = self.pages.page, self.beams
         if table.shape != self.table.shape:
@@ -74,8 +76,11 @@ class KvBeams:
         if any(t <= 0 for t in self._tokens):
             raise ValueError("the beams have no room for more tokens")
         full = [i for i, n in enumerate(self._length) if n % page == 0]
+        # (a full sequence's slots get two other pages in any case)
+        taken = [(slot, t) for slot, pair in enumerate(self.tails.tolist() if self._kept else []) for t in range(2)
+                 if pair[t] in self._kept and self._length[slot // beams] % page]
         out = None
-        if full:
+        if full or taken:
             new, left, free = table.detach().to("cpu", copy=True), [], len(self.pages._free)
             for i in full:
                 named = set(new[i * beams:i * beams + beams, :self._length[i] // page].flatten().tolist())
@@ -84,8 +89,9 @@ class KvBeams:
                     raise ValueError(f"the table names pages that sequence {i} does not hold: {sorted(strange)}")
                 left.append(self._own[i] - named)
                 free += len(left[-1])
-            if 2 * beams * len(full) > free:
-                raise RuntimeError(f"out of pages: {2 * beams * len(full)} needed, {free} of {self.pages.pages} free")
+            need = 2 * beams * len(full) + len(taken)
+            if need > free:
+                raise RuntimeError(f"out of pages: {need} needed, {free} of {self.pages.pages} free")
             for i, pages in zip(full, left):
                 for p in sorted(pages, reverse=True):
                     self.pages._drop(p)
@@ -94,13 +100,17 @@ class KvBeams:
             for i in full:
                 self._hand_out(i)
                 new[i * beams:i * beams + beams, self._length[i] // page] = self.tails[i * beams:i * beams + beams, 0]
+            for slot, t in taken:
+                self._tail(slot, t)
             out = new, self.tails
+        self._kept.clear()
         self._length = [n + 1 for n in self._length]
         self._tokens = [t - 1 for t in self._tokens]
         return out
 
     def keep(self, table: torch.Tensor, slot: int) -> int:
-        """A beam as a sequence of its own of the KvPages; returns its id."""
+        """A beam, with the tokens that the row table[slot] holds now, as a sequence of its own of the KvPages; returns its
+        id.  The search may go on: the page that the sequence ends in is nobody's to copy to from the next `room` on."""
         self._alive()
         if not 0 <= slot < self.table.shape[0]:
             raise ValueError(f"no slot {slot} of {self.table.shape[0]}")
@@ -114,6 +124,8 @@ class KvBeams:
         for p in row:
             if p >= 0:
                 pages._users[p] += 1
+        if self._length[i] % pages.page and row[-1] in self._own[i]:
+            self._kept.add(row[-1])
         return seq
 
     def free(self) -> None:
@@ -134,5 +146,8 @@ class KvBeams:
         """Two pages to each slot of sequence i."""
         for slot in range(i * self.beams, i * self.beams + self.beams):
             for t in range(2):
-                self.tails[slot, t] = p = self.pages._take()
-                self._own[i].add(p)
+                self._tail(slot, t)
+
+    def _tail(self, slot: int, t: int) -> None:
+        self.tails[slot, t] = page = self.pages._take()
+        self._own[slot // self.beams].add(page)

@@ -155,3 +155,25 @@ def test_the_example_runs():
                                    "--page", "16", "--group", "32", "--sequences", "3", "--beams", "4", "--prompt", "100",
                                    "--chunk", "64", "--steps", "40", "--vocabulary", "1000"])
     assert tokens.shape == (3, 4, 41) and scores.isfinite().all()
+
+
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "replayed"])
+@pytest.mark.parametrize("beams,lengths,page", [(4, [45, 32, 7], 16), (3, [100], 64)])
+def test_kept_beams_outlive_the_moves_of_their_slots(beams, lengths, page, graph):
+    """Set aside after some steps, in the middle of a page, and read again when the search is over."""
+    run, model = search(beams, 40, lengths, page=page)
+
+    def read(seq):
+        row, n = model.pages.table([seq])
+        at = torch.arange(int(n))
+        slots = (row[0, at // page].long() * page + at % page).cuda()
+        return [x for cache in model.cache for x in qmm.kv4_read(cache, slots, 64, torch.float32)]
+
+    kept = []
+    for step in range(40):
+        run.step(graph=graph)
+        if step in (2, 3, 9, 17, 30):
+            kept += [(seq, read(seq)) for seq in (run.host.keep(run.table, slot) for slot in (0, beams - 1))]
+    for seq, was in kept:
+        assert all(torch.equal(x, y) for x, y in zip(read(seq), was))
+    run.host.free()

@@ -317,6 +317,81 @@ def test_beams_hold_their_tokens(page, beams):
         raises(f, "were freed")
 
 
+@pytest.mark.parametrize("page,beams", [(4, 2), (4, 3), (16, 3), (16, 1)])
+@pytest.mark.parametrize("before", [False, True], ids=["moved", "before the move"])
+def test_a_beam_that_is_kept_stays_as_it_was(page, beams, before):
+    """Set aside in the middle of a page, while the search goes on and moves its slots; then read on by itself."""
+    g = torch.Generator().manual_seed(page + beams)
+    m = Store(900, page)
+    prompts = [m.prompt(n, g) for n in (page + 1, 2 * page, 7)]
+    b = qmm.KvBeams(m.k, [s for s, _ in prompts], beams, 8 * page)
+    m.cells[b.dst] = m.cells[b.src]
+    table, context, tails = b.table, b.context, b.tails
+    want, kept = [list(t) for _, t in prompts for _ in range(beams)], []
+    for step in range(8 * page):
+        grown = b.room(table)
+        assert grown is None or step % 3 == 1 or bool((context % page == 0).any())
+        if grown is not None:
+            table, tails = grown
+        at = torch.arange(len(table))
+        new = torch.randint(0, 10 ** 6, (len(table),), generator=g)
+        m.cells[table[at, (context // page).long()].long(), (context % page).long()] = new
+        want = [w + [int(x)] for w, x in zip(want, new)]
+        context = context + 1
+        slot = int(torch.randint(0, len(table), (), generator=g))
+        if before and step % 3 == 0:
+            kept.append((b.keep(table, slot), list(want[slot])))
+        parents = torch.randint(0, beams, (3, beams), generator=g)
+        table = m.reorder(table, context, tails, parents)
+        want = [list(want[i // beams * beams + int(parents.view(-1)[i])]) for i in range(len(want))]
+        if not before and step % 3 == 0:
+            kept += [(b.keep(table, s), list(want[s])) for s in {slot, 0}]
+        if step % 5 == 0 and kept:                           # one of them goes on by itself
+            seq, w = kept.pop(int(torch.randint(0, len(kept), (), generator=g)))
+            slots, src, dst = m.k.extend([seq], [2])
+            m.cells[dst] = m.cells[src]
+            m.cells.view(-1)[slots] = torch.tensor([-8, -9])
+            kept.append((seq, w + [-8, -9]))
+        if step % 11 == 0 and kept:
+            m.k.free(kept.pop(0)[0])
+        for seq, w in kept:
+            row, n = m.k.table([seq])
+            assert int(n) == len(w) and m.read(row, 0, len(w)) == w
+        for s, w in enumerate(want):
+            assert m.read(table, s, len(w)) == w
+        used = set(tails.flatten().tolist()) - {-1}
+        assert not used & set(m.k._free)
+    b.free()
+    for seq, w in kept:
+        row, n = m.k.table([seq])
+        assert m.read(row, 0, len(w)) == w
+        m.k.free(seq)
+    for s, _ in prompts:
+        m.k.free(s)
+    assert m.k.free_pages == 900
+
+
+def test_a_kept_beam_takes_a_page_only_where_the_search_goes_on():
+    m = Store(12, 4)
+    s, _ = m.prompt(6, torch.Generator().manual_seed(0))
+    b = qmm.KvBeams(m.k, [s], 2, 20)
+    assert m.k.free_pages == 6
+    assert b.room(b.table) is None                           # token 6: the page is not full
+    kept = [b.keep(b.table, 0), b.keep(b.table, 1), b.keep(b.table, 0)]
+    assert m.k.free_pages == 6
+    held = [m.k.table([k])[0][0, 1].item() for k in kept]
+    assert held[0] == held[2] and set(held) <= set(b.tails.flatten().tolist())
+    old = b.tails
+    table, tails = b.room(b.table)
+    assert m.k.free_pages == 4 and torch.equal(table, b.table) and not set(held) & set(tails.flatten().tolist())
+    assert torch.equal(old[:, 1], tails[:, 1]) and len(set(tails.flatten().tolist())) == 4
+    b.free()
+    assert m.k.free_pages == 12 - 2 - 2                      # the prompt's two and the kept ones' last
+    for k in kept + [s]:
+        m.k.free(k)
+    assert m.k.free_pages == 12
+
+
 def test_beams_need_few_pages():
     """The pages in use never exceed the prompt's, those that the beams' histories can hold and two a slot."""
     m = Store(200, 4)
