@@ -88,7 +88,7 @@ class KvBeams:
                 if strange:
                     raise ValueError(f"the table names pages that sequence {i} does not hold: {sorted(strange)}")
                 left.append(self._own[i] - named)
-                free += len(left[-1])
+                free += sum(self.pages._users[p] == 1 for p in left[-1])       # (others may be kept)
             need = 2 * beams * len(full) + len(taken)
             if need > free:
                 raise RuntimeError(f"out of pages: {need} needed, {free} of {self.pages.pages} free")

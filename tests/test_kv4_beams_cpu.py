@@ -392,6 +392,41 @@ def test_a_kept_beam_takes_a_page_only_where_the_search_goes_on():
     assert m.k.free_pages == 12
 
 
+@pytest.mark.parametrize("pages", range(6, 10))
+def test_kept_pages_are_not_counted_as_free(pages):
+    """A full page whose beam is gone stays in use while a sequence holds it: too few pages are found before anything has
+    changed, and enough are enough."""
+    m = Store(pages, 4)
+    s, _ = m.prompt(6, torch.Generator().manual_seed(0))
+    b = qmm.KvBeams(m.k, [s], 2, 20)
+    table, context, tails = b.table, b.context, b.tails
+    for _ in range(2):
+        assert b.room(table) is None
+        context = context + 1
+    kept = [b.keep(table, slot) for slot in (0, 1)]          # with the page that is full now
+    other = m.k.add()
+    table = m.reorder(table, context, tails, torch.zeros((1, 2), dtype=i64))     # slot 1's page is in no row any more
+
+    def state():
+        return (list(m.k._free), list(m.k._users), {k: list(v) for k, v in m.k._held.items()}, [set(x) for x in b._own],
+                b.tails.tolist(), list(b._length), list(b._tokens))
+
+    # in use: the prompt's two, two tails a slot; the spare ones are given back, the kept ones are not
+    enough = pages - 6 + 2 >= 4
+    was = state()
+    if enough:
+        table, tails = b.room(table)
+        assert len(set(tails.flatten().tolist())) == 4 and m.k.free_pages == pages - 8
+    else:
+        with pytest.raises(RuntimeError, match=f"4 needed, {pages - 4} of {pages} free"):
+            b.room(table)
+        assert state() == was
+        m.k.free(kept[1])
+        m.k.free(other)
+        if pages - 6 + 3 >= 4:
+            b.room(table)
+
+
 def test_beams_need_few_pages():
     """The pages in use never exceed the prompt's, those that the beams' histories can hold and two a slot."""
     m = Store(200, 4)
