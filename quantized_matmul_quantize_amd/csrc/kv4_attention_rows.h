@@ -34,6 +34,7 @@
 #include <utility>
 
 #include "kv4_attention.h"
+#include "kv4_deal.h"
 
 namespace qmm {
 namespace {
@@ -264,8 +265,8 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   const int strips = (rows + L::kStrip - 1) / L::kStrip, tiles = (strips + kW - 1) / kW;
   for (int tile = tile0; tile < tiles; tile += a.p_row_tiles) {
     // the strips are dealt evenly to the tiles
-    const int strip = tile * strips / tiles + wave;
-    const bool active = strip < (tile + 1) * strips / tiles;
+    const int strip = first_strip(tile, strips, tiles) + wave;
+    const bool active = strip < first_strip(tile + 1, strips, tiles);
     const int row = strip * L::kStrip + r;
     const bool live = active && row < rows;
     const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;

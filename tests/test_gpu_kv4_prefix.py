@@ -363,3 +363,31 @@ def test_rows_enough_for_a_wavefront_each(D, group):
     b = Groups(15, BF16, D, group, 16, 15, 5, [(100, [3] * 40), (64, [400, 1]), (600, [2] * 60), (48, [None, -5])] + [(16, [1])] * 70, before=[1, 300])
     assert b.q.shape[0] * 15 >= 8 * torch.cuda.get_device_properties(0).multi_processor_count
     b.check(b.run())
+
+
+def test_more_rows_of_a_prefix_than_products_of_their_tiles_hold():
+    """8.4 million rows of one kv head: against kv4_attention, whose results differ by roundings alone (twice the bound of
+    each)."""
+    D, hkv, hq, page, group, P, S = 64, 1, 128, 16, 32, 64, 65535
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda").to(BF16)
+    cache = qmm.kv4_cache(P // page + S, hkv, D, page, group).zero_()
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32, device="cuda")
+    table = torch.empty((S, P // page + 1), dtype=torch.int32, device="cuda")
+    table[:, :-1] = torch.arange(P // page)
+    table[:, -1] = torch.arange(P // page, P // page + S)
+    v = rand(P + S, hkv, D)
+    slots = torch.cat((torch.arange(P), (P // page + torch.arange(S)) * page)).cuda()
+    qmm.kv4_append(rand(P + S, hkv, D), v, slots, cache)
+    q = rand(S, hq, D)
+    context = i32([P + 1]).expand(S).contiguous()
+    got = qmm.kv4_prefix_attention(q, cache, table, context, i32([0, S]), i32([P]), max_group=S, max_prefix=P, max_tail=1)
+    want = qmm.kv4_attention(q, cache, table, context).float()
+    # of fp64 each is within 2^-11 of the mass a rounding (two each), 2^-21, 64 roundings of the join, 2 dx and an output
+    # rounding; dx = 16 u 31 S sk |scale| with S <= 64 |q| and sk a fifteenth of a key's range, at most 12
+    mass, most_q = float(v.float().abs().max()), float(q.float().abs().max())
+    dx = 16 * U * 31 * 64 * most_q * 12 / 15 * D ** -0.5
+    bound = (4 * 2.0 ** -11 + 128 * U + 4 * dx) * mass + 2.0 ** -21
+    for at in range(0, S, 8192):
+        part = want[at:at + 8192]
+        assert ((got[at:at + 8192].float() - part).abs() <= bound + 2 * OUT_HALF_ULP[BF16] * (part.abs() + bound)).all()
