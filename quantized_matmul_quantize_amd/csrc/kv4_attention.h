@@ -139,6 +139,14 @@ __device__ __forceinline__ bool past_one(f16x2_t v) {
   return v[0] > static_cast<_Float16>(1.0f) || v[1] > static_cast<_Float16>(1.0f);
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// What a base that moves from `from` to `to` for scores up to `top` (less `from`)
+// leaves of them but 7, where that is more than 1.  Past 2^24 the base's rounding
+// does, past 2^31 by more than an exponential has room for: scores are then taken
+// less this too.  (So large they are known no better than that.)
+__device__ __forceinline__ float unrounded(float top, float from, float to, bool moved) {
+  const float rest = top + (from - to) - 7.0f;
+  return rest > 1.0f || (rest < -1.0f && moved) ? rest : 0.0f;
+}
 // log sum exp from the base-2 maximum and the sum, and what results are divided
 // by.  A sum of 0 is that of no key; one that is not a number is its row's.
 __device__ __forceinline__ float lse_of(float base, float sum) {

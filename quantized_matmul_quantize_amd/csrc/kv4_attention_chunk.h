@@ -464,9 +464,9 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
       if (__any(grow)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float to = fmaxf(base[n], max_over_quads(top[n]) + from[n] - 7.0f);
+          const float both = max_over_quads(top[n]), to = fmaxf(base[n], both + from[n] - 7.0f);
           const float fade = to == -INFINITY ? 1.0f : exp2_fast(base[n] - to);
-          const float now_from = to == -INFINITY ? 0.0f : to;
+          const float now_from = to == -INFINITY ? 0.0f : to, rest = unrounded(both, from[n], now_from, to > base[n]);
           f16x2_t own[G];
 #pragma unroll
           for (int g = 0; g < G; ++g) own[g] = most_s[g];
@@ -502,7 +502,9 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
             for (int y = 0; y < MT; ++y) o[n][g][y] *= f;
           }
 #pragma unroll
-          for (int u = 0; u < 2 * U; ++u) x[n][u] += from[n] - now_from;
+          for (int u = 0; u < 2 * U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][u][e] = x[n][u][e] + (from[n] - now_from) - rest;
           from[n] = now_from;
           limit[n] = to == -INFINITY ? -INFINITY : 15.0f;
           base[n] = to;

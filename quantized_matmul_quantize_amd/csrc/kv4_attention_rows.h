@@ -413,9 +413,11 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
         const float both = fmaxf(top, __shfl_xor(top, 32, kWave));
         const float to = fmaxf(base, both + from - 7.0f);
         const float fade = to == -INFINITY ? 1.0f : exp2_fast(base - to);
-        const float now_from = to == -INFINITY ? 0.0f : to;
+        const float now_from = to == -INFINITY ? 0.0f : to, rest = unrounded(both, from, now_from, to > base);
 #pragma unroll
-        for (int t = 0; t < T; ++t) x[t] += from - now_from;
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[t][e] = x[t][e] + (from - now_from) - rest;
 #pragma unroll
         for (int c = 0; c < kCh; ++c) o[c] *= fade;
         l *= fade;

@@ -164,3 +164,15 @@ def test_a_query_that_is_not_finite_has_no_log_sum(dtype, hq, hkv, lens, queries
     out, lse = c.run(q=q)
     assert lse[bad].isnan().all() and out[bad].isnan().all()
     assert lse[~bad].isfinite().all() and out[~bad].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_scores_past_the_range_in_which_ones_differ(dtype, shape):
+    """Known no better than to 16 and more: results are finite and between the values."""
+    hq, hkv, lens, queries = SHAPES[shape]
+    c = Case(5, dtype, 128, 64, 16, hq, hkv, lens, queries)
+    for scale in (1e9, 1e20, -1e30):
+        out, lse = c.run(scale=scale)
+        assert (out[lse > -math.inf].abs() <= 1.01 * max(np.abs(v).max() for v in c.v if len(v))).all()
+        assert not lse.isnan().any() and not (lse == math.inf).any()

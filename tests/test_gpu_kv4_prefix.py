@@ -391,3 +391,27 @@ def test_more_rows_of_a_prefix_than_products_of_their_tiles_hold():
     for at in range(0, S, 8192):
         part = want[at:at + 8192]
         assert ((got[at:at + 8192].float() - part).abs() <= bound + 2 * OUT_HALF_ULP[BF16] * (part.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("scale", [1e9, 1e20, -1e30])
+@pytest.mark.parametrize("kind", ["few", "many", "long", "chunks"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (128, 128), (256, 32)])
+def test_scores_past_the_range_in_which_ones_differ(scale, kind, dtype, D, group):
+    """Where scores are known no better than to 16 and more the largest has the weight: results are finite, mean values of
+    the keys', and their log-sum-exp is a score."""
+    note(f"kv4_prefix_attention scale={scale} {kind} D={D} group={group} {dtype}")
+    queries = [1 + 40 * (i % 3) for i in range(12)] if kind == "chunks" else None
+    b = Groups(18, dtype, D, group, 32, 4, 1, [(320, [90 + i for i in range(10 if queries else 5 if kind == "few" else 40)]), (64, [70, 99])],
+               queries=queries)
+    out, lse = b.run(scale=scale, **(long_table(b) if kind == "long" else {}))
+    _, l, _, b_lse, _ = bounds.attention(b.q.float().numpy(), b.k, b.v, b.sk, b.sv, b.lens, b.queries, scale)
+    assert (np.abs(lse.cpu().numpy() - l) <= b_lse).all()
+    row = 0
+    for n, ctx, v in zip(b.queries, b.lens, b.v):
+        got = out[row:row + n].double().cpu().numpy()
+        most = np.abs(v[:, 0]).max()
+        # (a probability of 2^7 .. 2^15, its product with a scale and sums of codes with 64 added, as in kv4_bounds.py)
+        slack = (b.roundings * 2.0 ** -11 + 2 * OUT_HALF_ULP[dtype]) * most + (ctx / 16 + 96) * U * 158 * most + 2.0 ** -20
+        assert (got <= v[:, 0].max(0) + slack).all() and (got >= v[:, 0].min(0) - slack).all()
+        row += n
