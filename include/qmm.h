@@ -726,9 +726,11 @@ int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_h
  * (bf16 queries: rounded, 2^-11 or a step of 2^-20 below 2^-10; fp16 ones: exact
  * to that step) and probabilities rounded to it, instead of the products of
  * probabilities and scales, and with bf16 queries brought into binary16's range
- * by one power of two for up to 256 rows.  Which kernels run is chosen by the
- * hints; results differ by these roundings and do not depend on timing.  Up to
- * 65535 groups, and the blocks of a launch below 2^24.
+ * by one power of two for up to 256 rows whose largest are within 2^12 of each
+ * other (shorter ones: by each row's own).  What the queries of one sequence are
+ * costs no other one its bits.  Which kernels run is chosen by the hints; results
+ * differ by these roundings and do not depend on timing.  Up to 65535 groups, and
+ * the blocks of a launch below 2^24.
  * ------------------------------------------------------------------------- */
 size_t kv4_prefix_attention_workspace_bytes(int64_t T, int64_t seqs, int64_t max_q, int64_t n_groups,
                                             int64_t max_group, int64_t max_prefix, int64_t max_tail, int64_t q_heads,

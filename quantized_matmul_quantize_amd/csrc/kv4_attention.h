@@ -363,13 +363,25 @@ __device__ __forceinline__ void attention_block(const A& a, uint32_t id, uint8_t
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) qv[n][j] = live ? ld16(qp + 32 * j) : u32x4{0u, 0u, 0u, 0u};
     }
-    float key_scale = a.scale_log2;
-    if constexpr (DT == QMM_BF16) {
+    // (the power of two of bf16 queries is that of all rows, which are a sequence's;
+    // in a prefix each row's own: no sequence's queries cost another's bits)
+    constexpr bool kApart = PART == kPrefix;
+    float key_scale[kApart ? NT : 1];
+#pragma unroll
+    for (int n = 0; n < (kApart ? NT : 1); ++n) key_scale[n] = a.scale_log2;
+    if constexpr (DT == QMM_BF16 && kApart) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const QueryScale qs = query_scale(max_over_quads(largest_bf16(qv[n], 0.0f)));
+        key_scale[n] *= qs.up;
+        to_f16(qv[n], qs.down);
+      }
+    } else if constexpr (DT == QMM_BF16) {
       float most = 0.0f;
 #pragma unroll
       for (int n = 0; n < NT; ++n) most = largest_bf16(qv[n], most);
       const QueryScale qs = query_scale(wave_max(most));
-      key_scale *= qs.up;
+      key_scale[0] *= qs.up;
 #pragma unroll
       for (int n = 0; n < NT; ++n) to_f16(qv[n], qs.down);
     }
@@ -475,9 +487,10 @@ __device__ __forceinline__ void attention_block(const A& a, uint32_t id, uint8_t
           const u32x4 par = *reinterpret_cast<const u32x4*>(params + u * L::kKTile + g * 64);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float sc = kv4_scale(par[i]) * key_scale, z = kv4_zero(par[i]);
+            const float ks = kv4_scale(par[i]), z = kv4_zero(par[i]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+              const float sc = ks * key_scale[kApart ? n : 0];
               const float v = fmaf(-z, qsum[n][g], prod[n][g][u][i]);
               x[n][u][i] = g == 0 ? sc * v : fmaf(sc, v, x[n][u][i]);
             }

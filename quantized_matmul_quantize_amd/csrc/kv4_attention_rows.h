@@ -263,12 +263,20 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
   };
 
   const int strips = (rows + L::kStrip - 1) / L::kStrip, tiles = (strips + kW - 1) / kW;
-  for (int tile = tile0; tile < tiles; tile += a.p_row_tiles) {
+  // bf16 queries have one power of two a block, in which binary16 holds what lies
+  // 2^31 below the largest.  The rows may be of several sequences, none of which
+  // may cost another its bits: a tile takes its rows with a largest query below
+  // `below` and down to 2^-12 of the largest of those (what is lost, 2^-27 of a row's
+  // largest a channel, is less than its products' roundings), then those that are
+  // left: none, but where a slot's queries are of another order, such as what an
+  // unused one holds.
+  float below = INFINITY;
+  for (int tile = tile0; tile < tiles;) {
     // the strips are dealt evenly to the tiles
     const int strip = first_strip(tile, strips, tiles) + wave;
     const bool active = strip < first_strip(tile + 1, strips, tiles);
     const int row = strip * L::kStrip + r;
-    const bool live = active && row < rows;
+    bool live = active && row < rows;
     const int tok = live ? row / a.ratio : 0, qh = live ? kvh * a.ratio + row - tok * a.ratio : 0;
     const uint16_t* qp = a.q + (sq.row0 + tok) * a.q_ts + qh * a.q_hs + 8 * h;
     __syncthreads();                               // LDS is free: the rows before are done
@@ -283,17 +291,34 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
 #pragma unroll
     for (int i = 0; i < L::kRing; ++i) fetch(i, ring + i * L::kSlot, page_at(i));
     fetch_pages(1);
-    float unscale = 1.0f;
+    float unscale = 1.0f, left = 0.0f;             // left: rows below that are
     if constexpr (DT == QMM_BF16) {
       float* stat = reinterpret_cast<float*>(lds);
-      float most = wave_max(largest_bf16(qv, 0.0f));
-      if (lane == 0) stat[wave] = most;
+      float own = largest_bf16(qv, 0.0f);
+      own = fmaxf(own, __shfl_xor(own, 32, kWave));
+      float most = wave_max(own < below ? own : 0.0f), least = -wave_max(own > 0.0f ? -own : -INFINITY);
+      if (lane == 0) {
+        stat[wave] = most;
+        stat[kW + wave] = least;
+      }
       meet();
       most = stat[0];
+      least = stat[kW];
 #pragma unroll
-      for (int w = 1; w < kW; ++w) most = fmaxf(most, stat[w]);
-      const QueryScale qs = query_scale(most);
+      for (int w = 1; w < kW; ++w) {
+        most = fmaxf(most, stat[w]);
+        least = fminf(least, stat[kW + w]);
+      }
       meet();
+      const float floor = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(most * 0x1p-12f)));
+      left = __any(least < floor) ? floor : 0.0f;
+      // (rows without a finite query but 0 are of the first)
+      if (own == 0.0f ? below < INFINITY : own < floor || own >= below) {
+        live = false;
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) qv[j] = u32x4{0u, 0u, 0u, 0u};
+      }
+      const QueryScale qs = query_scale(most);
       unscale = qs.up;
       to_f16(qv, qs.down);
     }
@@ -500,6 +525,8 @@ __device__ __forceinline__ void attention_rows_block(const SharedArgs& a, uint32
               f32x4{o[c][4 * i], o[c][4 * i + 1], o[c][4 * i + 2], o[c][4 * i + 3]} * 16.0f;
       if (h == 0) a.part_ml[at] = make_float2(base, l);
     }
+    below = left > 0.0f ? left : INFINITY;
+    tile += left > 0.0f ? 0 : a.p_row_tiles;
   }
 }
 

@@ -415,3 +415,37 @@ def test_scores_past_the_range_in_which_ones_differ(scale, kind, dtype, D, group
         slack = (b.roundings * 2.0 ** -11 + 2 * OUT_HALF_ULP[dtype]) * most + (ctx / 16 + 96) * U * 158 * most + 2.0 ** -20
         assert (got <= v[:, 0].max(0) + slack).all() and (got >= v[:, 0].min(0) - slack).all()
         row += n
+
+
+@pytest.mark.parametrize("kind", ["few", "many", "long"])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (256, 32)])
+def test_queries_of_very_different_sizes_keep_to_their_rows(kind, dtype, D, group):
+    """Unused slots, sequences shorter than the prefix and sequences that share it, whose queries are far larger or smaller
+    than the others': whatever they are, the others have their bounds."""
+    note(f"kv4_prefix_attention, queries of other sizes, {kind} D={D} group={group} {dtype}")
+    own = [3, 9, None, 20, -40, 1, 6] * (6 if kind != "few" else 1)
+    b = Groups(16, dtype, D, group, 32, 4, 1, [(160, own), (64, [9, None, 2])])
+    q, rows, T = b.q.clone(), np.ones(b.q.shape[:2], bool), b.q.shape[0]
+    far = {BF16: (1e12, 1e30, 1e-30, 1e-12, 3e4, 1e-4), F16: (3e4, 1e-4)}[dtype]
+    for i, t in enumerate(range(2, T - 3, 3)):               # every third sequence; the unused and the short ones
+        q[t] = (q[t].float() * far[i % len(far)]).clamp(-6e4 if dtype == F16 else -1e38, 6e4 if dtype == F16 else 1e38).to(dtype)
+        rows[t] = far[i % len(far)] < 1
+    for t, n in enumerate(own):
+        if n is None or n < 0:
+            q[t], rows[t] = (q[t].float().sign() * (6e4 if dtype == F16 else 1e35)).to(dtype), False
+    q[T - 2], rows[T - 2] = q[T - 2].sign() * 5e4, False
+    b.check(b.run(q=q, **(long_table(b) if kind == "long" else {})), q=q, rows=rows)
+
+
+def test_rows_without_a_finite_query_but_zero_among_others_of_other_sizes():
+    b = Groups(17, BF16, 128, 64, 32, 4, 1, [(256, [5] * 70)])
+    q, rows = b.q.clone(), np.ones(b.q.shape[:2], bool)
+    q[3] = 0
+    q[4], q[5, 1] = math.nan, math.inf
+    q[6] = (q[6].float() * 1e20).to(BF16)
+    q[7:] = (q[7:].float() * 1e-20).to(BF16)
+    rows[4], rows[5, 1], rows[6] = False, False, False
+    out, lse = b.run(q=q, **long_table(b))
+    b.check((out, lse), q=torch.where(q.isfinite(), q, 0), rows=rows)
+    assert out[4].isnan().all() and lse[4].isnan().all() and out[6].isfinite().all()
