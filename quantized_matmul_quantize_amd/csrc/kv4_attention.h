@@ -275,7 +275,9 @@ __device__ __forceinline__ void attention_block(const A& a, uint32_t id, uint8_t
                     sq.first + (min((tile + 1) * L::kRows, rows) - 1) / a.ratio);
       ch = {a.chunk, max(1, (st.count + a.chunk - 1) / a.chunk)};
     } else {
-      st = {0, item.lo, steps_in(sq.ctx - item.lo)};
+      // (chunks by all of the part's keys, as they are joined; a sequence's own up to what the tile's last row sees)
+      const int end = PART == kPrefix ? sq.ctx : min(sq.ctx, sq.first + (min((tile + 1) * L::kRows, rows) - 1) / a.ratio + 1);
+      st = {0, item.lo, steps_in(end - item.lo)};
       ch = part_chunks<PART>(a, item);
     }
     const int chunk = ch.chunk, chunks = ch.chunks;

@@ -110,7 +110,8 @@ __device__ __forceinline__ void attention_chunk_block(const A& a, uint32_t id, u
       st = steps_of(a, blk_lo, blk_hi);
       ch = {a.chunk, max(1, (st.count + a.chunk - 1) / a.chunk)};
     } else {
-      st = {0, item.lo, steps_in(sq.ctx - item.lo)};
+      // (chunks by all of the sequence's own keys, as they are joined; the tile's end before)
+      st = {0, item.lo, steps_in(min(sq.ctx, blk_hi + 1) - item.lo)};
       ch = part_chunks<PART>(a, item);
     }
     const int chunk = ch.chunk, chunks = ch.chunks;

@@ -449,3 +449,30 @@ def test_rows_without_a_finite_query_but_zero_among_others_of_other_sizes():
     out, lse = b.run(q=q, **long_table(b))
     b.check((out, lse), q=torch.where(q.isfinite(), q, 0), rows=rows)
     assert out[4].isnan().all() and lse[4].isnan().all() and out[6].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+@pytest.mark.parametrize("queries,back", [([21, 12, 24, 9, 5, 17], 1), ([21, 12, 24, 9, 5, 17], 7), ([130, 60, 300, 1, 200, 150], 1),
+                                          ([130, 60, 300, 1, 200, 150], 90)], ids=["few", "few, before", "chunks", "chunks, before"])
+def test_what_later_tokens_hold_changes_nothing(queries, back, dtype, D, group):
+    """The values of a token near the end of each sequence have scales of NaN, infinity or the largest there is: whether it
+    is in the last round of keys of a row that stands before it or rounds behind.  (Scales that are not finite, which no
+    append writes: where many rows share the operands of a block, that has to hold for the rows of other blocks, of up to
+    128 rows each, as in kv4_attention: 0 times the block's scale is not 0.)"""
+    note(f"kv4_prefix_attention, later tokens, D={D} group={group} {queries[0]} {back} {dtype}")
+    page = 32
+    b = Groups(19, dtype, D, group, page, 4, 1, [(100, [300, 77]), (64, [301, 20]), (0, [200])], queries=queries, after=[170])
+    G, finite, others = D // group, np.ones(b.q.shape[:2], bool), np.ones(b.q.shape[:2], bool)
+    for at, n in zip(b.starts, queries):
+        first = max(0, n - back)                             # that sees the token
+        finite[at + first:at + n] = False
+        others[at + (first * 4 // 128 * 32 if max(queries) > 24 else first):at + n] = False
+    for word in (-1, 0x7C00, 0xFC00, 0x000F7BFF):
+        rec = b.cache.cpu().view(torch.int32).view(b.cache.shape[0], 1, -1)
+        for s, (n, ctx) in enumerate(zip(queries, b.lens)):
+            if n >= back:
+                place, params = (ctx - back) % page, page * D // 4 + G * page
+                rec[int(b.table[s, (ctx - back) // page]), :, params + place:params + G * page:page] = word
+        b.cache.copy_(rec.view(torch.uint8).view(b.cache.shape))
+        b.check(b.run(), rows=finite if word == 0x000F7BFF else others)
