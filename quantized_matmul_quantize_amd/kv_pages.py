@@ -174,24 +174,49 @@ class KvPages:
 
     def shared(self, seqs: Sequence[int]) -> Tuple[torch.Tensor, torch.Tensor]:
         """(groups int32 [n + 1], prefix int32 [n]) of ``kv4_prefix_attention``: of the sequences in their order, runs
-        that begin in the same page, and the tokens in the pages that all of a run have in common."""
+        with pages in common, and the tokens in the pages that all of a run have in common; cut so that the most tokens
+        need not be read again (two prompts that begin with the same page of text, with samples of each, are two runs)."""
         seqs = list(seqs)
         self._check(seqs, distinct=False)
-        starts, prefix = [], []
-        for i, seq in enumerate(seqs):
-            held, last = self._held[seq], self._held[seqs[i - 1]] if i else []
-            if held and last and held[0] == last[0] >= 0:
-                same = 0
-                while same < min(len(held), prefix[-1] // self.page) and held[same] == last[same]:
-                    same += 1
-                prefix[-1] = min(prefix[-1], same * self.page)
-            else:
-                starts.append(i)
-                prefix.append(len(held) * self.page)
-        for i, start in enumerate(starts):
-            run = seqs[start:(starts + [len(seqs)])[i + 1]]
-            prefix[i] = min([prefix[i]] + [self._length[s] for s in run])
-        return torch.tensor(starts + [len(seqs)], dtype=torch.int32), torch.tensor(prefix, dtype=torch.int32)
+        count = len(seqs)
+        common = [0] * count                                       # tokens that a sequence shares with the one before
+        for i in range(1, count):
+            a, b = seqs[i - 1], seqs[i]
+            mine, theirs = self._held[b], self._held[a]
+            if mine and theirs and mine[0] == theirs[0] >= 0:
+                same = next((k for k, (x, y) in enumerate(zip(mine, theirs)) if x != y), min(len(mine), len(theirs)))
+                common[i] = min(same * self.page, self._length[a], self._length[b])
+        # Of the first j sequences: the most that is saved, and where the last run starts.  That is, of all starts i,
+        # saved[i] + (j - 1 - i) n with n the least in common from i on.  Starts are kept by n, which rises; of those with
+        # the same only the ones that no later start beats (as n falls, the later ones gain).
+        saved, begin = [0] * (count + 1), [0] * (count + 1)
+        starts: List[Tuple[int, List[int]]] = []
+        for j in range(1, count + 1):
+            saved[j], begin[j] = saved[j - 1], j - 1               # a run of one
+            n = common[j - 1]
+            if n == 0:
+                starts = []
+                continue
+            merged = [j - 2]
+            while starts and starts[-1][0] >= n:
+                merged = starts.pop()[1] + merged
+            kept: List[int] = []
+            for i in reversed(merged):
+                if not kept or saved[i] - i * n >= saved[kept[-1]] - kept[-1] * n:
+                    kept.append(i)
+            starts.append((n, kept[::-1]))
+            for least, (i, *_) in reversed(starts):
+                now = saved[i] + (j - 1 - i) * least
+                if now >= saved[j]:
+                    saved[j], begin[j] = now, i
+        groups, j = [], count
+        while j:
+            i = begin[j]
+            groups.append((i, self._length[seqs[i]] if j - i == 1 else min(common[i + 1:j])))
+            j = i
+        groups.reverse()
+        return (torch.tensor([i for i, _ in groups] + [count], dtype=torch.int32),
+                torch.tensor([n for _, n in groups], dtype=torch.int32))
 
     def _check(self, seqs, distinct: bool = True) -> None:
         for seq in seqs:

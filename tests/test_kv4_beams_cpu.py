@@ -494,3 +494,50 @@ def test_runs_of_sequences_that_share_pages():
     assert k.shared([a, a])[1].tolist() == [13]
     assert [t.tolist() for t in k.shared([])] == [[0], []]
     raises(lambda: k.shared([99]), "no sequence")
+
+
+def test_runs_are_cut_where_parts_of_them_share_more():
+    """Two prompts that fork from a page of the same text, with samples of each; and others, against all ways to cut."""
+    k = qmm.KvPages(600, 4)
+    text = k.add()
+    k.extend([text], [4])
+    samples = []
+    for n in (80, 121):
+        prompt = k.fork(text)
+        k.extend([prompt], [n])
+        samples += [k.fork(prompt) for _ in range(5)]
+    groups, prefix = k.shared(samples)
+    assert groups.tolist() == [0, 5, 10] and prefix.tolist() == [84, 125]
+    assert [x.tolist() for x in k.shared([text] + samples)] == [[0, 1, 6, 11], [4, 84, 125]]
+    k.extend(samples, range(1, 11))
+    assert [x.tolist() for x in k.shared(samples)] == [[0, 5, 10], [84, 124]]
+    assert [x.tolist() for x in k.shared(samples[4:6])] == [[0, 2], [4]]
+
+    g = torch.Generator().manual_seed(0)
+    draw = lambda n: int(torch.randint(0, n, (), generator=g))
+    for _ in range(60):
+        k, seqs = qmm.KvPages(900, 4), []
+        for _ in range(9):                                   # a random family: roots, forks of any, shortened or extended
+            s = k.fork(seqs[draw(len(seqs))]) if seqs and draw(4) else k.add()
+            if k.length(s) and draw(2):
+                k.shrink(s, draw(k.length(s) + 1))
+            k.extend([s], [draw(30)])
+            seqs.append(s)
+        seqs = [seqs[draw(9)] for _ in range(8)]
+        held = [k._held[s] for s in seqs]
+
+        def common(i, j):
+            pages = 0
+            while all(pages < len(h) and h[pages] == held[i][pages] for h in held[i:j]):
+                pages += 1
+            return min([pages * 4] + [k.length(s) for s in seqs[i:j]])
+
+        groups, prefix = (x.tolist() for x in k.shared(seqs))
+        assert groups[0] == 0 and groups[-1] == 8 and all(a < b for a, b in zip(groups, groups[1:]))
+        assert prefix == [common(a, b) for a, b in zip(groups, groups[1:])]
+        got = sum((b - a - 1) * n for a, b, n in zip(groups, groups[1:], prefix))
+        every = []
+        for cuts in range(128):
+            at = [0] + [c for c in range(1, 8) if cuts >> (c - 1) & 1] + [8]
+            every.append(sum((b - a - 1) * common(a, b) for a, b in zip(at, at[1:])))
+        assert got == max(every)
