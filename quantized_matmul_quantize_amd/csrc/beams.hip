@@ -34,21 +34,13 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
-__device__ __forceinline__ uint64_t ordered(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
-  return u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 0x8000000000000000ull);
-}
-__device__ __forceinline__ double unordered(uint64_t k) {
-  return __builtin_bit_cast(double, k >> 63 ? k ^ 0x8000000000000000ull : ~k);
-}
 
 // The k-th and the few-th largest key of the wavefront's lanes (0: not so many
 // are not 0), few <= k.  Two searches at once: each waits for its own counts.
-template <typename K>
-__device__ __forceinline__ void kth_largest(K key, int bits, int k, int few, K* at_k, K* at_few) {
-  K a = 0, b = 0;
+__device__ __forceinline__ void kth_largest(uint32_t key, int bits, int k, int few, uint32_t* at_k, uint32_t* at_few) {
+  uint32_t a = 0, b = 0;
   for (int bit = bits - 1; bit >= 0; --bit) {
-    const K next_a = a | K{1} << bit, next_b = b | K{1} << bit;
+    const uint32_t next_a = a | 1u << bit, next_b = b | 1u << bit;
     if (__popcll(__ballot(key >= next_a)) >= k) a = next_a;
     if (__popcll(__ballot(key >= next_b)) >= few) b = next_b;
   }
@@ -56,58 +48,29 @@ __device__ __forceinline__ void kth_largest(K key, int bits, int k, int few, K* 
   *at_few = b;
 }
 
-// A bound below which no value is among the k best: the k-th best of the lanes'
-// best values, of equal ones those with the lowest indexes first.  Of a
-// wavefront at most k lanes hold values that it lets through.
-template <typename K>
-struct Bound {
-  K key;             // 0: no bound
-  uint32_t index;    // of values with that key, up to this index
+// A key below which no value is among the k best (0: no bound): the k-th best of
+// the lanes' best ones.  But for equal keys at most k lanes of a wavefront hold
+// values that it lets through.  A wavefront's by its k best lanes and by its share
+// of k best of the block's; what the block then goes by: the tightest of the first
+// or the loosest of the second, which lets through k lanes of all together and is
+// the tighter one but for few or sorted values.
+struct Bounds {
+  uint32_t k, share;
 };
-template <typename K>
-__device__ __forceinline__ bool tighter(const Bound<K>& a, const Bound<K>& b) {
-  return a.key > b.key || (a.key == b.key && a.index < b.index);
-}
-// The index that belongs to the k-th largest key; `first()` gives the lowest at
-// which the lane holds its best value.  Not `exact`: any, so that all equal
-// values pass, however many.
-template <typename K, typename First>
-__device__ __forceinline__ Bound<K> bound_at(K best, K key, int k, bool exact, First first) {
-  Bound<K> b{key, 0xFFFFFFFFu};
-  if (key == 0 || !exact) return b;
-  const int more = k - __popcll(__ballot(best > key));
-  if (__popcll(__ballot(best == key)) > more) {
-    uint32_t at, unused;
-    kth_largest<uint32_t>(best == key ? ~first() : 0u, 32, more, more, &at, &unused);
-    b.index = ~at;
-  }
+__device__ __forceinline__ Bounds bounds_of(uint32_t best, int bits, int k, int waves) {
+  Bounds b;
+  kth_largest(best, bits, k, (k + waves - 1) / waves, &b.k, &b.share);
   return b;
 }
-// A wavefront's bounds by its k best lanes and by its share of k best of the
-// block's; what the block then goes by: the tightest of the first, which lets
-// through no more than k lanes a wavefront, or the loosest of the second, which
-// lets through k lanes of all together and is the tighter one but for few or
-// sorted values.
-template <typename K>
-struct Bounds {
-  Bound<K> k, share;
-};
-template <typename K, typename First>
-__device__ __forceinline__ Bounds<K> bounds_of(K best, int bits, int k, int waves, bool exact, First first) {
-  const int share = (k + waves - 1) / waves;
-  K at_k, at_share;
-  kth_largest(best, bits, k, share, &at_k, &at_share);
-  return {bound_at(best, at_k, k, exact, first), bound_at(best, at_share, share, exact, first)};
-}
-template <typename K, int WAVES>
-__device__ __forceinline__ Bound<K> block_bound(const Bounds<K> (&all)[WAVES]) {
-  Bound<K> most = all[0].k, least = all[0].share;
+template <int WAVES>
+__device__ __forceinline__ uint32_t block_bound(const Bounds (&all)[WAVES]) {
+  uint32_t most = all[0].k, least = all[0].share;
 #pragma unroll
   for (int w = 1; w < WAVES; ++w) {
-    if (tighter(all[w].k, most)) most = all[w].k;
-    if (tighter(least, all[w].share)) least = all[w].share;
+    most = max(most, all[w].k);
+    least = min(least, all[w].share);
   }
-  return tighter(least, most) ? least : most;
+  return max(most, least);
 }
 // Candidates that a wavefront has room for.
 __host__ __device__ constexpr int room_of(int k) { return 2 * k + 32; }
@@ -245,7 +208,7 @@ __global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
   extern __shared__ __attribute__((aligned(16))) float pool_x[];       // [4][room_of(k)], then as many tokens
   __shared__ float s_most[4], s_sum[4];
   __shared__ double s_large[4];
-  __shared__ Bounds<uint32_t> s_bound[4];
+  __shared__ Bounds s_bound[4];
   __shared__ uint64_t s_best[4];
   __shared__ int s_rank[4][kWave];
   __shared__ int s_count[4], s_again[4];
@@ -283,19 +246,18 @@ __global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
 
   // ---- the lane's best, the block's maximum, the bound
   const float best = fmaxf(L::largest(raw), odd);
-  const Bounds<uint32_t> mine =
-      bounds_of(best > -INFINITY ? L::key(best) : 0u, L::kBits, a.k, 4, false, [] { return 0u; });
+  const Bounds mine = bounds_of(best > -INFINITY ? L::key(best) : 0u, L::kBits, a.k, 4);
   float most = wave_max(best);
   if (lane == 0) {
     s_most[wave] = most;
     s_bound[wave] = mine;
   }
   __syncthreads();
-  const Bound<uint32_t> bound = block_bound(s_bound);
+  const uint32_t bound = block_bound(s_bound);
   most = fmaxf(fmaxf(s_most[0], s_most[1]), fmaxf(s_most[2], s_most[3]));
   // ---- sums below the bound; what passes it (without one all but -inf does)
   // goes to the wavefront's part of LDS
-  const float least = bound.key ? L::value(bound.key) : -3.402823466e38f;
+  const float least = bound ? L::value(bound) : -3.402823466e38f;
   const float at_base = most == -INFINITY ? 0.0f : most * kLog2e;
   float sum = 0.0f;
   int mine_n = 0;
@@ -453,16 +415,19 @@ __global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
 }
 
 // A block joins the rows of a sequence: each beam's log sum, then the k best of
-// the blocks' candidates, 2048 at a time, by the same bound.  Values are fp64.
-// One block to a sequence: 64 x 8 rows 14.6 us, a chain of loads, searches and
-// barriers; their fp32 keys bound first (32 steps of a search, not 64) 18 -> 14.6.
+// the blocks' candidates, 2048 at a time, by the same bound.  Values are fp64, the
+// bound is by fp32 keys: all that round to the bound's pass.  There is room for
+// every candidate that is looked at; they come to it in any order, and each counts
+// those before it by value and index.
+//   One block to a sequence: 64 x 8 rows 14.5 us, a chain of loads, searches and
+// barriers.
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinPer = 4;
-constexpr int kJoinRoom = kJoinWaves * kMostK * kJoinPer + kMostK;     // (as room_of, and the ones kept)
+constexpr int kJoinRoom = kJoinThreads * kJoinPer + kMostK;            // and the ones kept
 
 __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
   __shared__ double s_offset[kMostBeams];
   __shared__ int s_alive[kMostBeams];
-  __shared__ Bounds<uint64_t> s_bound[kJoinWaves];
+  __shared__ Bounds s_bound[kJoinWaves];
   __shared__ int s_count;
   __shared__ double value[kJoinRoom], kept_value[kMostK];
   __shared__ uint32_t place[kJoinRoom], kept_place[kMostK];
@@ -532,41 +497,24 @@ __global__ __launch_bounds__(kJoinThreads) void beam_join_kernel(Select a) {
       }
       best = fmax(best, v[i]);
     }
-    // The bound by fp32 keys first (all that round to the bound's pass); where
-    // that lets through more than there is room for, by fp64 ones and indexes.
-    for (int turn = 0;; ++turn) {
-      const bool some = best > -__builtin_inf();
-      const uint64_t key = !some ? 0 : turn ? ordered(best) : ordered(static_cast<float>(best));
-      const Bounds<uint64_t> mine = bounds_of(key, turn ? 64 : 32, a.k, kJoinWaves, turn > 0, [&] {
-        uint32_t low = 0xFFFFFFFFu;
-#pragma unroll
-        for (int i = 0; i < kJoinPer; ++i)
-          if (v[i] == best) low = min(low, at[i]);
-        return low;
-      });
-      if (lane == 0) s_bound[wave] = mine;
-      for (int i = tid; i < kept; i += kJoinThreads) {         // the best of those before
-        value[i] = kept_value[i];
-        place[i] = kept_place[i];
-      }
-      if (tid == 0) s_count = kept;
-      __syncthreads();
-      const Bound<uint64_t> bound = block_bound(s_bound);
-#pragma unroll
-      for (int i = 0; i < kJoinPer; ++i) {
-        const uint64_t own = turn ? ordered(v[i]) : ordered(static_cast<float>(v[i]));
-        if (v[i] > -__builtin_inf() && (own > bound.key || (own == bound.key && at[i] <= bound.index))) {
-          const int n = atomicAdd(&s_count, 1);
-          if (n < kJoinRoom) {
-            value[n] = v[i];
-            place[n] = at[i];
-          }
-        }
-      }
-      __syncthreads();
-      if (s_count <= kJoinRoom) break;
-      __syncthreads();                 // the count may be written again
+    const Bounds mine = bounds_of(best > -__builtin_inf() ? ordered(static_cast<float>(best)) : 0u, 32, a.k, kJoinWaves);
+    if (lane == 0) s_bound[wave] = mine;
+    for (int i = tid; i < kept; i += kJoinThreads) {           // the best of those before
+      value[i] = kept_value[i];
+      place[i] = kept_place[i];
     }
+    if (tid == 0) s_count = kept;
+    __syncthreads();
+    const uint32_t bound = block_bound(s_bound);
+#pragma unroll
+    for (int i = 0; i < kJoinPer; ++i) {
+      if (v[i] > -__builtin_inf() && ordered(static_cast<float>(v[i])) >= bound) {
+        const int n = atomicAdd(&s_count, 1);
+        value[n] = v[i];
+        place[n] = at[i];
+      }
+    }
+    __syncthreads();
     const int n = s_count;
     kept = min(n, a.k);
     for (int i = tid; i < n; i += kJoinThreads) {

@@ -203,3 +203,17 @@ def test_no_sequences_workspace_another_stream_and_a_replayed_graph():
         want = qmm.beam_select(x, scores, 6)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["fp32", "bf16"])
+def test_more_equal_candidates_than_are_joined_at_once(dtype):
+    """Of 64 beams of equal logits, and with one that is better by less than an fp32 value tells: 64 each of 3 to 5 blocks
+    a beam, all of the same fp32 key."""
+    x = torch.zeros((64, 40001), dtype=dtype, device="cuda")
+    scores = torch.full((1, 64), -3.0, device="cuda")
+    best, tokens, parents = qmm.beam_select(x, scores, 64)
+    assert tokens[0].tolist() == list(range(64)) and (parents == 0).all() and (best == best[0, 0]).all()
+    x[37, 100] = 2.0 ** -20                                  # 2^-20 (1 - 1 / 40001) above, below a step of 13.6 in fp32
+    best, tokens, parents = qmm.beam_select(x, scores, 64)
+    assert (int(parents[0, 0]), int(tokens[0, 0])) == (37, 100)
+    assert tokens[0, 1:].tolist() == list(range(63)) and (parents[0, 1:] == 0).all()
