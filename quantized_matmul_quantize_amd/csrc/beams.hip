@@ -75,13 +75,6 @@ __device__ __forceinline__ uint32_t block_bound(const Bounds (&all)[WAVES]) {
 // Candidates that a wavefront has room for.
 __host__ __device__ constexpr int room_of(int k) { return 2 * k + 32; }
 
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
 __device__ __forceinline__ double wave_sum(double v) {
   v += dpp_d<kDppXor1>(v);
   v += dpp_d<kDppXor2>(v);
@@ -105,14 +98,6 @@ struct Select {
   int64_t* out_tokens;
   int64_t* out_parents;
 };
-
-// The compiler's maximum quiets each operand first.  (A NaN makes it wrong, and
-// is found in the sum.)
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
-  return d;
-}
 
 // The largest of 16-bit floating-point numbers by their bits: as whole numbers
 // with a sign the positive ones stand in their order, the negative ones in the
@@ -142,7 +127,7 @@ struct Logits<QMM_F32> {
   static __device__ __forceinline__ uint32_t key(float x) { return ordered(x); }
   template <int N>
   static __device__ __forceinline__ float largest(const u32x4 (&v)[N]) {
-    float most = -INFINITY;
+    float most = -INFINITY;                                  // (a NaN makes it wrong, and is found in the sum)
 #pragma unroll
     for (int j = 0; j < N; ++j) most = max3(max3(most, get(v[j], 0), get(v[j], 1)), get(v[j], 2), get(v[j], 3));
     return most;

@@ -115,12 +115,6 @@ __device__ __forceinline__ float sum_over_quads(float v) {
   v += __shfl_xor(v, 16, kWave);
   return v + __shfl_xor(v, 32, kWave);
 }
-// The compiler's maximum quiets each operand first; these are products already.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
-  return d;
-}
 __device__ __forceinline__ f16x2_t pk_max(f16x2_t a, f16x2_t b) { return __builtin_elementwise_max(a, b); }
 __device__ __forceinline__ f16x2_t pair16(float v) {
   return f16x2_t{static_cast<_Float16>(v), static_cast<_Float16>(v)};

@@ -42,14 +42,6 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int c, floa
   else load8<DT>(w, c, x);
 }
 
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-
 // 1 / sqrt(x) to a few units of the last place: the instruction's 24 bits and
 // two Newton steps.  Zeros and infinities (and NaN) keep the instruction's result.
 __device__ __forceinline__ double inverse_sqrt(double x) {
