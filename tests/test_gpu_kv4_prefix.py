@@ -476,3 +476,16 @@ def test_what_later_tokens_hold_changes_nothing(queries, back, dtype, D, group):
                 rec[int(b.table[s, (ctx - back) // page]), :, params + place:params + G * page:page] = word
         b.cache.copy_(rec.view(torch.uint8).view(b.cache.shape))
         b.check(b.run(), rows=finite if word == 0x000F7BFF else others)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("D,group", FORMATS)
+def test_many_rows_by_the_kernel_for_few_have_its_bounds(dtype, D, group):
+    """Prefixes of few steps run by it whatever their rows: no rounding of the values."""
+    note(f"kv4_prefix_attention, many rows by the kernel for few, D={D} group={group} {dtype}")
+    for plan, queries in (([(1000, [1 + 3 * i for i in range(37)]), (333, [20] * 2), (95, [1] * 26)], None),
+                          ([(200, [30, 40, 25, 5, None]), (97, [60, 1])], [20, 24, 3, 0, 0, 24, 1])):
+        b = Groups(20 + D - group, dtype, D, group, 32, 4, 1, plan, queries=queries)
+        assert b.many
+        b.many, b.roundings = False, 1
+        b.check(b.run())
