@@ -1,7 +1,7 @@
 """Beam search over a 4-bit key/value cache, end to end on one GPU.
 
 Prompts are read in chunks; then the beams of each of them decode together,
-with the prompt's keys and values read once for all of its beams. Every step
+with the prompt's keys and values taken for all of its beams. Every step
 of a layer, and every step of the search, is one library call:
 
     q, k, v   w4a16_gemv / w4a16_gemm

@@ -692,7 +692,8 @@ int beam_select(const void* logits, int dtype, int64_t row_stride, int64_t seqs,
  * cache [layers, pages, kv_heads, page, D + 8 D/g]; page_table, table_out int32
  * [seqs * beams, table_width]; context, context_out int32 [seqs * beams]; tails
  * int32 [seqs * beams, 2]; parents int64 [seqs, beams].  Tail pages are in no
- * other slot's row or tails.  The outputs are other memory than the inputs (so
+ * other slot's row or tails, nor in a row that is to stay as it is (a beam that is
+ * set aside while the search goes on).  The outputs are other memory than the inputs (so
  * a captured step has two tables, for every second turn).  A page outside
  * [0, pages) is not copied.
  * ------------------------------------------------------------------------- */
@@ -704,15 +705,16 @@ int kv4_beam_reorder(uint8_t* cache, int64_t layers, int64_t pages, int64_t kv_h
 /* ---------------------------------------------------------------------------
  * kv4_prefix_attention -- kv4_attention of a batch in groups of sequences whose
  * first tokens are the same (branches, samples or beams of one prompt, questions
- * on one document): those are read and attended to once for a group, with the
- * queries of all of its sequences, and joined with each sequence's own.  The
+ * on one document): those are attended to for a group, with the queries of all of
+ * its sequences, and joined with each sequence's own; they are read once a tile of
+ * rows (8, 16, 32 or up to 256 queries times the heads that share a kv head).  The
  * results are kv4_attention's (window 0) but for roundings.
  * groups  : int32 [n_groups + 1], device, rising: group g are the sequences
  *           groups[g] .. groups[g + 1] - 1 (those in none share nothing).
  * prefix  : int32 [n_groups], device: the first prefix[g] tokens of a group's
  *           sequences are the same, whether in the same pages or in copies of
- *           one.  Whole steps of 32 are read once, through the pages of one of
- *           the sequences that hold them; a sequence that is shorter (an unused
+ *           one.  Whole steps of 32 are read through the pages of one of the
+ *           sequences that hold them; a sequence that is shorter (an unused
  *           slot, context 0) is attended to by itself.
  * max_group, max_prefix, max_tail : the most sequences of a group, tokens of a
  *           prefix and tokens of a sequence behind it.  Hints (at least 1), like

@@ -954,7 +954,7 @@ def kv4_prefix_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
                          max_tail: Optional[int] = None, scale: Optional[float] = None, return_lse: bool = False,
                          out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """kv4_attention (without a window) where sequences groups[g] .. groups[g + 1] - 1 (int32 [n + 1]) have their first
-    prefix[g] (int32 [n]) tokens in common: these are attended to once for a group.  max_group, max_prefix and max_tail,
+    prefix[g] (int32 [n]) tokens in common: these are attended to for all of a group.  max_group, max_prefix and max_tail,
     hints as max_q: the most sequences of a group, tokens of a prefix and tokens of a sequence behind it."""
     T, q_heads, D = shape = _rows(q, "q", _HALVES)
     dtype = q.dtype

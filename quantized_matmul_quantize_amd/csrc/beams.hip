@@ -180,7 +180,7 @@ struct Logits<QMM_F16> {
 // candidates that are nearly as good are told apart by their rows' sums.
 //   Where values equal to the bound, or sorted ones, are more than LDS has room
 // for, or a NaN is met (the sum has taken it), the k largest are found one by one.
-//   64 x 8 rows of 131072 bf16 logits 43 us, 3.1 TB/s: bound by vector operations,
+//   64 x 8 rows of 131072 bf16 logits 42 us, 3.2 TB/s: bound by vector operations,
 // about ten a logit (unpacking, maximum, exponential at a quarter of the rate, sum,
 // comparison).  With 64 bytes of logits a thread the call took 67 us instead of
 // 60.6: its searches come twice as often.
@@ -404,7 +404,7 @@ __global__ __launch_bounds__(256, 5) void beam_rows_kernel(Select a) {
 // bound is by fp32 keys: all that round to the bound's pass.  There is room for
 // every candidate that is looked at; they come to it in any order, and each counts
 // those before it by value and index.
-//   One block to a sequence: 64 x 8 rows 14.5 us, a chain of loads, searches and
+//   One block to a sequence: 64 x 8 rows 12 us, a chain of loads, searches and
 // barriers.
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinPer = 4;
 constexpr int kJoinRoom = kJoinThreads * kJoinPer + kMostK;            // and the ones kept

@@ -28,7 +28,7 @@
 // in order made each wait one for all operands behind it), 254 -> 240 us.  Now a
 // round of 64 keys takes ~2 us, of which two wavefronts' matrix instructions on a
 // SIMD fill 0.85; the vector phase alone takes ~2100 cycles, ~330 operations that a
-// wavefront alone issues no faster.  LDS is in use 28% of the time.
+// wavefront alone issues no faster.  LDS is in use 33% of the time.
 #pragma once
 
 #include <utility>

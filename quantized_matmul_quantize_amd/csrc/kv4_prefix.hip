@@ -2,9 +2,10 @@
 // a prefix: argument checks and the launch plan (kernels: kv4_attention.h,
 // kv4_attention_chunk.h for own parts, kv4_attention_rows.h for prefixes).
 //
-// A prefix is a part of its own: attended to once for a group with all of its
-// rows, which turns loads and expansions of codes per sequence into matrix
-// products, and joined with each sequence's own part by log-sum-exp in fp32.
+// A prefix is a part of its own: attended to for a group with all of its rows, in
+// tiles of 8, 16, 32 or up to 256 that read it once each, which turns loads and
+// expansions of codes per sequence into matrix products, and joined with each
+// sequence's own part by log-sum-exp in fp32.
 // Two launches where both parts take the kernel for few rows, else three.  24
 // questions on each of two documents of 100000 tokens (64/8 heads of 128) 240
 // us, 4 beams after 1000 tokens (32/8) 13.5.

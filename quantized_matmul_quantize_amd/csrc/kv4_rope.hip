@@ -61,9 +61,9 @@ __device__ __forceinline__ double inverse_sqrt(double x) {
 // which side of a border the key falls, and in fp64 that no longer depends on
 // the order of the sums.  The partner's channels of a rotation by halves come as
 // the 16-bit inputs and are normed again: half the exchange of fp64 values.
-//   8191 tokens of 32/8 heads of 128 42 us, 213 MB at 5 TB/s: memory's rate.  64
-// tokens 4.6 us: launch, the loads of slots, positions and their rows of the
-// table one after another, and the norm's chain of sums.
+//   8191 tokens of 32/8 heads of 128 42 us, 181 MB at 4.3 TB/s (a copy reaches
+// 5.2).  64 tokens 4.6 us: launch, the loads of slots, positions and their rows of
+// the table one after another, and the norm's chain of sums.
 template <int DT, int D, int GROUP, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void kv4_rope_append_kernel(RopeAppend a) {
   constexpr int kLanes = D / 8, kTokens = kWave / kLanes;
